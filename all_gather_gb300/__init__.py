@@ -11,6 +11,11 @@ Everything runs in libtide.so (hand-written sm_103a kernels behind a C ABI,
 functions mirror the C entry points one to one, and :class:`Plan` is a thin
 convenience wrapper that takes torch tensors and passes their pointers.
 torch is used for device memory and streams only.
+
+The operators of the training step around the collectives (norm of queries
+and keys with the position rotation, vocabulary cross entropy, SwiGLU with
+8-bit checkpoints, each with its gradient) are in :mod:`all_gather_gb300.ops`
+and re-exported here.
 """
 from __future__ import annotations
 
@@ -27,7 +32,24 @@ from ._binding import (  # noqa: F401  (re-exported C-ABI names)
     tide_last_error, tide_launch_count, tide_plan_build, tide_plan_destroy, tide_plan_fold_config,
     tide_plan_num_segments, tide_plan_rebind, tide_plan_segment, tide_plan_slot_numel, tide_rs_fold,
     tide_rs_fold_noalloc, tide_status_string, tide_latin_square_gpu, tide_rs_wave_plan, tide_rs_wave_zero_mask,
-    tide_bruck_schedule, tide_sm_probe, tide_sm_probe_max_clusters, tide_corun_cta_budget, pointer_array)
+    tide_bruck_schedule, tide_sm_probe, tide_sm_probe_max_clusters, tide_corun_cta_budget, pointer_array,
+    tide_rope_table, tide_qk_norm_rope, tide_qk_norm_rope_grad, tide_qk_norm_rope_grad_workspace, tide_ce_loss,
+    tide_ce_loss_workspace, tide_ce_grad, tide_ce_grad_workspace, tide_swiglu_ckpt8, tide_swiglu_ckpt8_grad,
+    tide_ops_device_status)
+
+_OPS = ("rope_table", "qk_norm_rope", "qk_norm_rope_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
+        "Ckpt8", "new_ckpt8", "swiglu_ckpt8", "swiglu_ckpt8_grad")
+
+
+def __getattr__(name):
+    """The operators, imported on first use: they need torch at import time, the rest of the package does not."""
+    if name in _OPS:
+        from . import ops
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 AG_MODES = {"sm": TIDE_AG_SM, "ce2d": TIDE_AG_CE_2D, "ce1d": TIDE_AG_CE_1D}
 

@@ -37,7 +37,9 @@ EXPORTED = ("tide_plan_build", "tide_plan_rebind", "tide_rs_fold", "tide_ag_plac
             "tide_last_device_status", "tide_launch_count", "tide_status_string", "tide_last_error",
             "tide_rs_fold_noalloc", "tide_ag_place_f32", "tide_latin_square_gpu", "tide_rs_wave_plan",
             "tide_rs_wave_zero_mask", "tide_bruck_schedule", "tide_sm_probe", "tide_sm_probe_max_clusters",
-            "tide_corun_cta_budget")
+            "tide_corun_cta_budget", "tide_rope_table", "tide_qk_norm_rope", "tide_qk_norm_rope_grad",
+            "tide_qk_norm_rope_grad_workspace", "tide_ce_loss", "tide_ce_loss_workspace", "tide_ce_grad",
+            "tide_ce_grad_workspace", "tide_swiglu_ckpt8", "tide_swiglu_ckpt8_grad", "tide_ops_device_status")
 
 
 class WavePlan(ctypes.Structure):
@@ -67,6 +69,30 @@ class PlanFlags(ctypes.Structure):
 class Segment(ctypes.Structure):
     _fields_ = [("param", ctypes.c_int32), ("rank", ctypes.c_int32), ("src_elem", ctypes.c_int64),
                 ("dst_elem", ctypes.c_int64), ("n_valid", ctypes.c_int64), ("n_pad", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class QkDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("max_position", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("position_bytes", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class CeDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_int64), ("targets", ctypes.c_void_p), ("target_bytes", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64)]
+
+
+class Ckpt8Desc(ctypes.Structure):
+    _fields_ = [("gate_codes", ctypes.c_void_p), ("gate_exps", ctypes.c_void_p), ("up_codes", ctypes.c_void_p),
+                ("up_exps", ctypes.c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -128,6 +154,28 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tide_sm_probe_max_clusters.restype = i32
     lib.tide_corun_cta_budget.argtypes = [i32, i32, i32]
     lib.tide_corun_cta_budget.restype = i32
+    f32, f64, P = ctypes.c_float, ctypes.c_double, ctypes.POINTER
+    lib.tide_rope_table.argtypes = [i64, i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.tide_rope_table.restype = st
+    lib.tide_qk_norm_rope.argtypes = [P(QkDesc)] + [P(Heads)] * 4 + [vp]
+    lib.tide_qk_norm_rope.restype = st
+    lib.tide_qk_norm_rope_grad.argtypes = [P(QkDesc)] + [P(Heads)] * 6 + [vp, vp, vp, i64, vp]
+    lib.tide_qk_norm_rope_grad.restype = st
+    lib.tide_qk_norm_rope_grad_workspace.argtypes = [P(QkDesc)]
+    lib.tide_qk_norm_rope_grad_workspace.restype = i64
+    lib.tide_ce_loss.argtypes = [P(CeDesc), vp, vp, vp, i64, vp]
+    lib.tide_ce_loss.restype = st
+    lib.tide_ce_grad.argtypes = [P(CeDesc), vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    lib.tide_ce_grad.restype = st
+    for name in ("tide_ce_loss_workspace", "tide_ce_grad_workspace"):
+        getattr(lib, name).argtypes = [P(CeDesc)]
+        getattr(lib, name).restype = i64
+    lib.tide_swiglu_ckpt8.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, i64, P(Ckpt8Desc), vp]
+    lib.tide_swiglu_ckpt8.restype = st
+    lib.tide_swiglu_ckpt8_grad.argtypes = [i64, i64, i32, P(Ckpt8Desc), vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.tide_swiglu_ckpt8_grad.restype = st
+    lib.tide_ops_device_status.argtypes = [vp]
+    lib.tide_ops_device_status.restype = st
     _lib = lib
     return lib
 
@@ -308,3 +356,76 @@ def tide_sm_probe_max_clusters(cluster: int, smem_bytes: int) -> int:
 
 def tide_corun_cta_budget(cluster_slots: int, gemm_ctas: int, cluster: int) -> int:
     return int(load_library().tide_corun_cta_budget(cluster_slots, gemm_ctas, cluster))
+
+
+def tide_rope_table(max_position: int, rotary_dim: int, base: float, scaling: int, factor: float,
+                    low_freq_factor: float, high_freq_factor: float, original: float, table: int,
+                    stream: int = 0) -> None:
+    _check(load_library().tide_rope_table(max_position, rotary_dim, base, scaling, factor, low_freq_factor,
+                                          high_freq_factor, original, table or None, stream or None),
+           "tide_rope_table")
+
+
+def tide_qk_norm_rope(qk: QkDesc, q: Heads, k: Heads, q_out: Heads, k_out: Heads, stream: int = 0) -> None:
+    _check(load_library().tide_qk_norm_rope(qk, q, k, q_out, k_out, stream or None), "tide_qk_norm_rope")
+
+
+def tide_qk_norm_rope_grad_workspace(qk: QkDesc) -> int:
+    return _size(load_library().tide_qk_norm_rope_grad_workspace(qk), "tide_qk_norm_rope_grad_workspace")
+
+
+def tide_qk_norm_rope_grad(qk: QkDesc, dq_out: Heads, dk_out: Heads, q: Optional[Heads], k: Optional[Heads],
+                           dq: Heads, dk: Heads, dq_weight: int, dk_weight: int, workspace: int,
+                           workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().tide_qk_norm_rope_grad(qk, dq_out, dk_out, q, k, dq, dk, dq_weight or None,
+                                                 dk_weight or None, workspace or None, workspace_bytes,
+                                                 stream or None), "tide_qk_norm_rope_grad")
+
+
+def _size(n: int, where: str) -> int:
+    """A workspace size; -1 stands for refused arguments."""
+    if n < 0:
+        raise TideError(TIDE_ERR_INVALID_ARG, where, load_library().tide_last_error().decode())
+    return n
+
+
+def tide_ce_loss_workspace(ce: CeDesc) -> int:
+    return _size(load_library().tide_ce_loss_workspace(ce), "tide_ce_loss_workspace")
+
+
+def tide_ce_loss(ce: CeDesc, loss: int, lse: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().tide_ce_loss(ce, loss or None, lse or None, workspace or None, workspace_bytes,
+                                       stream or None), "tide_ce_loss")
+
+
+def tide_ce_grad_workspace(ce: CeDesc) -> int:
+    return _size(load_library().tide_ce_grad_workspace(ce), "tide_ce_grad_workspace")
+
+
+def tide_ce_grad(ce: CeDesc, lse: int, dloss: int, dx: int, dx_stride: int, dweight: int, dweight_stride: int,
+                 workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().tide_ce_grad(ce, lse or None, dloss or None, dx or None, dx_stride, dweight or None,
+                                       dweight_stride, workspace or None, workspace_bytes, stream or None),
+           "tide_ce_grad")
+
+
+def tide_swiglu_ckpt8(rows: int, cols: int, dtype: int, gate: int, gate_stride: int, up: int, up_stride: int, h: int,
+                      h_stride: int, ckpt: Ckpt8Desc, stream: int = 0) -> None:
+    _check(load_library().tide_swiglu_ckpt8(rows, cols, dtype, gate or None, gate_stride, up or None, up_stride,
+                                            h or None, h_stride, ckpt, stream or None), "tide_swiglu_ckpt8")
+
+
+def tide_swiglu_ckpt8_grad(rows: int, cols: int, dtype: int, ckpt: Ckpt8Desc, dh: int, dh_stride: int, dgate: int,
+                           dgate_stride: int, dup: int, dup_stride: int, h: int, h_stride: int,
+                           stream: int = 0) -> None:
+    _check(load_library().tide_swiglu_ckpt8_grad(rows, cols, dtype, ckpt, dh or None, dh_stride, dgate or None,
+                                                 dgate_stride, dup or None, dup_stride, h or None, h_stride,
+                                                 stream or None), "tide_swiglu_ckpt8_grad")
+
+
+def tide_ops_device_status(stream: int = 0) -> int:
+    """Returns the status code (TIDE_OK or TIDE_ERR_TIMEOUT) instead of raising on a timeout."""
+    st = load_library().tide_ops_device_status(stream or None)
+    if st not in (TIDE_OK, TIDE_ERR_TIMEOUT):
+        _check(st, "tide_ops_device_status")
+    return st

@@ -364,6 +364,186 @@ TIDE_API tide_status_t tide_rs_fold_noalloc(int32_t world, int32_t num_params, c
                                             int32_t accumulate, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Training-step operators
+ *
+ * The compute next to the collectives of an FSDP2 step: it reads the bf16
+ * parameters that the placements write and leaves gradients in the form (and,
+ * when the caller passes views of them, in the buffers) that the fold reads.
+ * None of these has a counterpart in the TIDE paper.
+ *
+ * Common to all: the conventions at the top of this file (caller owns every
+ * tensor, status codes, stream order, 64-bit sizes, no allocation); element
+ * types are TIDE_DTYPE_BF16 and TIDE_DTYPE_F32; strides are in elements and
+ * innermost dimensions are contiguous; sums, statistics and intermediate
+ * values are fp32 and rounded once, to nearest even, when they are stored.
+ * Tensors are aligned to their element size; rows on 16-byte boundaries take
+ * the vector paths.  Outputs must not overlap inputs or each other, except
+ * that tide_qk_norm_rope and its gradient may write an output over the input
+ * it is computed from (same pointer and strides).  Scratch memory is passed
+ * in: `workspace` points to at least the bytes that the operator's
+ * *_workspace function returns, 256-byte aligned, and is free for reuse when
+ * the call's work on the stream is done; calls that can overlap need a
+ * workspace each.  Results do not depend on what the workspace held, and
+ * repeated calls give the same bits.  Every call may be captured into a CUDA
+ * graph.  Zero tokens or rows are valid and launch nothing beyond the
+ * gradients' zeroes.
+ * ---------------------------------------------------------------------- */
+
+/* One tensor of heads: element (t, h, d) is data[t * token_stride +
+ * h * head_stride + d]; strides may be 0 (broadcast) for inputs. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} tide_heads_t;
+
+/* What the head norm with rotation needs besides the heads. */
+typedef struct {
+    int64_t tokens;          /* T >= 0 */
+    int32_t q_heads;         /* >= 0 */
+    int32_t k_heads;         /* >= 0 */
+    int32_t head_dim;        /* D in [1, 4096] */
+    int32_t rotary_dim;      /* R even, in [0, D]: columns 0..R-1 are rotated, the rest are not */
+    int64_t max_position;    /* rows of the table */
+    const float *table;      /* device fp32 [max_position, R]: R/2 cosines, then R/2 sines (see tide_rope_table);
+                                16-byte aligned for the vector path; unused if R = 0 */
+    const void *positions;   /* device integers [T]: row of the table for each token; unused if R = 0.  A position
+                                outside [0, max_position) makes the token's rotated columns NaN */
+    int32_t position_bytes;  /* 4 or 8 */
+    int32_t dtype;           /* of heads, weights and their gradients */
+    int32_t interleaved;     /* pairs of the rotation: 0 = (i, i + R/2), 1 = (2i, 2i + 1) */
+    float eps;               /* >= 0, added to the mean square */
+    const void *q_weight;    /* device [D] norm weight of the queries, or NULL: no norm */
+    const void *k_weight;    /* the same for the keys */
+} tide_qk_t;
+
+/*
+ * Table of a rotary embedding: entry (p, i) is cos(p f_i) and (p, R/2 + i)
+ * sin(p f_i), computed in 64 bits and rounded to fp32, with the frequencies
+ * f_i = base^(-2 i / R).  scaling = 0 leaves them; 1 divides all by `factor`
+ * (positions interpolated); 2 scales by parts for contexts longer than the
+ * `original` training context: with wavelength w = 2 pi / f, frequencies with
+ * w < original / high_freq_factor stay, those with w > original /
+ * low_freq_factor are divided by `factor`, and between the two the divided
+ * and the plain one are mixed linearly in original / w.
+ * R even, >= 2; base > 0; factor, low_freq_factor, high_freq_factor and
+ * original > 0 where they are used, high_freq_factor > low_freq_factor.
+ */
+TIDE_API tide_status_t tide_rope_table(int64_t max_position, int32_t rotary_dim, double base, int32_t scaling,
+                                       double factor, double low_freq_factor, double high_freq_factor,
+                                       double original, float *table, void *stream);
+
+/*
+ * Norm of queries and keys for each head, and the rotation of their first R
+ * columns by their position's angles, in one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (over the D columns of a head)
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)  for each pair.
+ */
+TIDE_API tide_status_t tide_qk_norm_rope(const tide_qk_t *qk, const tide_heads_t *q, const tide_heads_t *k,
+                                         const tide_heads_t *q_out, const tide_heads_t *k_out, void *stream);
+
+/*
+ * Gradient of tide_qk_norm_rope: from the gradients of its outputs (dq_out,
+ * dk_out) and its inputs (q, k; not read where the weight is NULL, and may
+ * then be NULL) to the gradients of the inputs (dq, dk) and of the weights
+ * (dq_weight, dk_weight: device [D] of `dtype`, overwritten; NULL where the
+ * weight is).  Weight gradients are summed in a fixed order.
+ */
+TIDE_API tide_status_t tide_qk_norm_rope_grad(const tide_qk_t *qk, const tide_heads_t *dq_out,
+                                              const tide_heads_t *dk_out, const tide_heads_t *q,
+                                              const tide_heads_t *k, const tide_heads_t *dq, const tide_heads_t *dk,
+                                              void *dq_weight, void *dk_weight, void *workspace,
+                                              int64_t workspace_bytes, void *stream);
+TIDE_API int64_t tide_qk_norm_rope_grad_workspace(const tide_qk_t *qk);
+
+/* Vocabulary head and targets: logits z = x weight^T, never written out. */
+typedef struct {
+    int64_t tokens;          /* T >= 0 */
+    int64_t vocab;           /* V in [1, 2^31 - 512] */
+    int64_t hidden;          /* H in [1, 2^20] */
+    const void *x;           /* device bf16 [T, H] */
+    int64_t x_stride;        /* elements between rows, >= H */
+    const void *weight;      /* device bf16 [V, H] */
+    int64_t weight_stride;
+    const void *targets;     /* device integers [T] */
+    int32_t target_bytes;    /* 4 or 8 */
+    int64_t ignore_index;    /* tokens with this target count for nothing */
+} tide_ce_t;
+
+/*
+ * Softmax cross entropy of every token, with the logits taken in pieces of
+ * the vocabulary and kept nowhere:
+ *   lse[t] = log sum_v exp(z_tv);  loss[t] = lse[t] - z_t,target.
+ * loss and lse are device fp32 [T].  An ignored token's loss is 0; a target
+ * outside [0, V) that is not ignore_index makes the token's loss NaN.
+ * bf16 only.  Rows that are not on 16-byte boundaries are copied into the
+ * workspace first.
+ */
+TIDE_API tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+TIDE_API int64_t tide_ce_loss_workspace(const tide_ce_t *ce);
+
+/*
+ * Gradient of tide_ce_loss from its lse and the gradient dloss (device fp32
+ * [T]) of its losses:
+ *   dz = (exp(z - lse) - [v = target]) dloss;  dx = dz weight;  dweight = dz^T x.
+ * The logits are computed again, one piece of the vocabulary at a time; dz is
+ * rounded to bf16 for the two products.  dx (bf16 [T, H], row stride
+ * dx_stride) and dweight (bf16 [V, H], dweight_stride) are overwritten.  An
+ * ignored token gives nothing, whatever its dloss; a target outside [0, V)
+ * that is not ignore_index makes the token's dz NaN.
+ */
+TIDE_API tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *dloss, void *dx,
+                                    int64_t dx_stride, void *dweight, int64_t dweight_stride, void *workspace,
+                                    int64_t workspace_bytes, void *stream);
+TIDE_API int64_t tide_ce_grad_workspace(const tide_ce_t *ce);
+
+/* Columns of a row that share one scale in an 8-bit checkpoint. */
+#define TIDE_CKPT8_BLOCK 128
+
+/* An 8-bit activation checkpoint of gate and up ([rows, cols] each): codes
+ * are e4m3, contiguous; the value of a code in column c is code * 2^(e - 127)
+ * with e = exps[row * ceil(cols / 128) + c / 128].  e is the smallest
+ * exponent >= 1 that brings the block's largest finite magnitude to at most
+ * 448 (127 for a block of zeroes), so scaling rounds nothing; a value that is
+ * not finite is kept as NaN and does not count for the scale. */
+typedef struct {
+    void *gate_codes;  /* device uint8 [rows, cols] */
+    void *gate_exps;   /* device uint8 [rows, ceil(cols / 128)] */
+    void *up_codes;
+    void *up_exps;
+} tide_ckpt8_t;
+
+/*
+ * SwiGLU h = gate / (1 + exp(-gate)) * up with its 8-bit checkpoint, in one
+ * pass.  gate, up: device [rows, cols] with row strides; h likewise.  h is
+ * computed from the inputs, not from their codes.
+ */
+TIDE_API tide_status_t tide_swiglu_ckpt8(int64_t rows, int64_t cols, int32_t dtype, const void *gate,
+                                         int64_t gate_stride, const void *up, int64_t up_stride, void *h,
+                                         int64_t h_stride, const tide_ckpt8_t *ckpt, void *stream);
+
+/*
+ * Gradient of SwiGLU from its checkpoint and dh ([rows, cols], dh_stride), as
+ * if the values that the codes stand for had been the inputs:
+ *   dgate = dh up s (1 + gate (1 - s)), s = 1 / (1 + exp(-gate));
+ *   dup = dh gate s;  h = gate s up  (for the next layer's weight gradient;
+ *   h may be NULL).
+ */
+TIDE_API tide_status_t tide_swiglu_ckpt8_grad(int64_t rows, int64_t cols, int32_t dtype, const tide_ckpt8_t *ckpt,
+                                              const void *dh, int64_t dh_stride, void *dgate, int64_t dgate_stride,
+                                              void *dup, int64_t dup_stride, void *h, int64_t h_stride,
+                                              void *stream);
+
+/*
+ * Read and clear the operators' status word of the current device
+ * (synchronises `stream`): TIDE_ERR_TIMEOUT if a bounded device-side wait of
+ * tide_ce_loss or tide_ce_grad expired there since the last such read (the
+ * outputs of that call are then incomplete), else TIDE_OK.
+ */
+TIDE_API tide_status_t tide_ops_device_status(void *stream);
+
+/* ------------------------------------------------------------------------
  * Multi-node schedule planners (host only).  A single GPU runs none of these
  * schedules; a multi-node runtime plans with them.
  * ---------------------------------------------------------------------- */
