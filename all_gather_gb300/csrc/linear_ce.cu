@@ -8,20 +8,42 @@
 // each of its rows, its maximum m and sum s of exp(z - m), and a second kernel
 // joins a row's pairs in a fixed order.  The gradient makes the logits again,
 // a piece of the vocabulary at a time, and keeps only that piece's dz.
+//
+// All products run in one persistent kernel, one block a SM: a thread fetches
+// 64 columns of both operands at a time into a ring of swizzled tiles (TMA),
+// a thread issues the tensor-core products of 128 x 256 tiles into one of two
+// accumulators in tensor memory, and four warps work on the other one (a
+// thread a row).  The operand whose rows are the summed dimension (W and x in
+// the gradients, dz in dW) is read as it lies, MN-major, so nothing is
+// transposed in memory.  Bound by the tensor cores for many tokens and by the
+// weight's bytes for few.
 #include <cuda_runtime.h>
 
 #include "ops_internal.h"
+#include "umma.h"
 
 namespace {
 
 using tide::op_aligned;
 using tide::op_fail;
-using tide::to_f32;
 using bf16 = __nv_bfloat16;
+namespace um = tide::umma;
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
+constexpr int kM = 128, kN = 256, kK = 64;   // tile and step of the sum
+constexpr int kStages = 4;
+constexpr int kABytes = kM * kK * 2, kBBytes = kN * kK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kRingBytes = kStages * kStageBytes;
+constexpr int kSmemBytes = kRingBytes + 1024 + 256;  // 1024: the ring's alignment; 256: barriers
+constexpr int kThreads = 192;                        // fetch, products, 4 warps of results
+constexpr int kTmemCols = 512;                       // two accumulators of 256 columns
+constexpr int kGroupM = 16;                          // row tiles that share a sweep over the columns
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
 constexpr int64_t kMinPiece = 8192;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Set when a bounded wait of a product runs out; read and cleared by
+// tide_ops_device_status.
+__device__ int g_timed_out;
 
 // target of a token: its column, -1 = ignored, -2 = outside the vocabulary
 struct Targets {
@@ -36,16 +58,13 @@ struct Targets {
     }
 };
 
-struct Operand {
-    const bf16 *p;
-    int64_t row, k;  // strides of the tile's rows (or columns) and of the sum
-};
-
 enum Epilogue { kStats, kDz, kAdd, kStore };
 
 struct Gemm {
-    Operand a, b;
+    CUtensorMap a, b;
     int64_t M, N, K;
+    int a_mn, b_mn;      // operand is MN-major
+    int tiles_m, tiles_n, splits, steps;  // steps of the sum in all
     int64_t v0;          // first vocabulary column of this piece
     Targets y;
     float2 *part;        // kStats: [column tiles][M]
@@ -53,75 +72,290 @@ struct Gemm {
     const float *lse, *dloss;
     bf16 *out;           // kDz, kStore
     int64_t out_stride;
-    float *acc;          // kAdd: [M][N], added to unless `first`
+    int out_vec;         // its rows are on 16-byte boundaries
+    float *acc;          // kAdd: [splits][M][N], added to unless `first`
     int first;
+    uint64_t wait_ns;
 };
 
-template <int E>
-__global__ void __launch_bounds__(kThreads) gemm_kernel(const Gemm g)
+// exp of a difference of logits.  The difference is taken before the factor
+// log2(e): folded into one multiply-add with a rounded log2(e) z it would be
+// off by the rounding of z, and overflow for the largest z.
+__device__ __forceinline__ float exp_fast(float x)
 {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
-    __shared__ float cs[E == kStats ? kTile : 1][kTile + 1];
-    const int64_t m0 = int64_t(blockIdx.y) * kTile, n0 = int64_t(blockIdx.x) * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float c[4][4] = {};
-    for (int64_t k0 = 0; k0 < g.K; k0 += kStep) {
-        for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
-            const int k = i % kStep, r = i / kStep;
-            const bool in_k = k0 + k < g.K;
-            as[k][r] = in_k && m0 + r < g.M ? to_f32(g.a.p[(m0 + r) * g.a.row + (k0 + k) * g.a.k]) : 0.f;
-            bs[k][r] = in_k && n0 + r < g.N ? to_f32(g.b.p[(n0 + r) * g.b.row + (k0 + k) * g.b.k]) : 0.f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j)
-                    c[i][j] = __fmaf_rn(as[k][ty * 4 + i], bs[k][tx * 4 + j], c[i][j]);
-        __syncthreads();
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+    return y;
+}
+
+struct Work {
+    int m, n, split, s0, s1;  // tile, share of the sum, its steps
+};
+__device__ __forceinline__ Work work_of(const Gemm &g, int64_t i)
+{
+    Work w;
+    const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
+    w.split = int(i / tiles);
+    i -= w.split * tiles;
+    const int64_t group = i / (int64_t(kGroupM) * g.tiles_n);
+    const int rows = min(kGroupM, g.tiles_m - int(group) * kGroupM);
+    i -= group * kGroupM * g.tiles_n;
+    w.n = int(i / rows);
+    w.m = int(group) * kGroupM + int(i % rows);
+    const int64_t s = g.steps;
+    w.s0 = int(s * w.split / g.splits);
+    w.s1 = int(s * (w.split + 1) / g.splits);
+    return w;
+}
+
+// Running maximum and sum of a row over 32 more logits, of which the first
+// `cols` count.
+__device__ __forceinline__ void add_stats(const uint32_t (&v)[32], int cols, float &top, float &sum)
+{
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < cols)
+            m = fmaxf(m, __uint_as_float(v[i]));
+    const float now = fmaxf(top, m);
+    const float at = isinf(now) ? 0.f : now;  // an infinite maximum: exp(z) itself, 0 or infinite
+    if (now != top) {
+        sum *= isinf(top) ? 0.f : exp_fast(top - at);
+        top = now;
     }
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx * 4 + j;
-            if (E == kStats) {
-                cs[ty * 4 + i][tx * 4 + j] = c[i][j];
-            } else if (m < g.M && n < g.N) {
-                if (E == kDz) {
-                    const int64_t y = g.y.get(m);
-                    float d = 0.f;
-                    if (y != -1) {
-                        d = (expf(c[i][j] - g.lse[m]) - (g.v0 + n == y ? 1.f : 0.f)) * g.dloss[m];
-                        if (y == -2)
-                            d = __int_as_float(0x7fffffff);
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        if (i < cols)
+            a += exp_fast(__uint_as_float(v[i]) - at);
+        if (i + 1 < cols)
+            b += exp_fast(__uint_as_float(v[i + 1]) - at);
+    }
+    sum += a + b;
+}
+
+template <int E>
+__device__ __forceinline__ void store_bf16(const Gemm &g, int64_t m, int64_t n, int cols, const float (&f)[32])
+{
+    bf16 *out = g.out + m * g.out_stride + n;
+    if (g.out_vec && cols >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            tide::store8(out + i, f + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < cols)
+                out[i] = __float2bfloat16_rn(f[i]);
+    }
+}
+
+template <int E>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
+    __shared__ uint64_t bars[2 * kStages + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages;
+    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            um::mbar_init(full + 8 * i, 1);
+            um::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            um::mbar_init(acc_full + 8 * i, 1);
+            um::mbar_init(acc_empty + 8 * i, 4);
+        }
+        um::mbar_init(drained, 1);
+        um::fence_barrier_init();
+        gave_up = 0;
+        um::prefetch_map(&g.a);
+        um::prefetch_map(&g.b);
+    }
+    if (warp == 1)
+        um::tmem_alloc(um::smem_addr(&tmem_slot), kTmemCols);
+    um::fence_before();
+    __syncthreads();
+    um::fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, turns = 0;  // ring position, and how often the ring went round
+            bool ok = true;
+            for (int64_t i = blockIdx.x; ok && i < works; i += gridDim.x) {
+                const Work w = work_of(g, i);
+                for (int s = w.s0; s < w.s1; ++s) {
+                    if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
+                        break;
+                    const uint32_t a = ring + stage * kStageBytes, b = a + kABytes, bar = full + 8 * stage;
+                    um::mbar_expect(bar, kStageBytes);
+                    if (g.a_mn) {
+                        for (int j = 0; j < kM / 64; ++j)
+                            um::tma_load_2d(a + j * 64 * kK * 2, &g.a, w.m * kM + j * 64, s * kK, bar);
+                    } else {
+                        um::tma_load_2d(a, &g.a, s * kK, w.m * kM, bar);
                     }
-                    g.out[m * g.out_stride + n] = __float2bfloat16_rn(d);
-                } else if (E == kAdd) {
-                    float *p = g.acc + m * g.N + n;
-                    *p = g.first ? c[i][j] : *p + c[i][j];
-                } else {
-                    g.out[m * g.out_stride + n] = __float2bfloat16_rn(c[i][j]);
+                    if (g.b_mn) {
+                        for (int j = 0; j < kN / 64; ++j)
+                            um::tma_load_2d(b + j * 64 * kK * 2, &g.b, w.n * kN + j * 64, s * kK, bar);
+                    } else {
+                        um::tma_load_2d(b, &g.b, s * kK, w.n * kN, bar);
+                    }
+                    if (++stage == kStages)
+                        stage = 0, ++turns;
+                }
+            }
+            if (!ok) {  // wait for the copies in flight before the block's memory goes
+                for (int k = 0; k < kStages; ++k) {
+                    const int times = turns + (k < stage);
+                    const uint64_t t0 = um::now_ns();
+                    while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) &&
+                           um::now_ns() - t0 < g.wait_ns) {
+                    }
                 }
             }
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = um::instr_desc(kM, kN, g.a_mn, g.b_mn);
+            const uint32_t a_step = (g.a_mn ? 2048 : 32) >> 4, b_step = (g.b_mn ? 2048 : 32) >> 4;  // 16 of the sum
+            int stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; ok && i < works; i += gridDim.x) {
+                const Work w = work_of(g, i);
+                if (!(ok = um::mbar_wait(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
+                    break;
+                um::fence_after();
+                const uint32_t d = tmem + buf * kN;
+                for (int s = w.s0; s < w.s1; ++s) {
+                    if (!(ok = um::mbar_wait(full + 8 * stage, phase, &gave_up, g.wait_ns)))
+                        break;
+                    um::fence_after();
+                    const uint32_t base = ring + stage * kStageBytes;
+                    const uint64_t a = um::operand_desc(base, g.a_mn, 64 * kK * 2);
+                    const uint64_t b = um::operand_desc(base + kABytes, g.b_mn, 64 * kK * 2);
+#pragma unroll
+                    for (int k = 0; k < kK / 16; ++k)
+                        um::mma_bf16(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
+                    um::mma_commit(empty + 8 * stage);
+                    if (++stage == kStages)
+                        stage = 0, phase ^= 1;
+                }
+                if (ok)
+                    um::mma_commit(acc_full + 8 * buf);
+                if (++buf == 2)
+                    buf = 0, buf_phase ^= 1;
+            }
+            if (!ok) {  // wait for the products in flight before the accumulators and tiles go
+                g_timed_out = 1;
+                um::mma_commit(drained);
+                const uint64_t t0 = um::now_ns();
+                while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < g.wait_ns) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp % 4;  // a warp reads the tensor-memory lanes of its number modulo 4
+        int buf = 0, buf_phase = 0;
+        for (int64_t i = blockIdx.x; i < works; i += gridDim.x) {
+            const Work w = work_of(g, i);
+            const int64_t m = int64_t(w.m) * kM + quarter * 32 + lane, n0 = int64_t(w.n) * kN;
+            const bool row = m < g.M;
+            int64_t y = -1;
+            float lse = 0.f, scale = 0.f;
+            if ((E == kStats || E == kDz) && row)
+                y = g.y.get(m);
+            if (E == kDz && row && y != -1) {
+                lse = g.lse[m];
+                scale = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[m];
+            }
+            if (!um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns)) {
+                g_timed_out = 1;
+                break;
+            }
+            um::fence_after();
+            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + buf * kN;
+            float top = -INFINITY, sum = 0.f;
+            for (int c = 0; c < kN; c += 32) {
+                const int cols = int(min(int64_t(32), g.N - n0 - c));
+                if (cols <= 0)
+                    break;
+                uint32_t v[32];
+                um::tmem_load32(d + c, v);
+                um::tmem_wait_load();
+                if (E == kAdd && w.s0 == w.s1) {  // a last piece shorter than its splits: nothing was summed
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = 0;
+                }
+                const int64_t n = n0 + c;
+                if (E == kStats) {
+                    add_stats(v, cols, top, sum);
+                    const int64_t at = y - n;
+                    if (at >= 0 && at < cols) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j == int(at))
+                                g.zy[m] = __uint_as_float(v[j]);
+                    }
+                } else if (row) {
+                    float f[32];
+                    if (E == kDz) {
+                        const int64_t at = y - g.v0 - n;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float p = exp_fast(__uint_as_float(v[j]) - lse);
+                            f[j] = y == -1 ? 0.f : (p - (j == at ? 1.f : 0.f)) * scale;
+                        }
+                        store_bf16<E>(g, m, n, cols, f);
+                    } else if (E == kStore) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            f[j] = __uint_as_float(v[j]);
+                        store_bf16<E>(g, m, n, cols, f);
+                    } else {
+                        float *acc = g.acc + (w.split * g.M + m) * g.N + n;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < cols)
+                                acc[j] = g.first ? __uint_as_float(v[j]) : acc[j] + __uint_as_float(v[j]);
+                    }
+                }
+            }
+            um::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                um::mbar_arrive(acc_empty + 8 * buf);
+            if (E == kStats && row)
+                g.part[int64_t(w.n) * g.M + m] = make_float2(top, sum);
+            if (++buf == 2)
+                buf = 0, buf_phase ^= 1;
+        }
     }
-    if (E != kStats)
-        return;
+    um::fence_before();
     __syncthreads();
-    const int r = threadIdx.x;
-    if (r >= kTile || m0 + r >= g.M)
-        return;
-    const int64_t t = m0 + r, y = g.y.get(t);
-    const int cols = int(min(int64_t(kTile), g.N - n0));
-    float top = -INFINITY, sum = 0.f;
-    for (int j = 0; j < cols; ++j) {
-        top = fmaxf(top, cs[r][j]);
-        if (n0 + j == y)
-            g.zy[t] = cs[r][j];
-    }
-    const float at = isinf(top) ? 0.f : top;
-    for (int j = 0; j < cols; ++j)
-        sum += expf(cs[r][j] - at);
-    g.part[int64_t(blockIdx.x) * g.M + t] = make_float2(top, sum);
+    um::fence_after();
+    if (warp == 1)
+        um::tmem_free(tmem, kTmemCols);
+}
+
+// Rows that the tiled copies cannot take (16-byte boundaries) go into the
+// workspace first, `pitch` elements apart.
+__global__ void __launch_bounds__(256) align_kernel(const bf16 *in, int64_t stride, int64_t rows, int64_t cols,
+                                                    bf16 *out, int64_t pitch)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256)
+            out[r * pitch + c] = in[r * stride + c];
 }
 
 __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int64_t tiles, int64_t T, const float *zy,
@@ -143,11 +377,17 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int64_t t
     loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - zy[t];
 }
 
-__global__ void __launch_bounds__(256) round_kernel(const float *acc, int64_t T, int64_t H, bf16 *out, int64_t stride)
+// dx = sum of the splits, in order.
+__global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, bf16 *out,
+                                                    int64_t stride)
 {
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < T * H)
-        out[i / H * stride + i % H] = __float2bfloat16_rn(acc[i]);
+    if (i >= T * H)
+        return;
+    float x = acc[i];
+    for (int s = 1; s < splits; ++s)
+        x += acc[s * T * H + i];
+    out[i / H * stride + i % H] = __float2bfloat16_rn(x);
 }
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -193,13 +433,155 @@ int64_t piece_of(const tide_ce_t *ce)
     return std::min(round_up(ce->vocab, 256), std::max(kMinPiece, fit));
 }
 
-dim3 grid_of(int64_t M, int64_t N) { return dim3(unsigned((N + kTile - 1) / kTile), unsigned((M + kTile - 1) / kTile)); }
+// ---------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A row-major bf16 matrix.
+struct Mat {
+    const bf16 *p;
+    int64_t rows, cols, stride;
+};
+
+bool rows_aligned(const void *p, int64_t stride, int64_t rows)
+{
+    return op_aligned(p, 16) && (rows < 2 || stride % 8 == 0);
+}
+
+// Tensor map whose copies are `box_rows` rows of 64 columns; what lies outside
+// the matrix reads as 0.
+tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows)
+{
+    const EncodeTiled enc = encode_tiled();
+    if (!enc)
+        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(m.rows < 2 ? (m.cols + 7) / 8 * 16 : m.stride * 2)};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, step[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box, step,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled: %d", int(r));
+    return TIDE_OK;
+}
 
 Gemm base(const tide_ce_t *ce)
 {
     Gemm g = {};
     g.y = {ce->targets, ce->target_bytes, ce->ignore_index, ce->vocab};
+    g.splits = 1;
+    g.wait_ns = tide::kWaitBudgetNs;
     return g;
+}
+
+// C[M, N] = sum over k of A B.  An operand is given with its rows as the tile's
+// dimension (K-major) or, mn, with its rows as the summed one.
+template <int E>
+tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, const char *what, cudaStream_t st)
+{
+    g.a_mn = a_mn, g.b_mn = b_mn;
+    g.M = a_mn ? a.cols : a.rows;
+    g.N = b_mn ? b.cols : b.rows;
+    g.K = a_mn ? a.rows : a.cols;
+    g.tiles_m = int((g.M + kM - 1) / kM);
+    g.tiles_n = int((g.N + kN - 1) / kN);
+    g.steps = int((g.K + kK - 1) / kK);
+    tide_status_t s = make_map(&g.a, a, a_mn ? kK : kM);
+    if (!s)
+        s = make_map(&g.b, b, b_mn ? kK : kN);
+    if (s)
+        return s;
+    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+    const unsigned grid = unsigned(std::min<int64_t>(works, tide::op_sm_count()));
+    gemm_kernel<E><<<grid, kThreads, kSmemBytes, st>>>(g);
+    return tide::op_launched(what);
+}
+
+// Where a call's scratch data lies in its workspace, in bytes.
+struct Layout {
+    int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
+    int64_t part = 0, zy = 0;           // loss
+    int64_t dz = 0, acc = 0, piece = 0; // gradient
+    int splits = 1;
+    int64_t bytes = 0;
+    int64_t take(int64_t n)
+    {
+        const int64_t at = bytes;
+        bytes += round_up(n, 256);
+        return at;
+    }
+};
+
+// Shares of the vocabulary piece that dx's sum is split into: its tiles alone
+// may be fewer than the SMs, or just over a whole number of rounds.
+int splits_of(const tide_ce_t *ce, int64_t piece)
+{
+    const int64_t sms = std::max(tide::op_sm_count(), 1);
+    const int64_t tiles = ((ce->tokens + kM - 1) / kM) * ((ce->hidden + kN - 1) / kN);
+    const int64_t steps = (std::min(piece, ce->vocab) + kK - 1) / kK;
+    int best = 1;
+    double best_time = 1e30;
+    for (int s = 1; s <= 64 && s <= steps / 4 + 1; ++s) {
+        if (s > 1 && ce->tokens * ce->hidden * 4 * s > kPieceBytes)
+            break;
+        // rounds of steps, and two steps' time a share for the tile's own start and end
+        const double time = double((tiles * s + sms - 1) / sms) * (double(steps) / s + 4.0);
+        if (time < best_time * 0.98)
+            best = s, best_time = time;
+    }
+    return best;
+}
+
+Layout layout_of(const tide_ce_t *ce, bool grad)
+{
+    Layout l;
+    l.pitch = round_up(ce->hidden, 8);
+    if (!rows_aligned(ce->x, ce->x_stride, ce->tokens))
+        l.x = l.take(ce->tokens * l.pitch * 2);
+    if (!rows_aligned(ce->weight, ce->weight_stride, ce->vocab))
+        l.w = l.take(ce->vocab * l.pitch * 2);
+    if (grad) {
+        l.piece = piece_of(ce);
+        l.splits = splits_of(ce, l.piece);
+        l.dz = l.take(ce->tokens * l.piece * 2);
+        l.acc = l.take(ce->tokens * ce->hidden * 4 * l.splits);
+    } else {
+        l.part = l.take((ce->vocab + kN - 1) / kN * ce->tokens * 8);
+        l.zy = l.take(ce->tokens * 4);
+    }
+    l.bytes = std::max<int64_t>(l.bytes, 256);
+    return l;
+}
+
+tide_status_t align_rows(Mat &m, char *workspace, int64_t at, int64_t pitch, cudaStream_t st)
+{
+    if (at < 0 || m.rows == 0)
+        return TIDE_OK;
+    bf16 *out = reinterpret_cast<bf16 *>(workspace + at);
+    align_kernel<<<unsigned(std::min<int64_t>(m.rows, 1 << 20)), 256, 0, st>>>(m.p, m.stride, m.rows, m.cols, out,
+                                                                             pitch);
+    m.p = out, m.stride = pitch;
+    return tide::op_launched("ce: aligned rows");
 }
 
 }  // namespace
@@ -209,10 +591,7 @@ extern "C" {
 int64_t tide_ce_loss_workspace(const tide_ce_t *ce)
 {
     tide::record_error("");
-    if (check_desc(ce))
-        return -1;
-    const int64_t tiles = (ce->vocab + kTile - 1) / kTile;
-    return 256 + round_up(tiles * ce->tokens * 8, 256) + round_up(ce->tokens * 4, 256);
+    return check_desc(ce) ? -1 : layout_of(ce, false).bytes;
 }
 
 tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *workspace, int64_t workspace_bytes,
@@ -228,31 +607,35 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
         return op_fail(TIDE_ERR_INVALID_ARG, "loss or lse is NULL");
     if (!op_aligned(loss, 4) || !op_aligned(lse, 4))
         return op_fail(TIDE_ERR_ALIGNMENT, "loss or lse is not aligned to its element size");
-    s = check_workspace(workspace, workspace_bytes, tide_ce_loss_workspace(ce));
+    const Layout l = layout_of(ce, false);
+    s = check_workspace(workspace, workspace_bytes, l.bytes);
     if (s)
         return s;
     const tide::NvtxRange range("tide_ce_loss");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t T = ce->tokens, V = ce->vocab, tiles = (V + kTile - 1) / kTile;
-    Gemm g = base(ce);
-    g.a = {static_cast<const bf16 *>(ce->x), ce->x_stride, 1};
-    g.b = {static_cast<const bf16 *>(ce->weight), ce->weight_stride, 1};
-    g.M = T, g.N = V, g.K = ce->hidden;
-    g.part = static_cast<float2 *>(workspace);
-    g.zy = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(tiles * T * 8, 256));
-    gemm_kernel<kStats><<<grid_of(T, V), kThreads, 0, st>>>(g);
-    if ((s = tide::op_launched("ce_loss")))
+    char *ws = static_cast<char *>(workspace);
+    const int64_t T = ce->tokens, V = ce->vocab, H = ce->hidden;
+    Mat x = {static_cast<const bf16 *>(ce->x), T, H, ce->x_stride};
+    Mat w = {static_cast<const bf16 *>(ce->weight), V, H, ce->weight_stride};
+    s = align_rows(x, ws, l.x, l.pitch, st);
+    if (!s)
+        s = align_rows(w, ws, l.w, l.pitch, st);
+    if (s)
         return s;
-    join_kernel<<<unsigned((T + 255) / 256), 256, 0, st>>>(g.part, tiles, T, g.zy, g.y, loss, lse);
+    Gemm g = base(ce);
+    g.part = reinterpret_cast<float2 *>(ws + l.part);
+    g.zy = reinterpret_cast<float *>(ws + l.zy);
+    s = launch<kStats>(g, x, false, w, false, "ce_loss", st);
+    if (s)
+        return s;
+    join_kernel<<<unsigned((T + 255) / 256), 256, 0, st>>>(g.part, g.tiles_n, T, g.zy, g.y, loss, lse);
     return tide::op_launched("ce_loss: join");
 }
 
 int64_t tide_ce_grad_workspace(const tide_ce_t *ce)
 {
     tide::record_error("");
-    if (check_desc(ce))
-        return -1;
-    return 256 + round_up(ce->tokens * piece_of(ce) * 2, 256) + round_up(ce->tokens * ce->hidden * 4, 256);
+    return check_desc(ce) ? -1 : layout_of(ce, true).bytes;
 }
 
 tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *dloss, void *dx, int64_t dx_stride,
@@ -273,54 +656,69 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
         (ce->tokens > 1 && dx_stride < ce->hidden) || (ce->vocab > 1 && dweight_stride < ce->hidden))
         return op_fail(TIDE_ERR_INVALID_ARG, "dx_stride %lld, dweight_stride %lld for hidden %lld",
                        (long long)dx_stride, (long long)dweight_stride, (long long)ce->hidden);
-    s = check_workspace(workspace, workspace_bytes, tide_ce_grad_workspace(ce));
+    const Layout l = layout_of(ce, true);
+    s = check_workspace(workspace, workspace_bytes, l.bytes);
     if (s)
         return s;
     const tide::NvtxRange range("tide_ce_grad");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t T = ce->tokens, V = ce->vocab, H = ce->hidden, piece = piece_of(ce);
-    const bf16 *x = static_cast<const bf16 *>(ce->x), *w = static_cast<const bf16 *>(ce->weight);
-    bf16 *dz = static_cast<bf16 *>(workspace);
-    float *acc = reinterpret_cast<float *>(static_cast<char *>(workspace) + round_up(T * piece * 2, 256));
-    for (int64_t v0 = 0; v0 < V; v0 += piece) {
-        const int64_t n = std::min(piece, V - v0);
+    char *ws = static_cast<char *>(workspace);
+    const int64_t T = ce->tokens, V = ce->vocab, H = ce->hidden;
+    if (T == 0) {  // nothing to sum
+        const cudaError_t e = cudaMemset2DAsync(dweight, size_t(V > 1 ? dweight_stride : H) * 2, 0, size_t(H) * 2,
+                                                size_t(V), st);
+        return e == cudaSuccess ? TIDE_OK : op_fail(TIDE_ERR_CUDA, "ce_grad: %s", cudaGetErrorString(e));
+    }
+    Mat x = {static_cast<const bf16 *>(ce->x), T, H, ce->x_stride};
+    Mat w = {static_cast<const bf16 *>(ce->weight), V, H, ce->weight_stride};
+    s = align_rows(x, ws, l.x, l.pitch, st);
+    if (!s)
+        s = align_rows(w, ws, l.w, l.pitch, st);
+    bf16 *dz = reinterpret_cast<bf16 *>(ws + l.dz);
+    float *acc = reinterpret_cast<float *>(ws + l.acc);
+    for (int64_t v0 = 0; !s && v0 < V; v0 += l.piece) {
+        const int64_t n = std::min(l.piece, V - v0);
+        const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece};
         Gemm g = base(ce);
         g.v0 = v0;
-        if (T > 0) {
-            g.a = {x, ce->x_stride, 1};
-            g.b = {w + v0 * ce->weight_stride, ce->weight_stride, 1};
-            g.M = T, g.N = n, g.K = H;
-            g.lse = lse, g.dloss = dloss, g.out = dz, g.out_stride = piece;
-            gemm_kernel<kDz><<<grid_of(g.M, g.N), kThreads, 0, st>>>(g);
-            if ((s = tide::op_launched("ce_grad: dz")))
-                return s;
-            g.a = {dz, piece, 1};
-            g.b = {w + v0 * ce->weight_stride, 1, ce->weight_stride};
-            g.M = T, g.N = H, g.K = n;
-            g.acc = acc, g.first = v0 == 0;
-            gemm_kernel<kAdd><<<grid_of(g.M, g.N), kThreads, 0, st>>>(g);
-            if ((s = tide::op_launched("ce_grad: dx")))
-                return s;
-        }
-        g.a = {dz, 1, piece};
-        g.b = {x, 1, ce->x_stride};
-        g.M = n, g.N = H, g.K = T;
-        g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
-        gemm_kernel<kStore><<<grid_of(g.M, g.N), kThreads, 0, st>>>(g);
-        if ((s = tide::op_launched("ce_grad: dweight")))
+        g.lse = lse, g.dloss = dloss;
+        g.out = dz, g.out_stride = l.piece, g.out_vec = 1;
+        s = launch<kDz>(g, x, false, wp, false, "ce_grad: dz", st);
+        if (s)
             return s;
+        g.acc = acc, g.first = v0 == 0, g.splits = l.splits;
+        s = launch<kAdd>(g, dzp, false, wp, true, "ce_grad: dx", st);
+        if (s)
+            return s;
+        g.splits = 1;
+        g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
+        g.out_vec = rows_aligned(g.out, dweight_stride, V);
+        s = launch<kStore>(g, dzp, true, x, true, "ce_grad: dweight", st);
     }
-    if (T == 0)
-        return TIDE_OK;
-    round_kernel<<<unsigned((T * H + 255) / 256), 256, 0, st>>>(acc, T, H, static_cast<bf16 *>(dx), dx_stride);
+    if (s)
+        return s;
+    round_kernel<<<unsigned((T * H + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, static_cast<bf16 *>(dx),
+                                                               dx_stride);
     return tide::op_launched("ce_grad: rounding");
 }
 
 tide_status_t tide_ops_device_status(void *stream)
 {
     tide::record_error("");
-    const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? TIDE_OK : op_fail(TIDE_ERR_CUDA, "synchronise: %s", cudaGetErrorString(e));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int seen = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&seen, g_timed_out, sizeof seen, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && seen) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_timed_out, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+    }
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "operators' status: %s", cudaGetErrorString(e));
+    return seen ? op_fail(TIDE_ERR_TIMEOUT, "a bounded device-side wait expired") : TIDE_OK;
 }
 
 }  // extern "C"
