@@ -14,10 +14,13 @@
 // whole rotation pairs (half layout: columns 8u.. and R/2 + 8u..; interleaved:
 // 16 consecutive columns; unrotated columns: 16 consecutive), one unit a lane,
 // so the rotation needs no exchange between lanes and the two sums of a head
-// are butterflies over G = 4 to 32 lanes.  A warp holds 32 / G heads of one
-// token at a time, keeps the token's cosines and sines and the weight in
-// registers over the token's heads, and issues the loads of two heads before
-// it uses the first.
+// are butterflies over G = 4 to 32 lanes.  A warp takes 32 / G heads of one
+// token at a time (a step).  Persistent warps copy their next kDepth - 1 steps
+// into shared memory (cp.async, every lane its own vectors, so nothing waits
+// for another warp), which keeps enough bytes on their way from few warps with
+// many registers; a token's angles come along with its first step.  Products
+// run on pairs of fp32 (f32x2), with the weight folded into the cosines and
+// sines once a token: three instructions a pair.
 #include <cuda_runtime.h>
 
 #include "ops_internal.h"
@@ -67,6 +70,7 @@ struct QkArgs {
     const void *positions;
     int position_bytes;
     float eps;
+    int heads_per_item;  // forward: queries, then keys
 };
 
 template <typename T>
@@ -96,58 +100,6 @@ __device__ __forceinline__ Unit unit_of(int u, int D, int R)
     return n;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_unit(const T *row, const Unit &n, bool on, float (&v)[16])
-{
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = 0.f;
-    if (on && n.has0)
-        load8(row + n.off0, v);
-    if (on && n.has1)
-        load8(row + n.off1, v + 8);
-}
-template <typename T>
-__device__ __forceinline__ void store_unit(T *row, const Unit &n, bool on, const float (&v)[16])
-{
-    if (on && n.has0)
-        store8(row + n.off0, v);
-    if (on && n.has1)
-        store8(row + n.off1, v + 8);
-}
-
-// Cosines and sines of a unit's eight pairs.
-template <typename T>
-__device__ __forceinline__ void load_angles(const QkArgs<T> &a, int64_t t, const Unit &n, float (&c)[8], float (&s)[8])
-{
-    if (!n.rot)
-        return;
-    const int64_t pos = position_of(a, t);
-    if (pos < 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[i] = s[i] = __int_as_float(0x7fffffff);
-        return;
-    }
-    const float *row = a.table + pos * a.R;
-    load8(row + n.ci, c);
-    load8(row + a.R / 2 + n.ci, s);
-}
-
-// (a, b) -> (a c - b s, b c + a s), with s negated for the way back.
-template <bool IL, bool BACK>
-__device__ __forceinline__ void rotate(float (&v)[16], const float (&c)[8], const float (&s)[8])
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float &x = v[IL ? 2 * j : j], &y = v[IL ? 2 * j + 1 : 8 + j];
-        const float sj = BACK ? -s[j] : s[j];
-        const float nx = __fmaf_rn(x, c[j], -__fmul_rn(y, sj));
-        y = __fmaf_rn(y, c[j], __fmul_rn(x, sj));
-        x = nx;
-    }
-}
-
 template <int G>
 __device__ __forceinline__ float group_sum(float x)
 {
@@ -157,130 +109,463 @@ __device__ __forceinline__ float group_sum(float x)
     return x;
 }
 
-template <int G>
-__device__ __forceinline__ float inv_rms(const float (&v)[16], int D, float eps)
+// Two fp32 values in one 64-bit register pair.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi)
 {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        ss = __fmaf_rn(v[i], v[i], ss);
-    return rsqrtf(__fdividef(group_sum<G>(ss), float(D)) + eps);
+    return f32x2(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo_of(f32x2 x) { return __uint_as_float(uint32_t(x)); }
+__device__ __forceinline__ float hi_of(f32x2 x) { return __uint_as_float(uint32_t(x >> 32)); }
+__device__ __forceinline__ f32x2 swapped(f32x2 x) { return x >> 32 | x << 32; }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
 
-template <typename T, int G, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const QkArgs<T> a)
-{
-    constexpr int kRows = 32 / G;  // heads of one step of a warp
-    const int lane = threadIdx.x & 31, g = lane / G;
-    const Unit n = unit_of<IL>(lane % G, a.D, a.R);
-    int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int which = item >= a.part[0].items;
-    if (which)
-        item -= a.part[0].items;
-    const Part<T> &p = a.part[which];
-    if (item >= p.items)
-        return;
-    const int chunks = (p.heads + p.heads_per_item - 1) / p.heads_per_item;
-    const int64_t t = item / chunks;
-    const int h0 = int(item - t * chunks) * p.heads_per_item;
-    const int h1 = min(p.heads, h0 + p.heads_per_item);
+constexpr int kDepth = 4;  // steps of a warp's ring
 
-    float c[8], s[8], w[16];
-    load_angles(a, t, n, c, s);
-    if (p.w)
-        load_unit(p.w, n, true, w);
-    for (int hb = h0; hb < h1; hb += 2 * kRows) {
-        const int h[2] = {hb + g, hb + kRows + g};
-        float v[2][16];
+__device__ __forceinline__ void copy16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sixteen elements of a unit as pairs.
+__device__ __forceinline__ void unpack8(const uint4 *q, int stride, f32x2 *v, const __nv_bfloat16 *)
+{
+    const uint4 x = q[0];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            load_unit(p.x.row(t, h[k]), n, h[k] < h1, v[k]);
+    for (int i = 0; i < 4; ++i)
+        v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack8(const uint4 *q, int stride, f32x2 *v, const float *)
+{
+    const uint4 x = q[0], y = q[stride];
+    v[0] = f32x2(x.y) << 32 | x.x, v[1] = f32x2(x.w) << 32 | x.z;
+    v[2] = f32x2(y.y) << 32 | y.x, v[3] = f32x2(y.w) << 32 | y.z;
+}
+template <typename T>
+__device__ __forceinline__ void store_unit(T *row, const Unit &n, const f32x2 (&v)[8])
+{
+    float f[16];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (p.w) {
-                const float r = inv_rms<G>(v[k], a.D, a.eps);
+    for (int i = 0; i < 8; ++i)
+        f[2 * i] = lo_of(v[i]), f[2 * i + 1] = hi_of(v[i]);
+    if (n.has0)
+        store8(row + n.off0, f);
+    if (n.has1)
+        store8(row + n.off1, f + 8);
+}
+// A weight's elements of a unit (0 outside the head).
+template <typename T>
+__device__ __forceinline__ void load_weight(const T *w, const Unit &n, f32x2 (&v)[8])
+{
+    float f[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[k][i] = v[k][i] * r * w[i];
-            }
-            if (n.rot)
-                rotate<IL, false>(v[k], c, s);
-            store_unit(p.out.row(t, h[k]), n, h[k] < h1, v[k]);
+    for (int i = 0; i < 16; ++i)
+        f[i] = 0.f;
+    if (n.has0)
+        load8(w + n.off0, f);
+    if (n.has1)
+        load8(w + n.off1, f + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+// The other member of each element's rotation pair.
+template <bool IL>
+__device__ __forceinline__ f32x2 partner(const f32x2 (&v)[8], int i)
+{
+    return IL ? swapped(v[i]) : v[i ^ 4];
+}
+
+// Positions of a warp's items: lane j holds that of the j-th of 32 items, and
+// of the 32 after them.
+template <typename T>
+struct Positions {
+    int now, next;
+    int64_t block;
+    __device__ int load(const QkArgs<T> &a, int64_t item, int64_t items, int chunks) const
+    {
+        return a.R && item < items ? int(position_of(a, item / chunks)) : -1;
+    }
+    __device__ void start(const QkArgs<T> &a, int64_t first, int64_t step, int64_t items, int chunks)
+    {
+        const int lane = threadIdx.x & 31;
+        block = 0;
+        now = load(a, first + lane * step, items, chunks);
+        next = load(a, first + (lane + 32) * step, items, chunks);
+    }
+    // of the n-th item; n grows by at most one from call to call
+    __device__ int get(const QkArgs<T> &a, int64_t n, int64_t first, int64_t step, int64_t items, int chunks)
+    {
+        if (n / 32 != block) {
+            block = n / 32;
+            now = next;
+            next = load(a, first + ((block + 1) * 32 + (threadIdx.x & 31)) * step, items, chunks);
+        }
+        return __shfl_sync(0xffffffffu, now, int(n % 32));
+    }
+};
+
+// A warp's place in its list of steps.
+struct Cursor {
+    int64_t n, item, t;  // n-th item of the warp
+    int h, h0, h1;       // first head of the step; of the item; end of the item
+};
+template <typename T>
+__device__ __forceinline__ void enter(Cursor &c, int heads, int per_item, int chunks)
+{
+    c.t = c.item / chunks;
+    c.h = c.h0 = int(c.item - c.t * chunks) * per_item;
+    c.h1 = min(heads, c.h0 + per_item);
+}
+
+// Cosines and sines of a unit's pairs out of a token's row in shared memory,
+// as factors of an element and of its partner; back: of the reverse rotation.
+template <bool IL, bool BACK>
+__device__ __forceinline__ void angle_factors(const float *row, int R, const Unit &n, bool bad, f32x2 (&c2)[8],
+                                              f32x2 (&s2)[8])
+{
+    float c[8], s[8];
+    if (n.rot) {
+        load8(row + n.ci, c);
+        load8(row + R / 2 + n.ci, s);
+    }
+    if (bad) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c[j] = s[j] = __int_as_float(0x7fffffff);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (IL) {
+            c2[i] = pair(c[i], c[i]);
+            s2[i] = BACK ? pair(s[i], -s[i]) : pair(-s[i], s[i]);
+        } else {
+            const int j = 2 * (i & 3);
+            c2[i] = pair(c[j], c[j + 1]);
+            s2[i] = (i < 4) == BACK ? pair(s[j], s[j + 1]) : pair(-s[j], -s[j + 1]);
         }
     }
 }
 
+template <int G>
+__device__ __forceinline__ float inv_rms(const f32x2 (&v)[8], float inv_d, float eps)
+{
+    f32x2 ss = mul2(v[0], v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        ss = fma2(v[i], v[i], ss);
+    return rsqrtf(__fmaf_rn(group_sum<G>(lo_of(ss) + hi_of(ss)), inv_d, eps));
+}
+
+// Bytes of a warp's ring: kDepth steps of `tensors` tensors, and kDepth rows of angles.
+template <typename T>
+__host__ __device__ constexpr int ring_bytes(int tensors, int G)
+{
+    return kDepth * (tensors * 2 * int(sizeof(T)) / 2 * 512 + G * 64);
+}
+
 template <typename T, int G, bool IL>
-__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const QkArgs<T> a)
+__global__ void __launch_bounds__(kThreads, 2) qk_forward_kernel(const QkArgs<T> a)
+{
+    constexpr int kRows = 32 / G;       // heads of a step
+    constexpr int kVec = sizeof(T) / 2; // 16-byte pieces of eight elements
+    extern __shared__ uint4 smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
+    uint4 *ring = smem + warp * (ring_bytes<T>(1, G) / 16);
+    float *angles = reinterpret_cast<float *>(ring + kDepth * 2 * kVec * 32);
+    const Unit n = unit_of<IL>(lane % G, a.D, a.R);
+    const float inv_d = 1.f / float(a.D);
+    const int heads = a.part[0].heads + a.part[1].heads, hq = a.part[0].heads;
+    const int per_item = a.heads_per_item, chunks = (heads + per_item - 1) / per_item;
+    const int64_t items = a.tokens * chunks;
+    const int64_t first = int64_t(blockIdx.x) * kWarps + warp, step = int64_t(gridDim.x) * kWarps;
+    if (first >= items)
+        return;
+    Positions<T> positions;
+    positions.start(a, first, step, items, chunks);
+
+    // The next step to fetch, and its number.
+    Cursor f = {0, first, 0, 0, 0, 0};
+    enter<T>(f, heads, per_item, chunks);
+    int slot_f = 0, bad_bits = 0;  // bit n % 32: the n-th item's position is outside the table
+    auto fetch = [&] {
+        if (f.item < items) {
+            const int h = f.h + g;
+            if (h < f.h1) {
+                const Part<T> &p = a.part[h >= hq];
+                const T *row = p.x.row(f.t, h >= hq ? h - hq : h);
+                uint4 *to = ring + slot_f * 2 * kVec * 32 + lane;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) {
+                    if (n.has0)
+                        copy16(to + k * 32, row + n.off0 + k * 4);
+                    if (n.has1)
+                        copy16(to + (kVec + k) * 32, row + n.off1 + k * 4);
+                }
+            }
+            if (f.h == f.h0 && a.R) {
+                const int pos = positions.get(a, f.n, first, step, items, chunks);
+                const uint32_t bit = 1u << (f.n % 32);
+                bad_bits = pos < 0 ? bad_bits | bit : bad_bits & ~bit;
+                if (pos >= 0) {
+                    const float *row = a.table + int64_t(pos) * a.R;
+                    float *to = angles + (f.n % kDepth) * G * 16;
+                    for (int i = lane; i < a.R / 4; i += 32)
+                        copy16(to + 4 * i, row + 4 * i);
+                }
+            }
+            f.h += kRows;
+            if (f.h >= f.h1) {
+                f.item += step;
+                ++f.n;
+                if (f.item < items)
+                    enter<T>(f, heads, per_item, chunks);
+            }
+        }
+        copies_end();
+        slot_f = slot_f + 1 == kDepth ? 0 : slot_f + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kDepth - 1; ++i)
+        fetch();
+
+    int slot = 0;
+    int64_t count = 0;
+    for (int64_t item = first; item < items; item += step, ++count) {
+        Cursor c = {count, item, 0, 0, 0, 0};
+        enter<T>(c, heads, per_item, chunks);
+        f32x2 c2[8], s2[8];
+        int is_k = -1;
+        for (; c.h < c.h1; c.h += kRows) {
+            copies_wait<kDepth - 2>();
+            __syncwarp();
+            const int h = c.h + g;
+            const bool on = h < c.h1;
+            const int k = h >= hq;
+            const Part<T> &p = a.part[k];
+            if (on && k != is_k) {  // a token's first queries, or keys: angles and weight into factors
+                is_k = k;
+                angle_factors<IL, false>(angles + (count % kDepth) * G * 16, a.R, n, bad_bits >> (count % 32) & 1, c2,
+                                         s2);
+                if (p.w) {
+                    f32x2 w[8];
+                    load_weight(p.w, n, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        c2[i] = n.rot ? mul2(c2[i], w[i]) : w[i];
+                        s2[i] = mul2(s2[i], partner<IL>(w, i));
+                    }
+                }
+            }
+            f32x2 v[8], y[8];
+            unpack8(ring + slot * 2 * kVec * 32 + lane, 32, v, static_cast<const T *>(nullptr));
+            unpack8(ring + (slot * 2 + 1) * kVec * 32 + lane, 32, v + 4, static_cast<const T *>(nullptr));
+            if (!on || !n.has0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = 0;
+            }
+            if (!on || !n.has1) {
+#pragma unroll
+                for (int i = 4; i < 8; ++i)
+                    v[i] = 0;
+            }
+            const float r = inv_rms<G>(v, inv_d, a.eps);
+            if (n.rot) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = fma2(v[i], c2[i], mul2(partner<IL>(v, i), s2[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = p.w ? mul2(v[i], c2[i]) : v[i];
+            }
+            if (p.w) {
+                const f32x2 r2 = pair(r, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = mul2(y[i], r2);
+            }
+            if (on)
+                store_unit(p.out.row(c.t, k ? h - hq : h), n, y);
+            __syncwarp();
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+            fetch();
+        }
+    }
+    copies_wait<0>();
+}
+
+template <typename T, int G, bool IL>
+__global__ void __launch_bounds__(kThreads, 2) qk_backward_kernel(const QkArgs<T> a)
 {
     constexpr int kRows = 32 / G;
-    __shared__ float sums[kThreads / G][16 * G];
-    const int lane = threadIdx.x & 31, g = lane / G, u = lane % G;
-    const Unit n = unit_of<IL>(u, a.D, a.R);
+    constexpr int kVec = sizeof(T) / 2;
+    extern __shared__ uint4 smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
+    uint4 *ring = smem + warp * (ring_bytes<T>(2, G) / 16);
+    float *angles = reinterpret_cast<float *>(ring + kDepth * 4 * kVec * 32);
+    const Unit n = unit_of<IL>(lane % G, a.D, a.R);
+    const float inv_d = 1.f / float(a.D);
     const int which = int(blockIdx.x) >= a.part[0].blocks;
     const Part<T> &p = a.part[which];
     const int block = int(blockIdx.x) - (which ? a.part[0].blocks : 0);
-    const int chunks = (p.heads + p.heads_per_item - 1) / p.heads_per_item;
+    const int heads = p.heads, per_item = p.heads_per_item, chunks = (heads + per_item - 1) / per_item;
+    const int64_t items = p.items;
+    const int64_t first = int64_t(block) * kWarps + warp, step = int64_t(p.blocks) * kWarps;
 
-    float w[16], acc[16];
+    f32x2 w[8], acc[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        acc[i] = 0.f;
+    for (int i = 0; i < 8; ++i)
+        acc[i] = 0;
     if (p.w)
-        load_unit(p.w, n, true, w);
-    for (int64_t item = int64_t(block) * kWarps + (threadIdx.x >> 5); item < p.items;
-         item += int64_t(p.blocks) * kWarps) {
-        const int64_t t = item / chunks;
-        const int h0 = int(item - t * chunks) * p.heads_per_item;
-        const int h1 = min(p.heads, h0 + p.heads_per_item);
-        float c[8], s[8];
-        load_angles(a, t, n, c, s);
-        for (int hb = h0; hb < h1; hb += kRows) {
-            const int h = hb + g;
-            float d[16], x[16];
-            load_unit(p.d.row(t, h), n, h < h1, d);
-            if (p.w)
-                load_unit(p.x.row(t, h), n, h < h1, x);
-            if (n.rot)
-                rotate<IL, true>(d, c, s);
-            if (p.w) {
-                const float r = inv_rms<G>(x, a.D, a.eps);
-                float m = 0.f;
-                if (h >= h1) {  // an idle group's gradient is 0, even where its token's angles are NaN
+        load_weight(p.w, n, w);
+    Positions<T> positions;
+    positions.start(a, first, step, items, chunks);
+    Cursor f = {0, first, 0, 0, 0, 0};
+    enter<T>(f, heads, per_item, chunks);
+    int slot_f = 0, bad_bits = 0;
+    auto fetch = [&] {
+        if (f.item < items) {
+            const int h = f.h + g;
+            if (h < f.h1) {
+                uint4 *to = ring + slot_f * 4 * kVec * 32 + lane;
+                const T *row = p.d.row(f.t, h);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        d[i] = x[i] = 0.f;
+                for (int k = 0; k < kVec; ++k) {
+                    if (n.has0)
+                        copy16(to + k * 32, row + n.off0 + k * 4);
+                    if (n.has1)
+                        copy16(to + (kVec + k) * 32, row + n.off1 + k * 4);
                 }
+                if (p.w) {
+                    row = p.x.row(f.t, h);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[i] *= h < h1 ? r : 0.f;
-                    acc[i] = __fmaf_rn(d[i], x[i], acc[i]);
-                    d[i] *= w[i];
-                    m = __fmaf_rn(d[i], x[i], m);
+                    for (int k = 0; k < kVec; ++k) {
+                        if (n.has0)
+                            copy16(to + (2 * kVec + k) * 32, row + n.off0 + k * 4);
+                        if (n.has1)
+                            copy16(to + (3 * kVec + k) * 32, row + n.off1 + k * 4);
+                    }
                 }
-                m = __fdividef(group_sum<G>(m), float(a.D));
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    d[i] = r * __fmaf_rn(-x[i], m, d[i]);
             }
-            store_unit(p.out.row(t, h), n, h < h1, d);
+            if (f.h == f.h0 && a.R) {
+                const int pos = positions.get(a, f.n, first, step, items, chunks);
+                const uint32_t bit = 1u << (f.n % 32);
+                bad_bits = pos < 0 ? bad_bits | bit : bad_bits & ~bit;
+                if (pos >= 0) {
+                    const float *row = a.table + int64_t(pos) * a.R;
+                    float *to = angles + (f.n % kDepth) * G * 16;
+                    for (int i = lane; i < a.R / 4; i += 32)
+                        copy16(to + 4 * i, row + 4 * i);
+                }
+            }
+            f.h += kRows;
+            if (f.h >= f.h1) {
+                f.item += step;
+                ++f.n;
+                if (f.item < items)
+                    enter<T>(f, heads, per_item, chunks);
+            }
+        }
+        copies_end();
+        slot_f = slot_f + 1 == kDepth ? 0 : slot_f + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < kDepth - 1; ++i)
+        fetch();
+
+    int slot = 0;
+    int64_t count = 0;
+    for (int64_t item = first; item < items; item += step, ++count) {
+        Cursor c = {count, item, 0, 0, 0, 0};
+        enter<T>(c, heads, per_item, chunks);
+        f32x2 c2[8], s2[8];
+        for (; c.h < c.h1; c.h += kRows) {
+            copies_wait<kDepth - 2>();
+            __syncwarp();
+            if (c.h == c.h0)
+                angle_factors<IL, true>(angles + (count % kDepth) * G * 16, a.R, n, bad_bits >> (count % 32) & 1, c2,
+                                        s2);
+            const int h = c.h + g;
+            const bool on = h < c.h1;
+            const uint4 *from = ring + slot * 4 * kVec * 32 + lane;
+            f32x2 d[8], y[8];
+            unpack8(from, 32, d, static_cast<const T *>(nullptr));
+            unpack8(from + kVec * 32, 32, d + 4, static_cast<const T *>(nullptr));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = n.rot ? fma2(d[i], c2[i], mul2(partner<IL>(d, i), s2[i])) : d[i];
+            if (p.w) {
+                f32x2 x[8];
+                unpack8(from + 2 * kVec * 32, 32, x, static_cast<const T *>(nullptr));
+                unpack8(from + 3 * kVec * 32, 32, x + 4, static_cast<const T *>(nullptr));
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!on || !(i < 4 ? n.has0 : n.has1))
+                        x[i] = y[i] = 0;
+                const float r = inv_rms<G>(x, inv_d, a.eps);
+                const f32x2 r2 = pair(r, r);
+                f32x2 m2 = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = mul2(x[i], r2);
+                    acc[i] = fma2(y[i], x[i], acc[i]);
+                    y[i] = mul2(y[i], w[i]);
+                    m2 = fma2(y[i], x[i], m2);
+                }
+                const float m = -group_sum<G>(lo_of(m2) + hi_of(m2)) * inv_d;
+                m2 = pair(m, m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y[i] = mul2(fma2(x[i], m2, y[i]), r2);
+            }
+            if (on)
+                store_unit(p.out.row(c.t, h), n, y);
+            __syncwarp();
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+            fetch();
         }
     }
+    copies_wait<0>();
     if (!p.w)
         return;
-    const int row = (threadIdx.x >> 5) * kRows + g;
+    __syncthreads();  // the ring is free: the lanes' sums go through it
+    float *sums = reinterpret_cast<float *>(smem);
+    const int row = warp * kRows + g;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (n.has0)
-            sums[row][n.off0 + i] = acc[i];
-        if (n.has1)
-            sums[row][n.off1 + i] = acc[8 + i];
+        const int off = i < 4 ? n.off0 + 2 * i : n.off1 + 2 * (i - 4);
+        if (i < 4 ? n.has0 : n.has1) {
+            sums[row * 16 * G + off] = lo_of(acc[i]);
+            sums[row * 16 * G + off + 1] = hi_of(acc[i]);
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.D; i += kThreads) {
         float x = 0.f;
         for (int k = 0; k < kThreads / G; ++k)
-            x += sums[k][i];
+            x += sums[k * 16 * G + i];
         p.partial[int64_t(block) * a.D + i] = x;
     }
 }
@@ -478,8 +763,8 @@ tide_status_t check_desc(const tide_qk_t *qk)
     if (qk->rotary_dim > 0 && qk->tokens > 0) {
         if (qk->position_bytes != 4 && qk->position_bytes != 8)
             return op_fail(TIDE_ERR_INVALID_ARG, "position_bytes %d: need 4 or 8", qk->position_bytes);
-        if (!qk->table || !qk->positions || qk->max_position < 1 || qk->max_position > tide::kMaxExtent / kMaxHeadDim)
-            return op_fail(TIDE_ERR_INVALID_ARG, "a rotation needs a table, positions and max_position >= 1");
+        if (!qk->table || !qk->positions || qk->max_position < 1 || qk->max_position > 0x7fffffff)
+            return op_fail(TIDE_ERR_INVALID_ARG, "a rotation needs a table, positions and max_position in [1, 2^31)");
         if (!op_aligned(qk->table, 4) || !op_aligned(qk->positions, size_t(qk->position_bytes)))
             return op_fail(TIDE_ERR_ALIGNMENT, "table or positions not aligned to their element size");
     }
@@ -548,16 +833,25 @@ Heads<T> heads_of(const tide_heads_t *x)
     return x ? Heads<T>{static_cast<T *>(x->data), x->token_stride, x->head_stride} : Heads<T>{nullptr, 0, 0};
 }
 
-// Blocks of the backward for queries and for keys: four a SM, shared by heads.
+// Heads of one warp's item: all of a token, or whole steps of fewer where that
+// leaves warps without an item.
+int heads_per_item(int heads, int rows, int64_t tokens, int64_t warps)
+{
+    const int64_t steps = (heads + rows - 1) / rows, want = std::max<int64_t>(1, warps / std::max<int64_t>(tokens, 1));
+    return int((steps + std::min(steps, want) - 1) / std::min(steps, want)) * rows;
+}
+
+// Blocks of the backward for queries and for keys: two a SM, shared by heads.
 void grad_blocks(const tide_qk_t *qk, int sms, int *q, int *k)
 {
-    const int64_t all = int64_t(sms) * 4, heads = int64_t(qk->q_heads) + qk->k_heads;
+    const int64_t all = int64_t(sms) * 2, heads = int64_t(qk->q_heads) + qk->k_heads;
     int64_t nq = heads ? (all * qk->q_heads + heads - 1) / heads : 0;
     int64_t nk = all - nq;
     if (qk->k_heads > 0 && nk < 1)
         nk = 1;
-    *q = int(qk->q_heads > 0 ? std::min(nq, qk->tokens * qk->q_heads) : 0);
-    *k = int(qk->k_heads > 0 ? std::min(nk, qk->tokens * qk->k_heads) : 0);
+    // a block that gets a step of at least one of its warps
+    *q = int(qk->q_heads > 0 ? std::min(nq, (qk->tokens * qk->q_heads + kWarps - 1) / kWarps) : 0);
+    *k = int(qk->k_heads > 0 ? std::min(nk, (qk->tokens * qk->k_heads + kWarps - 1) / kWarps) : 0);
 }
 
 template <typename T>
@@ -579,21 +873,30 @@ QkArgs<T> make_args(const tide_qk_t *qk)
     return a;
 }
 
-template <typename T, int G>
-void launch_forward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
+// Starts a vector kernel with its rings, after letting it have them (once for
+// each kernel and device).
+template <typename K, typename T>
+tide_status_t launch_vec(K kernel, const QkArgs<T> &a, unsigned grid, int smem, const char *what, cudaStream_t st)
 {
-    if (il)
-        qk_forward_kernel<T, G, true><<<grid, kThreads, 0, st>>>(a);
-    else
-        qk_forward_kernel<T, G, false><<<grid, kThreads, 0, st>>>(a);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    kernel<<<grid, kThreads, size_t(smem), st>>>(a);
+    return tide::op_launched(what);
 }
 template <typename T, int G>
-void launch_backward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
+tide_status_t launch_forward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
 {
-    if (il)
-        qk_backward_kernel<T, G, true><<<grid, kThreads, 0, st>>>(a);
-    else
-        qk_backward_kernel<T, G, false><<<grid, kThreads, 0, st>>>(a);
+    constexpr int smem = kWarps * ring_bytes<T>(1, G);
+    return il ? launch_vec(qk_forward_kernel<T, G, true>, a, grid, smem, "qk_norm_rope", st)
+              : launch_vec(qk_forward_kernel<T, G, false>, a, grid, smem, "qk_norm_rope", st);
+}
+template <typename T, int G>
+tide_status_t launch_backward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
+{
+    constexpr int smem = std::max(kWarps * ring_bytes<T>(2, G), kThreads * 16 * 4);
+    return il ? launch_vec(qk_backward_kernel<T, G, true>, a, grid, smem, "qk_norm_rope_grad", st)
+              : launch_vec(qk_backward_kernel<T, G, false>, a, grid, smem, "qk_norm_rope_grad", st);
 }
 
 template <typename T, bool GRAD>
@@ -631,20 +934,18 @@ tide_status_t forward(const tide_qk_t *qk, const tide_heads_t *q, const tide_hea
         launch_generic<T, false>(a, qk->interleaved, st);
         return tide::op_launched("qk_norm_rope");
     }
-    const int g = lanes_of(qk);
-    for (Part<T> &p : a.part) {
-        // All heads of a token in one warp reuse its angles; few tokens are spread over more warps instead.
-        p.heads_per_item = qk->tokens >= 4096 ? std::max(p.heads, 1) : 32 / g;
-        p.items = qk->tokens * ((p.heads + p.heads_per_item - 1) / p.heads_per_item);
-    }
-    const unsigned grid = unsigned((a.part[0].items + a.part[1].items + kWarps - 1) / kWarps);
+    // All heads of a token in one warp reuse its angles; few tokens are spread over more warps instead.
+    const int g = lanes_of(qk), heads = qk->q_heads + qk->k_heads, rows = 32 / g;
+    const int64_t blocks = int64_t(tide::op_sm_count()) * 2;
+    a.heads_per_item = heads_per_item(heads, rows, qk->tokens, blocks * kWarps);
+    const int64_t items = qk->tokens * ((heads + a.heads_per_item - 1) / a.heads_per_item);
+    const unsigned grid = unsigned(std::min((items + kWarps - 1) / kWarps, blocks));
     switch (g) {
-    case 4: launch_forward<T, 4>(a, qk->interleaved, grid, st); break;
-    case 8: launch_forward<T, 8>(a, qk->interleaved, grid, st); break;
-    case 16: launch_forward<T, 16>(a, qk->interleaved, grid, st); break;
-    default: launch_forward<T, 32>(a, qk->interleaved, grid, st); break;
+    case 4: return launch_forward<T, 4>(a, qk->interleaved, grid, st);
+    case 8: return launch_forward<T, 8>(a, qk->interleaved, grid, st);
+    case 16: return launch_forward<T, 16>(a, qk->interleaved, grid, st);
+    default: return launch_forward<T, 32>(a, qk->interleaved, grid, st);
     }
-    return tide::op_launched("qk_norm_rope");
 }
 
 template <typename T>
@@ -670,24 +971,27 @@ tide_status_t backward(const tide_qk_t *qk, const tide_heads_t *dqo, const tide_
     if (!vec) {
         for (Part<T> &p : a.part)
             p.items = qk->tokens * p.heads;
-        if (grid)
+        if (grid) {
             launch_generic<T, true>(a, qk->interleaved, st);
+            if (const tide_status_t s = tide::op_launched("qk_norm_rope_grad"))
+                return s;
+        }
     } else if (grid) {
         const int g = lanes_of(qk);
         for (Part<T> &p : a.part) {
-            p.heads_per_item = qk->tokens >= 4096 ? std::max(p.heads, 1) : 32 / g;
+            p.heads_per_item = heads_per_item(std::max(p.heads, 1), 32 / g, qk->tokens, int64_t(p.blocks) * kWarps);
             p.items = qk->tokens * ((p.heads + p.heads_per_item - 1) / p.heads_per_item);
         }
+        tide_status_t s = TIDE_OK;
         switch (g) {
-        case 4: launch_backward<T, 4>(a, qk->interleaved, grid, st); break;
-        case 8: launch_backward<T, 8>(a, qk->interleaved, grid, st); break;
-        case 16: launch_backward<T, 16>(a, qk->interleaved, grid, st); break;
-        default: launch_backward<T, 32>(a, qk->interleaved, grid, st); break;
+        case 4: s = launch_backward<T, 4>(a, qk->interleaved, grid, st); break;
+        case 8: s = launch_backward<T, 8>(a, qk->interleaved, grid, st); break;
+        case 16: s = launch_backward<T, 16>(a, qk->interleaved, grid, st); break;
+        default: s = launch_backward<T, 32>(a, qk->interleaved, grid, st); break;
         }
-    }
-    if (grid)
-        if (const tide_status_t s = tide::op_launched("qk_norm_rope_grad"))
+        if (s)
             return s;
+    }
     if (!dwq && !dwk)
         return TIDE_OK;
     qk_weight_grad_kernel<T><<<dim3(unsigned((a.D + 31) / 32), 2), dim3(32, 32), 0, st>>>(
@@ -750,6 +1054,8 @@ int64_t tide_qk_norm_rope_grad_workspace(const tide_qk_t *qk)
     tide::record_error("");
     if (check_desc(qk))
         return -1;
+    if (!qk->q_weight && !qk->k_weight)
+        return 0;
     int nq, nk;
     grad_blocks(qk, tide::op_sm_count(), &nq, &nk);
     return std::max<int64_t>(256, (int64_t(nq) + nk) * qk->head_dim * 4);
@@ -781,9 +1087,10 @@ tide_status_t tide_qk_norm_rope_grad(const tide_qk_t *qk, const tide_heads_t *dq
     if ((dq_weight && !op_aligned(dq_weight, elem_bytes(qk->dtype))) ||
         (dk_weight && !op_aligned(dk_weight, elem_bytes(qk->dtype))))
         return op_fail(TIDE_ERR_ALIGNMENT, "a weight's gradient is not aligned to its element size");
-    if (workspace_bytes < tide_qk_norm_rope_grad_workspace(qk) || !workspace)
+    const int64_t need = tide_qk_norm_rope_grad_workspace(qk);
+    if (workspace_bytes < need || (need && !workspace))
         return op_fail(TIDE_ERR_INVALID_ARG, "workspace of %lld bytes: need %lld", (long long)workspace_bytes,
-                       (long long)tide_qk_norm_rope_grad_workspace(qk));
+                       (long long)need);
     if (!op_aligned(workspace, 256))
         return op_fail(TIDE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
     const tide::NvtxRange range("tide_qk_norm_rope_grad");

@@ -51,53 +51,59 @@ __device__ __forceinline__ float sigmoid(float g)
 template <bool VEC, typename T>
 __device__ __forceinline__ void load_cols(const T *row, int64_t c, int64_t cols, float (&v)[8])
 {
-    if (VEC) {
-        if (c < cols) {
-            load8(row + c, v);
-            return;
-        }
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        v[i] = !VEC && c + i < cols ? to_f32(row[c + i]) : 0.f;
+        v[i] = 0.f;
+    if constexpr (VEC) {
+        if (c < cols)
+            load8(row + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                v[i] = to_f32(row[c + i]);
+    }
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_cols(T *row, int64_t c, int64_t cols, const float (&v)[8])
 {
-    if (VEC) {
+    if constexpr (VEC) {
         if (c < cols)
             store8(row + c, v);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            row[c + i] = from_f32<T>(v[i]);
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                row[c + i] = from_f32<T>(v[i]);
+    }
 }
 template <bool VEC>
 __device__ __forceinline__ uint2 load_codes(const uint8_t *row, int64_t c, int64_t cols)
 {
-    if (VEC)
-        return c < cols ? *reinterpret_cast<const uint2 *>(row + c) : make_uint2(0, 0);
     uint32_t w[2] = {0, 0};
+    if constexpr (VEC) {
+        if (c < cols)
+            return *reinterpret_cast<const uint2 *>(row + c);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            w[i / 4] |= uint32_t(row[c + i]) << (8 * (i % 4));
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                w[i / 4] |= uint32_t(row[c + i]) << (8 * (i % 4));
+    }
     return make_uint2(w[0], w[1]);
 }
 template <bool VEC>
 __device__ __forceinline__ void store_codes(uint8_t *row, int64_t c, int64_t cols, uint2 q)
 {
-    if (VEC) {
+    if constexpr (VEC) {
         if (c < cols)
             *reinterpret_cast<uint2 *>(row + c) = q;
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols)
-            row[c + i] = uint8_t((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols)
+                row[c + i] = uint8_t((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+    }
 }
 
 // Codes of a lane's eight values and the exponent of their block (16 lanes).

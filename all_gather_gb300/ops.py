@@ -15,7 +15,6 @@ can be written straight into a gradient arena with ``out``.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple, Optional
 
 import torch
@@ -25,41 +24,48 @@ from . import _binding as _b
 _DTYPES = {torch.bfloat16: _b.TIDE_DTYPE_BF16, torch.float32: _b.TIDE_DTYPE_F32}
 _INT_BYTES = {torch.int32: 4, torch.int64: 8}
 ROPE_SCALINGS = {None: 0, "linear": 1, "by_parts": 2}
+_BF16, _F32 = torch.bfloat16, torch.float32
+_raw_stream, _current_device, _empty = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty
+
+# These wrappers run once for every layer and token, in front of kernels of a
+# few microseconds: each attribute is read once, checks are plain comparisons,
+# and names that only an error needs are put together there.
 
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _dtype(t, name):
-    dt = _DTYPES.get(t.dtype)
+def _dtype(dtype, name):
+    dt = _DTYPES.get(dtype)
     if dt is None:
-        raise TypeError(f"{name} is {t.dtype}: need bfloat16 or float32")
+        raise TypeError(f"{name} is {dtype}: need bfloat16 or float32")
     return dt
 
 
-def _on_device(t, name):
-    if not t.is_cuda:
+def _device(t, name) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} is not on a CUDA device")
+    return dev
 
 
-def _like(t, ref, shape, name):
-    """Checks an output or companion tensor: ref's type and device, this shape, contiguous rows."""
-    if t.dtype != ref.dtype or t.device != ref.device:
-        raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {ref.dtype} on {ref.device}")
-    if tuple(t.shape) != tuple(shape):
+def _like(t, dtype, dev, shape, name):
+    """Refuses a tensor that is not of this type, device and shape."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on CUDA device {dev}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} has no contiguous last dimension")
 
 
-def _workspace(n: int, workspace, device):
-    """(tensor that keeps it alive, pointer, bytes) of scratch memory."""
+def _scratch(n: int, workspace, device):
+    """Scratch memory: (tensor that keeps it alive, pointer, bytes)."""
     if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+        workspace = _empty(n, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), n
+    if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -84,35 +90,46 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
 
 
 def _heads(t, name):
-    if t.dim() != 3:
+    """A tensor of heads, with the dtype, device and shape already checked where it has to agree with another."""
+    st = t.stride()
+    if len(st) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if t.stride(2) != 1 and t.shape[2] > 1:
+    if st[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} has no contiguous last dimension")
-    return _b.Heads(t.data_ptr(), t.stride(0), t.stride(1))
+    return _b.Heads(t.data_ptr(), st[0], st[1])
 
 
 def _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved):
-    dt = _dtype(q, "q")
-    _on_device(q, "q")
-    T, Hq, D = q.shape
-    if k.dtype != q.dtype or k.device != q.device or k.shape[0] != T or k.shape[2] != D:
+    """(descriptor, device, q's shape, k's shape)."""
+    dtype, dev, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
+    dt = _dtype(dtype, "q")
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    T, Hq, D = qs
+    if k.dtype is not dtype or k.get_device() != dev or ks[0] != T or ks[2] != D:
         raise ValueError("q and k must agree in type, device, tokens and head_dim")
-    R = 0
+    if dev < 0:
+        raise ValueError("q is not on a CUDA device")
+    R = P = tp = pp = 0
+    pos_bytes = 8
     if table is not None:
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.device != q.device:
+        if table.dtype is not _F32 or table.get_device() != dev or table.dim() != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous float32 tensor [positions, rotary_dim] on q's device")
-        R = table.shape[1]
-        if positions is None or positions.dtype not in _INT_BYTES or positions.device != q.device:
+        P, R = table.shape
+        pos_bytes = _INT_BYTES.get(positions.dtype, 0) if positions is not None else 0
+        if not pos_bytes or positions.get_device() != dev:
             raise ValueError("positions must be an int32 or int64 tensor on q's device")
-        if tuple(positions.shape) != (T,) or (T > 1 and positions.stride(0) != 1):
+        if positions.shape != (T,) or not positions.is_contiguous():
             raise ValueError(f"positions must be contiguous of shape ({T},)")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, q, (D,), name)
-    return _b.QkDesc(T, Hq, k.shape[1], D, R, table.shape[0] if R else 0, table.data_ptr() if R else None,
-                     positions.data_ptr() if R else None, _INT_BYTES[positions.dtype] if R else 8, dt,
-                     int(bool(interleaved)), eps, None if q_weight is None else q_weight.data_ptr(),
-                     None if k_weight is None else k_weight.data_ptr())
+        tp, pp = table.data_ptr(), positions.data_ptr()
+    wq = wk = None
+    if q_weight is not None:
+        _like(q_weight, dtype, dev, (D,), "q_weight")
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _like(k_weight, dtype, dev, (D,), "k_weight")
+        wk = k_weight.data_ptr()
+    return _b.QkDesc(T, Hq, ks[1], D, R, P, tp, pp, pos_bytes, dt, 1 if interleaved else 0, eps, wq, wk), dev, qs, ks
 
 
 def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -121,14 +138,13 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     their first ``table.shape[1]`` columns rotated by the angles of ``positions`` [T] (where a table is given).
     ``out = (q_out, k_out)`` may be (q, k) themselves."""
     qh, kh = _heads(q, "q"), _heads(k, "k")
-    desc = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
+    desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     if out is None:
-        q_out, k_out = torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype,
-                                                                                         device=k.device)
+        q_out, k_out = q.new_empty(qs), k.new_empty(ks)
     else:
         q_out, k_out = out
-        _like(q_out, q, q.shape, "q_out")
-        _like(k_out, k, k.shape, "k_out")
+        _like(q_out, q.dtype, dev, qs, "q_out")
+        _like(k_out, q.dtype, dev, ks, "k_out")
     _b.tide_qk_norm_rope(desc, qh, kh, _heads(q_out, "q_out"), _heads(k_out, "k_out"), _stream(stream))
     return q_out, k_out
 
@@ -137,27 +153,29 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
                       eps: float = 1e-6, interleaved: bool = False, out=None, workspace=None, stream=None):
     """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` from its outputs' gradients and its inputs.  A weight
     that is None has no gradient (None), and its ``q`` or ``k`` is used for its shape only."""
-    desc = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
-    _like(dq_out, q, q.shape, "dq_out")
-    _like(dk_out, k, k.shape, "dk_out")
+    desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
+    dtype = q.dtype
+    _like(dq_out, dtype, dev, qs, "dq_out")
+    _like(dk_out, dtype, dev, ks, "dk_out")
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype,
-                                                                                device=k.device),
-               None if q_weight is None else torch.empty_like(q_weight),
-               None if k_weight is None else torch.empty_like(k_weight))
+        dq, dk = q.new_empty(qs), k.new_empty(ks)
+        dqw = None if q_weight is None else q.new_empty(qs[2])
+        dkw = None if k_weight is None else k.new_empty(qs[2])
     else:
-        _like(out[0], q, q.shape, "dq")
-        _like(out[1], k, k.shape, "dk")
-        for w, d, name in ((q_weight, out[2], "dq_weight"), (k_weight, out[3], "dk_weight")):
+        dq, dk, dqw, dkw = out
+        _like(dq, dtype, dev, qs, "dq")
+        _like(dk, dtype, dev, ks, "dk")
+        for w, d, name in ((q_weight, dqw, "dq_weight"), (k_weight, dkw, "dk_weight")):
             if (w is None) != (d is None):
                 raise ValueError(f"{name} goes with its weight: both or neither")
             if w is not None:
-                _like(d, w, w.shape, name)
-    dq, dk, dqw, dkw = out
-    _keep, ws, n = _workspace(_b.tide_qk_norm_rope_grad_workspace(desc), workspace, q.device)
+                _like(d, dtype, dev, (qs[2],), name)
+    ws = n = 0
+    if q_weight is not None or k_weight is not None or workspace is not None:
+        _keep, ws, n = _scratch(_b.tide_qk_norm_rope_grad_workspace(desc), workspace, q.device)
     _b.tide_qk_norm_rope_grad(desc, _heads(dq_out, "dq_out"), _heads(dk_out, "dk_out"),
-                              _heads(q, "q") if q_weight is not None else None,
-                              _heads(k, "k") if k_weight is not None else None, _heads(dq, "dq"), _heads(dk, "dk"),
+                              None if q_weight is None else _heads(q, "q"),
+                              None if k_weight is None else _heads(k, "k"), _heads(dq, "dq"), _heads(dk, "dk"),
                               0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(), ws, n,
                               _stream(stream))
     return dq, dk, dqw, dkw
@@ -166,41 +184,50 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
 # ------------------------------------------------------------------ vocabulary head with cross entropy
 
 def _ce_desc(x, weight, targets, ignore_index):
-    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+    """(descriptor, device, tokens)."""
+    if x.dtype is not _BF16 or weight.dtype is not _BF16:
         raise TypeError(f"x is {x.dtype} and weight {weight.dtype}: need bfloat16")
-    _on_device(x, "x")
-    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
+    dev, xs, ws = _device(x, "x"), x.shape, weight.shape
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
         raise ValueError("need x [tokens, hidden] and weight [vocab, hidden]")
-    for t, name in ((x, "x"), (weight, "weight")):
-        if t.stride(1) != 1 and t.shape[1] > 1:
-            raise ValueError(f"{name} has no contiguous last dimension")
-    if targets.dtype not in _INT_BYTES or tuple(targets.shape) != (x.shape[0],):
-        raise ValueError("targets must be an int32 or int64 tensor [tokens]")
-    if targets.shape[0] > 1 and targets.stride(0) != 1:
-        raise ValueError("targets must be contiguous")
-    if weight.device != x.device or targets.device != x.device:
+    T, H = xs
+    xt, wt = x.stride(), weight.stride()
+    if H > 1 and (xt[1] != 1 or wt[1] != 1):
+        raise ValueError("x or weight has no contiguous last dimension")
+    target_bytes = _INT_BYTES.get(targets.dtype)
+    if target_bytes is None or targets.shape != (T,) or not targets.is_contiguous():
+        raise ValueError("targets must be a contiguous int32 or int64 tensor [tokens]")
+    if weight.get_device() != dev or targets.get_device() != dev:
         raise ValueError("x, weight and targets must be on one device")
-    return _b.CeDesc(x.shape[0], weight.shape[0], x.shape[1], x.data_ptr(), x.stride(0), weight.data_ptr(),
-                     weight.stride(0), targets.data_ptr(), _INT_BYTES[targets.dtype], ignore_index)
+    return _b.CeDesc(T, ws[0], H, x.data_ptr(), xt[0], weight.data_ptr(), wt[0], targets.data_ptr(), target_bytes,
+                     ignore_index), dev, T
 
 
-def _per_token(t, x, name):
-    if t.dtype != torch.float32 or t.device != x.device or tuple(t.shape) != (x.shape[0],) or not t.is_contiguous():
+def _per_token(t, dev, T, name):
+    if t.dtype is not _F32 or t.get_device() != dev or t.shape != (T,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor [tokens] on x's device")
+
+
+def _rows(t, name) -> int:
+    """Row stride of a matrix with contiguous rows."""
+    st = t.stride()
+    if len(st) != 2 or (st[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be [rows, cols] with contiguous rows")
+    return st[0]
 
 
 def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None, workspace=None, stream=None):
     """(loss, lse), both fp32 [T]: every token's cross entropy of the logits ``x @ weight.T`` (x [T, H], weight
     [V, H], bf16) and the log of its sum of exponentials, which :func:`linear_cross_entropy_grad` takes.  The logits
     are not written to memory.  An ignored token's loss is 0."""
-    desc = _ce_desc(x, weight, targets, ignore_index)
+    desc, dev, T = _ce_desc(x, weight, targets, ignore_index)
     if out is None:
-        loss, lse = torch.empty((2, x.shape[0]), dtype=torch.float32, device=x.device)
+        loss, lse = _empty(T, dtype=_F32, device=x.device), _empty(T, dtype=_F32, device=x.device)
     else:
         loss, lse = out
-        _per_token(loss, x, "loss")
-        _per_token(lse, x, "lse")
-    _keep, ws, n = _workspace(_b.tide_ce_loss_workspace(desc), workspace, x.device)
+        _per_token(loss, dev, T, "loss")
+        _per_token(lse, dev, T, "lse")
+    _keep, ws, n = _scratch(_b.tide_ce_loss_workspace(desc), workspace, x.device)
     _b.tide_ce_loss(desc, loss.data_ptr(), lse.data_ptr(), ws, n, _stream(stream))
     return loss, lse
 
@@ -209,19 +236,18 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
                               stream=None):
     """(dx, dweight) of :func:`linear_cross_entropy` from its lse and the gradient ``dloss`` (fp32 [T]) of its losses
     (the mean over n tokens: 1 / n everywhere).  bf16, like x and weight."""
-    desc = _ce_desc(x, weight, targets, ignore_index)
-    _per_token(lse, x, "lse")
-    _per_token(dloss, x, "dloss")
+    desc, dev, T = _ce_desc(x, weight, targets, ignore_index)
+    _per_token(lse, dev, T, "lse")
+    _per_token(dloss, dev, T, "dloss")
     if out is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(weight.shape, dtype=weight.dtype, device=x.device)
+        dx, dw = x.new_empty(x.shape), weight.new_empty(weight.shape)
     else:
         dx, dw = out
-        _like(dx, x, x.shape, "dx")
-        _like(dw, weight, weight.shape, "dweight")
-    _keep, ws, n = _workspace(_b.tide_ce_grad_workspace(desc), workspace, x.device)
-    _b.tide_ce_grad(desc, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), dx.stride(0), dw.data_ptr(), dw.stride(0),
-                    ws, n, _stream(stream))
+        _like(dx, _BF16, dev, x.shape, "dx")
+        _like(dw, _BF16, dev, weight.shape, "dweight")
+    _keep, ws, n = _scratch(_b.tide_ce_grad_workspace(desc), workspace, x.device)
+    _b.tide_ce_grad(desc, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), _rows(dx, "dx"), dw.data_ptr(),
+                    _rows(dw, "dweight"), ws, n, _stream(stream))
     return dx, dw
 
 
@@ -236,63 +262,64 @@ class Ckpt8(NamedTuple):
     up_exps: torch.Tensor
 
 
-def _ckpt_desc(ckpt, rows, cols, device):
-    blocks = -(-cols // 128)
-    for t, dt, w in ((ckpt[0], torch.float8_e4m3fn, cols), (ckpt[1], torch.uint8, blocks),
-                     (ckpt[2], torch.float8_e4m3fn, cols), (ckpt[3], torch.uint8, blocks)):
-        if t.dtype != dt or tuple(t.shape) != (rows, w) or not t.is_contiguous() or t.device != device:
+_E4M3, _U8 = torch.float8_e4m3fn, torch.uint8
+
+
+def _ckpt_desc(ckpt, rows, cols, dev):
+    codes, exps = (rows, cols), (rows, -(-cols // 128))
+    g8, ge, u8, ue = ckpt
+    for t, dt, shape in ((g8, _E4M3, codes), (ge, _U8, exps), (u8, _E4M3, codes), (ue, _U8, exps)):
+        if t.dtype is not dt or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"a checkpoint tensor is {t.dtype} {tuple(t.shape)} on {t.device}: need contiguous {dt} "
-                             f"({rows}, {w}) on {device}")
-    return _b.Ckpt8Desc(*[t.data_ptr() for t in ckpt])
+                             f"{shape} on CUDA device {dev}")
+    return _b.Ckpt8Desc(g8.data_ptr(), ge.data_ptr(), u8.data_ptr(), ue.data_ptr())
 
 
 def new_ckpt8(rows: int, cols: int, device="cuda") -> Ckpt8:
     """An uninitialised checkpoint for [rows, cols]."""
-    blocks = -(-cols // 128)
-    make = lambda w, dt: torch.empty((rows, w), dtype=dt, device=device)  # noqa: E731
-    return Ckpt8(make(cols, torch.float8_e4m3fn), make(blocks, torch.uint8), make(cols, torch.float8_e4m3fn),
-                 make(blocks, torch.uint8))
-
-
-def _rows(t, name):
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be [rows, cols] with contiguous rows")
-    return t.stride(0)
+    codes, exps = (rows, cols), (rows, -(-cols // 128))
+    return Ckpt8(_empty(codes, dtype=_E4M3, device=device), _empty(exps, dtype=_U8, device=device),
+                 _empty(codes, dtype=_E4M3, device=device), _empty(exps, dtype=_U8, device=device))
 
 
 def swiglu_ckpt8(gate, up, out=None, stream=None):
     """(h, ckpt): h = silu(gate) * up ([rows, cols], bf16 or fp32) and gate and up in 8 bits.  ``out = (h, ckpt)``."""
-    dt = _dtype(gate, "gate")
-    _on_device(gate, "gate")
+    dtype, shape = gate.dtype, gate.shape
+    dt = _dtype(dtype, "gate")
+    dev = _device(gate, "gate")
     gs, us = _rows(gate, "gate"), _rows(up, "up")
-    _like(up, gate, gate.shape, "up")
-    rows, cols = gate.shape
+    _like(up, dtype, dev, shape, "up")
+    rows, cols = shape
     if out is None:
-        h, ckpt = torch.empty((rows, cols), dtype=gate.dtype, device=gate.device), new_ckpt8(rows, cols, gate.device)
+        device = gate.device
+        h, ckpt, hs = gate.new_empty(shape), new_ckpt8(rows, cols, device), cols
+        desc = _b.Ckpt8Desc(*[t.data_ptr() for t in ckpt])
     else:
         h, ckpt = out
-        _like(h, gate, gate.shape, "h")
-    _b.tide_swiglu_ckpt8(rows, cols, dt, gate.data_ptr(), gs, up.data_ptr(), us, h.data_ptr(), _rows(h, "h"),
-                         _ckpt_desc(ckpt, rows, cols, gate.device), _stream(stream))
+        _like(h, dtype, dev, shape, "h")
+        hs, desc = _rows(h, "h"), _ckpt_desc(ckpt, rows, cols, dev)
+    _b.tide_swiglu_ckpt8(rows, cols, dt, gate.data_ptr(), gs, up.data_ptr(), us, h.data_ptr(), hs, desc,
+                         _stream(stream))
     return h, ckpt
 
 
 def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=None):
     """(dgate, dup, h) of SwiGLU at the checkpoint's values; h, recomputed, is for the weight gradient of the
     projection that follows (None without ``need_h``).  ``out = (dgate, dup, h)``."""
-    dt = _dtype(dh, "dh")
-    _on_device(dh, "dh")
+    dtype, shape = dh.dtype, dh.shape
+    dt = _dtype(dtype, "dh")
+    dev = _device(dh, "dh")
     ds = _rows(dh, "dh")
-    rows, cols = dh.shape
-    desc = _ckpt_desc(ckpt, rows, cols, dh.device)
+    rows, cols = shape
+    desc = _ckpt_desc(ckpt, rows, cols, dev)
     if out is None:
-        out = [torch.empty((rows, cols), dtype=dh.dtype, device=dh.device) if i < 2 or need_h else None
-               for i in range(3)]
+        dgate, dup = dh.new_empty(shape), dh.new_empty(shape)
+        h = dh.new_empty(shape) if need_h else None
     else:
-        for t, name in zip(out, ("dgate", "dup", "h")):
+        dgate, dup, h = out
+        for t, name in ((dgate, "dgate"), (dup, "dup"), (h, "h")):
             if t is not None:
-                _like(t, dh, dh.shape, name)
-    dgate, dup, h = out
+                _like(t, dtype, dev, shape, name)
     _b.tide_swiglu_ckpt8_grad(rows, cols, dt, desc, dh.data_ptr(), ds, dgate.data_ptr(), _rows(dgate, "dgate"),
                               dup.data_ptr(), _rows(dup, "dup"), 0 if h is None else h.data_ptr(),
                               0 if h is None else _rows(h, "h"), _stream(stream))

@@ -404,7 +404,7 @@ typedef struct {
     int32_t k_heads;         /* >= 0 */
     int32_t head_dim;        /* D in [1, 4096] */
     int32_t rotary_dim;      /* R even, in [0, D]: columns 0..R-1 are rotated, the rest are not */
-    int64_t max_position;    /* rows of the table */
+    int64_t max_position;    /* rows of the table, below 2^31 */
     const float *table;      /* device fp32 [max_position, R]: R/2 cosines, then R/2 sines (see tide_rope_table);
                                 16-byte aligned for the vector path; unused if R = 0 */
     const void *positions;   /* device integers [T]: row of the table for each token; unused if R = 0.  A position
