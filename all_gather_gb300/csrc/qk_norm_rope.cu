@@ -196,47 +196,52 @@ __device__ __forceinline__ f32x2 partner(const f32x2 (&v)[8], int i)
     return IL ? swapped(v[i]) : v[i ^ 4];
 }
 
-// Positions of a warp's items: lane j holds that of the j-th of 32 items, and
-// of the 32 after them.
+// A warp's list of items (a token, or some of its heads): every `step`-th from
+// `first`, `count` in all.  Lane j holds the table row of the j-th item of 32,
+// and of the 32 after them, so that no item waits for its position.
 template <typename T>
-struct Positions {
-    int now, next;
-    int64_t block;
-    __device__ int load(const QkArgs<T> &a, int64_t item, int64_t items, int chunks) const
+struct Items {
+    int64_t first, step;
+    int count, chunks, per_item, heads;
+    int now, next, block;
+    __device__ int position(const QkArgs<T> &a, int n) const
     {
-        return a.R && item < items ? int(position_of(a, item / chunks)) : -1;
+        return a.R && n < count ? int(position_of(a, (first + n * step) / chunks)) : -1;
     }
-    __device__ void start(const QkArgs<T> &a, int64_t first, int64_t step, int64_t items, int chunks)
+    __device__ void start(const QkArgs<T> &a, int64_t first_, int64_t step_, int heads_, int per_item_)
     {
-        const int lane = threadIdx.x & 31;
+        first = first_, step = step_, heads = heads_, per_item = per_item_;
+        chunks = (heads + per_item - 1) / per_item;
+        const int64_t items = a.tokens * chunks;
+        count = first < items ? int((items - first + step - 1) / step) : 0;
         block = 0;
-        now = load(a, first + lane * step, items, chunks);
-        next = load(a, first + (lane + 32) * step, items, chunks);
+        now = position(a, threadIdx.x & 31);
+        next = position(a, (threadIdx.x & 31) + 32);
     }
-    // of the n-th item; n grows by at most one from call to call
-    __device__ int get(const QkArgs<T> &a, int64_t n, int64_t first, int64_t step, int64_t items, int chunks)
+    // Row of the table for the n-th item (-1: outside); n grows by at most one from call to call.
+    __device__ int row(const QkArgs<T> &a, int n)
     {
         if (n / 32 != block) {
             block = n / 32;
             now = next;
-            next = load(a, first + ((block + 1) * 32 + (threadIdx.x & 31)) * step, items, chunks);
+            next = position(a, (block + 1) * 32 + (threadIdx.x & 31));
         }
-        return __shfl_sync(0xffffffffu, now, int(n % 32));
+        return __shfl_sync(0xffffffffu, now, n % 32);
+    }
+    // Token, first head and end of the n-th item.
+    __device__ int64_t enter(int n, int &h0, int &h1) const
+    {
+        int64_t t = first + n * step;
+        h0 = 0;
+        if (chunks > 1) {
+            const int64_t item = t;
+            t = item / chunks;
+            h0 = int(item - t * chunks) * per_item;
+        }
+        h1 = min(heads, h0 + per_item);
+        return t;
     }
 };
-
-// A warp's place in its list of steps.
-struct Cursor {
-    int64_t n, item, t;  // n-th item of the warp
-    int h, h0, h1;       // first head of the step; of the item; end of the item
-};
-template <typename T>
-__device__ __forceinline__ void enter(Cursor &c, int heads, int per_item, int chunks)
-{
-    c.t = c.item / chunks;
-    c.h = c.h0 = int(c.item - c.t * chunks) * per_item;
-    c.h1 = min(heads, c.h0 + per_item);
-}
 
 // Cosines and sines of a unit's pairs out of a token's row in shared memory,
 // as factors of an element and of its partner; back: of the reverse rotation.
@@ -284,130 +289,146 @@ __host__ __device__ constexpr int ring_bytes(int tensors, int G)
     return kDepth * (tensors * 2 * int(sizeof(T)) / 2 * 512 + G * 64);
 }
 
+// Pieces that a lane's unit does not have read as 0 out of every slot.
+__device__ __forceinline__ void clear_missing(uint4 *ring, int lane, int pieces, int per_vector, const Unit &n)
+{
+    for (int i = 0; i < pieces; ++i)
+        if (!(i / per_vector % 2 ? n.has1 : n.has0))
+            ring[i * 32 + lane] = make_uint4(0, 0, 0, 0);
+}
+
 template <typename T, int G, bool IL>
 __global__ void __launch_bounds__(kThreads, 2) qk_forward_kernel(const QkArgs<T> a)
 {
     constexpr int kRows = 32 / G;       // heads of a step
     constexpr int kVec = sizeof(T) / 2; // 16-byte pieces of eight elements
+    constexpr int kSlot = 2 * kVec * 32;
     extern __shared__ uint4 smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
     uint4 *ring = smem + warp * (ring_bytes<T>(1, G) / 16);
-    float *angles = reinterpret_cast<float *>(ring + kDepth * 2 * kVec * 32);
+    float *angles = reinterpret_cast<float *>(ring + kDepth * kSlot);
+    ring += lane;
     const Unit n = unit_of<IL>(lane % G, a.D, a.R);
     const float inv_d = 1.f / float(a.D);
-    const int heads = a.part[0].heads + a.part[1].heads, hq = a.part[0].heads;
-    const int per_item = a.heads_per_item, chunks = (heads + per_item - 1) / per_item;
-    const int64_t items = a.tokens * chunks;
-    const int64_t first = int64_t(blockIdx.x) * kWarps + warp, step = int64_t(gridDim.x) * kWarps;
-    if (first >= items)
-        return;
-    Positions<T> positions;
-    positions.start(a, first, step, items, chunks);
+    const int hq = a.part[0].heads;
+    Items<T> items;
+    items.start(a, int64_t(blockIdx.x) * kWarps + warp, int64_t(gridDim.x) * kWarps, hq + a.part[1].heads,
+                a.heads_per_item);
+    clear_missing(ring - lane, lane, kDepth * 2 * kVec, kVec, n);
 
-    // The next step to fetch, and its number.
-    Cursor f = {0, first, 0, 0, 0, 0};
-    enter<T>(f, heads, per_item, chunks);
-    int slot_f = 0, bad_bits = 0;  // bit n % 32: the n-th item's position is outside the table
+    // The next step to fetch: its item, first head, the lane's row.
+    int fn = 0, fh = 0, fh1 = 0, slot_f = 0;
+    int64_t ft = 0, fd = 0;
+    const T *fp = nullptr;
+    uint32_t bad_bits = 0;  // bit n % 32: the n-th item's position is outside the table
+    auto aim = [&](int h) {
+        const Part<T> &p = a.part[h >= hq];
+        fp = p.x.row(ft, h >= hq ? h - hq : h);
+        fd = kRows * p.x.sh;
+    };
+    auto next_item = [&] {
+        if (fn < items.count) {
+            ft = items.enter(fn, fh, fh1);
+            aim(fh + g);
+        }
+    };
+    bool fresh = true;
     auto fetch = [&] {
-        if (f.item < items) {
-            const int h = f.h + g;
-            if (h < f.h1) {
-                const Part<T> &p = a.part[h >= hq];
-                const T *row = p.x.row(f.t, h >= hq ? h - hq : h);
-                uint4 *to = ring + slot_f * 2 * kVec * 32 + lane;
+        if (fn < items.count) {
+            const int h = fh + g;
+            if (h < fh1) {
+                uint4 *to = ring + slot_f * kSlot;
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) {
                     if (n.has0)
-                        copy16(to + k * 32, row + n.off0 + k * 4);
+                        copy16(to + k * 32, fp + n.off0 + k * 4);
                     if (n.has1)
-                        copy16(to + (kVec + k) * 32, row + n.off1 + k * 4);
+                        copy16(to + (kVec + k) * 32, fp + n.off1 + k * 4);
                 }
             }
-            if (f.h == f.h0 && a.R) {
-                const int pos = positions.get(a, f.n, first, step, items, chunks);
-                const uint32_t bit = 1u << (f.n % 32);
+            if (fresh && a.R) {
+                const int pos = items.row(a, fn);
+                const uint32_t bit = 1u << (fn % 32);
                 bad_bits = pos < 0 ? bad_bits | bit : bad_bits & ~bit;
                 if (pos >= 0) {
                     const float *row = a.table + int64_t(pos) * a.R;
-                    float *to = angles + (f.n % kDepth) * G * 16;
+                    float *to = angles + (fn % kDepth) * G * 16;
                     for (int i = lane; i < a.R / 4; i += 32)
                         copy16(to + 4 * i, row + 4 * i);
                 }
             }
-            f.h += kRows;
-            if (f.h >= f.h1) {
-                f.item += step;
-                ++f.n;
-                if (f.item < items)
-                    enter<T>(f, heads, per_item, chunks);
+            fresh = false;
+            fh += kRows;
+            if (fh >= fh1) {
+                ++fn;
+                fresh = true;
+                next_item();
+            } else if (h < hq && h + kRows >= hq) {
+                aim(h + kRows);
+            } else {
+                fp += fd;
             }
         }
         copies_end();
         slot_f = slot_f + 1 == kDepth ? 0 : slot_f + 1;
     };
+    next_item();
 #pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i)
         fetch();
 
     int slot = 0;
-    int64_t count = 0;
-    for (int64_t item = first; item < items; item += step, ++count) {
-        Cursor c = {count, item, 0, 0, 0, 0};
-        enter<T>(c, heads, per_item, chunks);
+    for (int i = 0; i < items.count; ++i) {
+        int h, h1;
+        const int64_t t = items.enter(i, h, h1);
         f32x2 c2[8], s2[8];
-        int is_k = -1;
-        for (; c.h < c.h1; c.h += kRows) {
+        const T *w = nullptr;
+        T *to = nullptr;
+        int64_t d = 0;
+        int part = -1;
+        for (int left = h1 - h - g, hh = h + g; h < h1; h += kRows, hh += kRows, left -= kRows) {
             copies_wait<kDepth - 2>();
             __syncwarp();
-            const int h = c.h + g;
-            const bool on = h < c.h1;
-            const int k = h >= hq;
-            const Part<T> &p = a.part[k];
-            if (on && k != is_k) {  // a token's first queries, or keys: angles and weight into factors
-                is_k = k;
-                angle_factors<IL, false>(angles + (count % kDepth) * G * 16, a.R, n, bad_bits >> (count % 32) & 1, c2,
-                                         s2);
-                if (p.w) {
-                    f32x2 w[8];
-                    load_weight(p.w, n, w);
+            if (left > 0 && part != (hh >= hq)) {  // a token's first queries, or keys: angles and weight into factors
+                part = hh >= hq;
+                const Part<T> &p = a.part[part];
+                to = p.out.row(t, hh - (part ? hq : 0));
+                d = kRows * p.out.sh;
+                w = p.w;
+                angle_factors<IL, false>(angles + (i % kDepth) * G * 16, a.R, n, bad_bits >> (i % 32) & 1, c2, s2);
+                if (w) {
+                    f32x2 f[8];
+                    load_weight(w, n, f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        c2[i] = n.rot ? mul2(c2[i], w[i]) : w[i];
-                        s2[i] = mul2(s2[i], partner<IL>(w, i));
+                    for (int j = 0; j < 8; ++j) {
+                        c2[j] = n.rot ? mul2(c2[j], f[j]) : f[j];
+                        s2[j] = mul2(s2[j], partner<IL>(f, j));
                     }
                 }
             }
             f32x2 v[8], y[8];
-            unpack8(ring + slot * 2 * kVec * 32 + lane, 32, v, static_cast<const T *>(nullptr));
-            unpack8(ring + (slot * 2 + 1) * kVec * 32 + lane, 32, v + 4, static_cast<const T *>(nullptr));
-            if (!on || !n.has0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = 0;
-            }
-            if (!on || !n.has1) {
-#pragma unroll
-                for (int i = 4; i < 8; ++i)
-                    v[i] = 0;
-            }
+            unpack8(ring + slot * kSlot, 32, v, static_cast<const T *>(nullptr));
+            unpack8(ring + slot * kSlot + kVec * 32, 32, v + 4, static_cast<const T *>(nullptr));
             const float r = inv_rms<G>(v, inv_d, a.eps);
             if (n.rot) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = fma2(v[i], c2[i], mul2(partner<IL>(v, i), s2[i]));
+                for (int j = 0; j < 8; ++j)
+                    y[j] = fma2(v[j], c2[j], mul2(partner<IL>(v, j), s2[j]));
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = p.w ? mul2(v[i], c2[i]) : v[i];
+                for (int j = 0; j < 8; ++j)
+                    y[j] = w ? mul2(v[j], c2[j]) : v[j];
             }
-            if (p.w) {
+            if (w) {
                 const f32x2 r2 = pair(r, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = mul2(y[i], r2);
+                for (int j = 0; j < 8; ++j)
+                    y[j] = mul2(y[j], r2);
             }
-            if (on)
-                store_unit(p.out.row(c.t, k ? h - hq : h), n, y);
+            if (left > 0) {  // a group without a head has worked on an old step
+                store_unit(to, n, y);
+                to += d;
+            }
             __syncwarp();
             slot = slot + 1 == kDepth ? 0 : slot + 1;
             fetch();
@@ -421,134 +442,148 @@ __global__ void __launch_bounds__(kThreads, 2) qk_backward_kernel(const QkArgs<T
 {
     constexpr int kRows = 32 / G;
     constexpr int kVec = sizeof(T) / 2;
+    constexpr int kSlot = 4 * kVec * 32;
     extern __shared__ uint4 smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
     uint4 *ring = smem + warp * (ring_bytes<T>(2, G) / 16);
-    float *angles = reinterpret_cast<float *>(ring + kDepth * 4 * kVec * 32);
+    float *angles = reinterpret_cast<float *>(ring + kDepth * kSlot);
+    ring += lane;
     const Unit n = unit_of<IL>(lane % G, a.D, a.R);
     const float inv_d = 1.f / float(a.D);
     const int which = int(blockIdx.x) >= a.part[0].blocks;
     const Part<T> &p = a.part[which];
     const int block = int(blockIdx.x) - (which ? a.part[0].blocks : 0);
-    const int heads = p.heads, per_item = p.heads_per_item, chunks = (heads + per_item - 1) / per_item;
-    const int64_t items = p.items;
-    const int64_t first = int64_t(block) * kWarps + warp, step = int64_t(p.blocks) * kWarps;
+    const bool norm = p.w != nullptr;
 
     f32x2 w[8], acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         acc[i] = 0;
-    if (p.w)
+    if (norm)
         load_weight(p.w, n, w);
-    Positions<T> positions;
-    positions.start(a, first, step, items, chunks);
-    Cursor f = {0, first, 0, 0, 0, 0};
-    enter<T>(f, heads, per_item, chunks);
-    int slot_f = 0, bad_bits = 0;
+    Items<T> items;
+    items.start(a, int64_t(block) * kWarps + warp, int64_t(p.blocks) * kWarps, p.heads, p.heads_per_item);
+    clear_missing(ring - lane, lane, kDepth * 4 * kVec, kVec, n);
+
+    int fn = 0, fh = 0, fh1 = 0, slot_f = 0;
+    const T *fd = nullptr, *fx = nullptr;
+    uint32_t bad_bits = 0;
+    const int64_t step_d = kRows * p.d.sh, step_x = kRows * p.x.sh, step_out = kRows * p.out.sh;
+    auto next_item = [&] {
+        if (fn < items.count) {
+            const int64_t t = items.enter(fn, fh, fh1);
+            fd = p.d.row(t, fh + g);
+            fx = p.x.row(t, fh + g);
+        }
+    };
+    bool fresh = true;
     auto fetch = [&] {
-        if (f.item < items) {
-            const int h = f.h + g;
-            if (h < f.h1) {
-                uint4 *to = ring + slot_f * 4 * kVec * 32 + lane;
-                const T *row = p.d.row(f.t, h);
+        if (fn < items.count) {
+            if (fh + g < fh1) {
+                uint4 *to = ring + slot_f * kSlot;
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) {
                     if (n.has0)
-                        copy16(to + k * 32, row + n.off0 + k * 4);
+                        copy16(to + k * 32, fd + n.off0 + k * 4);
                     if (n.has1)
-                        copy16(to + (kVec + k) * 32, row + n.off1 + k * 4);
-                }
-                if (p.w) {
-                    row = p.x.row(f.t, h);
-#pragma unroll
-                    for (int k = 0; k < kVec; ++k) {
-                        if (n.has0)
-                            copy16(to + (2 * kVec + k) * 32, row + n.off0 + k * 4);
-                        if (n.has1)
-                            copy16(to + (3 * kVec + k) * 32, row + n.off1 + k * 4);
-                    }
+                        copy16(to + (kVec + k) * 32, fd + n.off1 + k * 4);
+                    if (norm && n.has0)
+                        copy16(to + (2 * kVec + k) * 32, fx + n.off0 + k * 4);
+                    if (norm && n.has1)
+                        copy16(to + (3 * kVec + k) * 32, fx + n.off1 + k * 4);
                 }
             }
-            if (f.h == f.h0 && a.R) {
-                const int pos = positions.get(a, f.n, first, step, items, chunks);
-                const uint32_t bit = 1u << (f.n % 32);
+            if (fresh && a.R) {
+                const int pos = items.row(a, fn);
+                const uint32_t bit = 1u << (fn % 32);
                 bad_bits = pos < 0 ? bad_bits | bit : bad_bits & ~bit;
                 if (pos >= 0) {
                     const float *row = a.table + int64_t(pos) * a.R;
-                    float *to = angles + (f.n % kDepth) * G * 16;
+                    float *to = angles + (fn % kDepth) * G * 16;
                     for (int i = lane; i < a.R / 4; i += 32)
                         copy16(to + 4 * i, row + 4 * i);
                 }
             }
-            f.h += kRows;
-            if (f.h >= f.h1) {
-                f.item += step;
-                ++f.n;
-                if (f.item < items)
-                    enter<T>(f, heads, per_item, chunks);
+            fresh = false;
+            fh += kRows;
+            fd += step_d;
+            fx += step_x;
+            if (fh >= fh1) {
+                ++fn;
+                fresh = true;
+                next_item();
             }
         }
         copies_end();
         slot_f = slot_f + 1 == kDepth ? 0 : slot_f + 1;
     };
+    next_item();
 #pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i)
         fetch();
 
     int slot = 0;
-    int64_t count = 0;
-    for (int64_t item = first; item < items; item += step, ++count) {
-        Cursor c = {count, item, 0, 0, 0, 0};
-        enter<T>(c, heads, per_item, chunks);
+    for (int i = 0; i < items.count; ++i) {
+        int h, h1;
+        const int64_t t = items.enter(i, h, h1);
+        T *to = p.out.row(t, h + g);
         f32x2 c2[8], s2[8];
-        for (; c.h < c.h1; c.h += kRows) {
+        bool first = true;
+        for (; h < h1; h += kRows) {
             copies_wait<kDepth - 2>();
             __syncwarp();
-            if (c.h == c.h0)
-                angle_factors<IL, true>(angles + (count % kDepth) * G * 16, a.R, n, bad_bits >> (count % 32) & 1, c2,
-                                        s2);
-            const int h = c.h + g;
-            const bool on = h < c.h1;
-            const uint4 *from = ring + slot * 4 * kVec * 32 + lane;
+            if (first)
+                angle_factors<IL, true>(angles + (i % kDepth) * G * 16, a.R, n, bad_bits >> (i % 32) & 1, c2, s2);
+            first = false;
+            const bool on = h + g < h1;
+            const uint4 *from = ring + slot * kSlot;
             f32x2 d[8], y[8];
             unpack8(from, 32, d, static_cast<const T *>(nullptr));
             unpack8(from + kVec * 32, 32, d + 4, static_cast<const T *>(nullptr));
+            if (n.rot) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = n.rot ? fma2(d[i], c2[i], mul2(partner<IL>(d, i), s2[i])) : d[i];
-            if (p.w) {
+                for (int j = 0; j < 8; ++j)
+                    y[j] = fma2(d[j], c2[j], mul2(partner<IL>(d, j), s2[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = d[j];
+            }
+            if (norm) {
                 f32x2 x[8];
                 unpack8(from + 2 * kVec * 32, 32, x, static_cast<const T *>(nullptr));
                 unpack8(from + 3 * kVec * 32, 32, x + 4, static_cast<const T *>(nullptr));
+                if (h + kRows > h1 && !on) {  // a group without a head adds nothing to the weight's gradient
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!on || !(i < 4 ? n.has0 : n.has1))
-                        x[i] = y[i] = 0;
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = y[j] = 0;
+                }
                 const float r = inv_rms<G>(x, inv_d, a.eps);
                 const f32x2 r2 = pair(r, r);
                 f32x2 m2 = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = mul2(x[i], r2);
-                    acc[i] = fma2(y[i], x[i], acc[i]);
-                    y[i] = mul2(y[i], w[i]);
-                    m2 = fma2(y[i], x[i], m2);
+                for (int j = 0; j < 8; ++j) {
+                    x[j] = mul2(x[j], r2);
+                    acc[j] = fma2(y[j], x[j], acc[j]);
+                    y[j] = mul2(y[j], w[j]);
+                    m2 = fma2(y[j], x[j], m2);
                 }
                 const float m = -group_sum<G>(lo_of(m2) + hi_of(m2)) * inv_d;
                 m2 = pair(m, m);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = mul2(fma2(x[i], m2, y[i]), r2);
+                for (int j = 0; j < 8; ++j)
+                    y[j] = mul2(fma2(x[j], m2, y[j]), r2);
             }
             if (on)
-                store_unit(p.out.row(c.t, h), n, y);
+                store_unit(to, n, y);
+            to += step_out;
             __syncwarp();
             slot = slot + 1 == kDepth ? 0 : slot + 1;
             fetch();
         }
     }
     copies_wait<0>();
-    if (!p.w)
+    if (!norm)
         return;
     __syncthreads();  // the ring is free: the lanes' sums go through it
     float *sums = reinterpret_cast<float *>(smem);
@@ -841,11 +876,13 @@ int heads_per_item(int heads, int rows, int64_t tokens, int64_t warps)
     return int((steps + std::min(steps, want) - 1) / std::min(steps, want)) * rows;
 }
 
-// Blocks of the backward for queries and for keys: two a SM, shared by heads.
+// Blocks of the backward for queries and for keys: two a SM, shared by their
+// steps of four heads and one more for each token's own work.
 void grad_blocks(const tide_qk_t *qk, int sms, int *q, int *k)
 {
-    const int64_t all = int64_t(sms) * 2, heads = int64_t(qk->q_heads) + qk->k_heads;
-    int64_t nq = heads ? (all * qk->q_heads + heads - 1) / heads : 0;
+    const int64_t all = int64_t(sms) * 2;
+    const int64_t wq = qk->q_heads ? qk->q_heads + 4 : 0, wk = qk->k_heads ? qk->k_heads + 4 : 0;
+    int64_t nq = wq + wk ? (all * wq + wq + wk - 1) / (wq + wk) : 0;
     int64_t nk = all - nq;
     if (qk->k_heads > 0 && nk < 1)
         nk = 1;
