@@ -29,11 +29,18 @@ using tide::op_fail;
 using bf16 = __nv_bfloat16;
 namespace um = tide::umma;
 
-constexpr int kM = 128, kN = 256, kK = 64;   // tile and step of the sum
-constexpr int kStages = 4;
-constexpr int kABytes = kM * kK * 2, kBBytes = kN * kK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kRingBytes = kStages * kStageBytes;
-constexpr int kSmemBytes = kRingBytes + 1024 + 256;  // 1024: the ring's alignment; 256: barriers
+constexpr int kM = 128, kN = 256, kK = 64;   // a block's rows, the tile's columns, a step of the sum
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kSmemBytes = kRingBytes + 1024;        // 1024: the ring's alignment
+// A block's share of a step, and how many the ring holds.  A pair of blocks
+// works on 256 x 256 tiles: each fetches its 128 rows of A and half of B's
+// columns, so a product of the pair reads a third less than two single ones.
+template <bool PAIR>
+struct Ring {
+    static constexpr int rows_b = PAIR ? kN / 2 : kN;
+    static constexpr int a_bytes = kM * kK * 2, bytes = a_bytes + rows_b * kK * 2;
+    static constexpr int stages = kRingBytes / bytes;
+};
 constexpr int kThreads = 192;                        // fetch, products, 4 warps of results
 constexpr int kTmemCols = 512;                       // two accumulators of 256 columns
 constexpr int kGroupM = 16;                          // row tiles that share a sweep over the columns
@@ -150,9 +157,11 @@ __device__ __forceinline__ void store_bf16(const Gemm &g, int64_t m, int64_t n, 
     }
 }
 
-template <int E>
+template <int E, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
 {
+    using R = Ring<PAIR>;
+    constexpr int kStages = R::stages, kBlocks = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
     __shared__ uint64_t bars[2 * kStages + 5];
@@ -161,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages;
     const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? int(um::cluster_rank()) : 0;  // of a pair, block 0 issues the products
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(acc_full + 8 * i, 1);
-            um::mbar_init(acc_empty + 8 * i, 4);
+            um::mbar_init(acc_empty + 8 * i, 4 * kBlocks);
         }
         um::mbar_init(drained, 1);
         um::fence_barrier_init();
@@ -178,41 +188,55 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         um::prefetch_map(&g.b);
     }
     if (warp == 1)
-        um::tmem_alloc(um::smem_addr(&tmem_slot), kTmemCols);
+        um::tmem_alloc<PAIR>(um::smem_addr(&tmem_slot), kTmemCols);
     um::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        um::cluster_sync();
     um::fence_after();
     const uint32_t tmem = tmem_slot;
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+    const int64_t first = blockIdx.x / kBlocks, step = gridDim.x / kBlocks;
 
     if (warp == 0) {
         if (lane == 0) {
             int stage = 0, turns = 0;  // ring position, and how often the ring went round
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < works; i += gridDim.x) {
+            for (int64_t i = first; ok && i < works; i += step) {
                 const Work w = work_of(g, i);
+                const int m = (w.m * kBlocks + rank) * kM, n = w.n * kN + rank * R::rows_b;
                 for (int s = w.s0; s < w.s1; ++s) {
                     if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
                         break;
-                    const uint32_t a = ring + stage * kStageBytes, b = a + kABytes, bar = full + 8 * stage;
-                    um::mbar_expect(bar, kStageBytes);
+                    const uint32_t a = ring + stage * R::bytes, b = a + R::a_bytes;
+                    uint32_t bar = full + 8 * stage;
+                    if (rank == 0)
+                        um::mbar_expect(bar, R::bytes * kBlocks);
+                    if constexpr (PAIR)
+                        bar = um::cluster_addr(bar, 0);
+                    auto load = [&](uint32_t dst, const CUtensorMap *map, int x, int y) {
+                        if constexpr (PAIR)
+                            um::tma_load_2d_pair(dst, map, x, y, bar);
+                        else
+                            um::tma_load_2d(dst, map, x, y, bar);
+                    };
                     if (g.a_mn) {
                         for (int j = 0; j < kM / 64; ++j)
-                            um::tma_load_2d(a + j * 64 * kK * 2, &g.a, w.m * kM + j * 64, s * kK, bar);
+                            load(a + j * 64 * kK * 2, &g.a, m + j * 64, s * kK);
                     } else {
-                        um::tma_load_2d(a, &g.a, s * kK, w.m * kM, bar);
+                        load(a, &g.a, s * kK, m);
                     }
                     if (g.b_mn) {
-                        for (int j = 0; j < kN / 64; ++j)
-                            um::tma_load_2d(b + j * 64 * kK * 2, &g.b, w.n * kN + j * 64, s * kK, bar);
+                        for (int j = 0; j < R::rows_b / 64; ++j)
+                            load(b + j * 64 * kK * 2, &g.b, n + j * 64, s * kK);
                     } else {
-                        um::tma_load_2d(b, &g.b, s * kK, w.n * kN, bar);
+                        load(b, &g.b, s * kK, n);
                     }
                     if (++stage == kStages)
                         stage = 0, ++turns;
                 }
             }
-            if (!ok) {  // wait for the copies in flight before the block's memory goes
+            if (!ok && rank == 0) {  // wait for the copies in flight before the block's memory goes
                 for (int k = 0; k < kStages; ++k) {
                     const int times = turns + (k < stage);
                     const uint64_t t0 = um::now_ns();
@@ -224,14 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = um::instr_desc(kM, kN, g.a_mn, g.b_mn);
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = um::instr_desc(kM * kBlocks, kN, g.a_mn, g.b_mn);
             const uint32_t a_step = (g.a_mn ? 2048 : 32) >> 4, b_step = (g.b_mn ? 2048 : 32) >> 4;  // 16 of the sum
             int stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < works; i += gridDim.x) {
+            for (int64_t i = first; ok && i < works; i += step) {
                 const Work w = work_of(g, i);
-                if (!(ok = um::mbar_wait(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
+                if (!(ok = um::mbar_wait<PAIR>(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
                     break;
                 um::fence_after();
                 const uint32_t d = tmem + buf * kN;
@@ -239,24 +263,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     if (!(ok = um::mbar_wait(full + 8 * stage, phase, &gave_up, g.wait_ns)))
                         break;
                     um::fence_after();
-                    const uint32_t base = ring + stage * kStageBytes;
+                    const uint32_t base = ring + stage * R::bytes;
                     const uint64_t a = um::operand_desc(base, g.a_mn, 64 * kK * 2);
-                    const uint64_t b = um::operand_desc(base + kABytes, g.b_mn, 64 * kK * 2);
+                    const uint64_t b = um::operand_desc(base + R::a_bytes, g.b_mn, 64 * kK * 2);
 #pragma unroll
                     for (int k = 0; k < kK / 16; ++k)
-                        um::mma_bf16(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
-                    um::mma_commit(empty + 8 * stage);
+                        um::mma_bf16<PAIR>(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
+                    um::mma_commit<PAIR>(empty + 8 * stage);
                     if (++stage == kStages)
                         stage = 0, phase ^= 1;
                 }
                 if (ok)
-                    um::mma_commit(acc_full + 8 * buf);
+                    um::mma_commit<PAIR>(acc_full + 8 * buf);
                 if (++buf == 2)
                     buf = 0, buf_phase ^= 1;
             }
             if (!ok) {  // wait for the products in flight before the accumulators and tiles go
                 g_timed_out = 1;
-                um::mma_commit(drained);
+                um::mma_commit<PAIR>(drained);
                 const uint64_t t0 = um::now_ns();
                 while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < g.wait_ns) {
                 }
@@ -266,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     } else {
         const int quarter = warp % 4;  // a warp reads the tensor-memory lanes of its number modulo 4
         int buf = 0, buf_phase = 0;
-        for (int64_t i = blockIdx.x; i < works; i += gridDim.x) {
+        const uint32_t acc_done = PAIR ? um::cluster_addr(acc_empty, 0) : acc_empty;
+        for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
-            const int64_t m = int64_t(w.m) * kM + quarter * 32 + lane, n0 = int64_t(w.n) * kN;
+            const int64_t m = (int64_t(w.m) * kBlocks + rank) * kM + quarter * 32 + lane, n0 = int64_t(w.n) * kN;
             const bool row = m < g.M;
             int64_t y = -1;
             float lse = 0.f, scale = 0.f;
@@ -278,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 lse = g.lse[m];
                 scale = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[m];
             }
-            if (!um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns)) {
+            const bool ready = um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
+            if (!__all_sync(0xffffffffu, ready)) {
                 g_timed_out = 1;
                 break;
             }
@@ -333,8 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
             um::fence_before();
             __syncwarp();
-            if (lane == 0)
-                um::mbar_arrive(acc_empty + 8 * buf);
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    um::mbar_arrive_cluster(acc_done + 8 * buf);
+                else
+                    um::mbar_arrive(acc_done + 8 * buf);
+            }
             if (E == kStats && row)
                 g.part[int64_t(w.n) * g.M + m] = make_float2(top, sum);
             if (++buf == 2)
@@ -343,9 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     um::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        um::cluster_sync();
     um::fence_after();
     if (warp == 1)
-        um::tmem_free(tmem, kTmemCols);
+        um::tmem_free<PAIR>(tmem, kTmemCols);
 }
 
 // Rows that the tiled copies cannot take (16-byte boundaries) go into the
@@ -358,36 +390,68 @@ __global__ void __launch_bounds__(256) align_kernel(const bf16 *in, int64_t stri
             out[r * pitch + c] = in[r * stride + c];
 }
 
-__global__ void __launch_bounds__(256) join_kernel(const float2 *part, int64_t tiles, int64_t T, const float *zy,
+// Joins a row's pairs (maximum, sum): `rows` neighbouring rows a block, 256 /
+// rows slices of the column tiles each.
+__global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles, int64_t T, int rows, const float *zy,
                                                    Targets y, float *loss, float *lse)
 {
-    const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (t >= T)
-        return;
-    float top = -INFINITY, sum = 0.f;
-    for (int64_t i = 0; i < tiles; ++i)
-        top = fmaxf(top, part[i * T + t].x);
-    for (int64_t i = 0; i < tiles; ++i) {
-        const float2 p = part[i * T + t];
-        sum += p.x == top ? p.y : p.y * expf(p.x - top);
+    __shared__ float2 slices[256];
+    const int row = threadIdx.x % rows, slice = threadIdx.x / rows, n = 256 / rows;
+    const int64_t t = int64_t(blockIdx.x) * rows + row;
+    auto join = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
+        return make_float2(top, (a.x == top ? a.y : a.y * expf(a.x - top)) + (b.x == top ? b.y : b.y * expf(b.x - top)));
+    };
+    float2 s = make_float2(-INFINITY, 0.f);
+    if (t < T) {
+        int i = slice;
+        for (; i + 3 * n < tiles; i += 4 * n) {
+            float2 p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                p[k] = part[int64_t(i + k * n) * T + t];
+            s = join(s, join(join(p[0], p[1]), join(p[2], p[3])));
+        }
+        for (; i < tiles; i += n)
+            s = join(s, part[int64_t(i) * T + t]);
     }
-    const float l = logf(sum) + (isinf(top) ? 0.f : top);
+    slices[threadIdx.x] = s;
+    for (int half = n / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (slice < half)
+            slices[threadIdx.x] = s = join(s, slices[threadIdx.x + half * rows]);
+    }
+    if (slice > 0 || t >= T)
+        return;
+    const float l = logf(s.y) + (isinf(s.x) ? 0.f : s.x);
     const int64_t v = y.get(t);
     lse[t] = l;
     loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - zy[t];
 }
 
-// dx = sum of the splits, in order.
+// dx = sum of the splits, in order; four elements a thread where the rows allow.
+template <int N>
 __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, bf16 *out,
                                                     int64_t stride)
 {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= T * H)
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * N, n = T * H;
+    if (i >= n)
         return;
-    float x = acc[i];
-    for (int s = 1; s < splits; ++s)
-        x += acc[s * T * H + i];
-    out[i / H * stride + i % H] = __float2bfloat16_rn(x);
+    float x[N] = {};
+    for (int s = 0; s < splits; ++s) {
+        if constexpr (N == 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(acc + s * n + i);
+            x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w;
+        } else {
+            x[0] += acc[s * n + i];
+        }
+    }
+    const int64_t t = i / H, c = i - t * H;
+    if constexpr (N == 4)
+        *reinterpret_cast<uint2 *>(out + t * stride + c) =
+            make_uint2(tide::pack_bf16(x[0], x[1]), tide::pack_bf16(x[2], x[3]));
+    else
+        out[t * stride + c] = __float2bfloat16_rn(x[0]);
 }
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -491,6 +555,48 @@ Gemm base(const tide_ce_t *ce)
     return g;
 }
 
+// Whether pairs of blocks take a product of M rows.  A pair's tiles have 256
+// rows, a block's 128: where M just spills into another 256, single blocks
+// waste less.
+bool takes_pairs(int64_t M)
+{
+    const int64_t blocks = (M + kM - 1) / kM, pairs = (blocks + 1) / 2;
+    return pairs * 2 * 9 <= blocks * 10;
+}
+
+template <int E, bool PAIR>
+tide_status_t launch_as(Gemm &g, const Mat &a, const Mat &b, const char *what, cudaStream_t st)
+{
+    constexpr int blocks = PAIR ? 2 : 1;
+    g.tiles_m = int((g.M + blocks * kM - 1) / (blocks * kM));
+    g.tiles_n = int((g.N + kN - 1) / kN);
+    tide_status_t s = make_map(&g.a, a, g.a_mn ? kK : kM);
+    if (!s)
+        s = make_map(&g.b, b, g.b_mn ? kK : Ring<PAIR>::rows_b);
+    if (s)
+        return s;
+    auto kernel = gemm_kernel<E, PAIR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess) {
+        const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(std::min<int64_t>(works, tide::op_sm_count() / blocks)) * blocks);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, kernel, g);
+    }
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return tide::op_launched(what);
+}
+
 // C[M, N] = sum over k of A B.  An operand is given with its rows as the tile's
 // dimension (K-major) or, mn, with its rows as the summed one.
 template <int E>
@@ -500,21 +606,8 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
     g.M = a_mn ? a.cols : a.rows;
     g.N = b_mn ? b.cols : b.rows;
     g.K = a_mn ? a.rows : a.cols;
-    g.tiles_m = int((g.M + kM - 1) / kM);
-    g.tiles_n = int((g.N + kN - 1) / kN);
     g.steps = int((g.K + kK - 1) / kK);
-    tide_status_t s = make_map(&g.a, a, a_mn ? kK : kM);
-    if (!s)
-        s = make_map(&g.b, b, b_mn ? kK : kN);
-    if (s)
-        return s;
-    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess)
-        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
-    const unsigned grid = unsigned(std::min<int64_t>(works, tide::op_sm_count()));
-    gemm_kernel<E><<<grid, kThreads, kSmemBytes, st>>>(g);
-    return tide::op_launched(what);
+    return takes_pairs(g.M) ? launch_as<E, true>(g, a, b, what, st) : launch_as<E, false>(g, a, b, what, st);
 }
 
 // Where a call's scratch data lies in its workspace, in bytes.
@@ -536,8 +629,9 @@ struct Layout {
 // may be fewer than the SMs, or just over a whole number of rounds.
 int splits_of(const tide_ce_t *ce, int64_t piece)
 {
-    const int64_t sms = std::max(tide::op_sm_count(), 1);
-    const int64_t tiles = ((ce->tokens + kM - 1) / kM) * ((ce->hidden + kN - 1) / kN);
+    const int blocks = takes_pairs(ce->tokens) ? 2 : 1;
+    const int64_t sms = std::max(tide::op_sm_count() / blocks, 1);
+    const int64_t tiles = ((ce->tokens + blocks * kM - 1) / (blocks * kM)) * ((ce->hidden + kN - 1) / kN);
     const int64_t steps = (std::min(piece, ce->vocab) + kK - 1) / kK;
     int best = 1;
     double best_time = 1e30;
@@ -628,7 +722,10 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
     s = launch<kStats>(g, x, false, w, false, "ce_loss", st);
     if (s)
         return s;
-    join_kernel<<<unsigned((T + 255) / 256), 256, 0, st>>>(g.part, g.tiles_n, T, g.zy, g.y, loss, lse);
+    int rows = 32;  // few rows: more slices of each
+    while (rows > 1 && rows / 2 >= T)
+        rows /= 2;
+    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, g.tiles_n, T, rows, g.zy, g.y, loss, lse);
     return tide::op_launched("ce_loss: join");
 }
 
@@ -697,8 +794,11 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
     }
     if (s)
         return s;
-    round_kernel<<<unsigned((T * H + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, static_cast<bf16 *>(dx),
-                                                               dx_stride);
+    bf16 *out = static_cast<bf16 *>(dx);
+    if (H % 4 == 0 && op_aligned(dx, 8) && (T < 2 || dx_stride % 4 == 0))
+        round_kernel<4><<<unsigned((T * H / 4 + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, out, dx_stride);
+    else
+        round_kernel<1><<<unsigned((T * H + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, out, dx_stride);
     return tide::op_launched("ce_grad: rounding");
 }
 
