@@ -12,8 +12,8 @@
 // All products run in one persistent kernel, one block a SM: a thread fetches
 // 64 columns of both operands at a time into a ring of swizzled tiles (TMA),
 // a thread issues the tensor-core products of 128 x 256 tiles into one of two
-// accumulators in tensor memory, and four warps work on the other one (a
-// thread a row).  The operand whose rows are the summed dimension (W and x in
+// accumulators in tensor memory, and eight warps work on the other one (a
+// thread has half a row) and send their results through shared memory as tiles.  The operand whose rows are the summed dimension (W and x in
 // the gradients, dz in dW) is read as it lies, MN-major, so nothing is
 // transposed in memory.  Bound by the tensor cores for many tokens and by the
 // weight's bytes for few.
@@ -31,7 +31,9 @@ namespace um = tide::umma;
 
 constexpr int kM = 128, kN = 256, kK = 64;   // a block's rows, the tile's columns, a step of the sum
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kSmemBytes = kRingBytes + 1024;        // 1024: the ring's alignment
+constexpr int kOutWarps = 8;                         // warps that work on results
+constexpr int kOutBytes = 4096;                      // a warp's 32 rows of 128 bytes on their way out
+constexpr int kSmemBytes = kRingBytes + kOutWarps * kOutBytes + 1024;  // 1024: alignment
 // A block's share of a step, and how many the ring holds.  A pair of blocks
 // works on 256 x 256 tiles: each fetches its 128 rows of A and half of B's
 // columns, so a product of the pair reads a third less than two single ones.
@@ -41,7 +43,7 @@ struct Ring {
     static constexpr int a_bytes = kM * kK * 2, bytes = a_bytes + rows_b * kK * 2;
     static constexpr int stages = kRingBytes / bytes;
 };
-constexpr int kThreads = 192;                        // fetch, products, 4 warps of results
+constexpr int kThreads = 64 + 32 * kOutWarps;        // fetch, products, results
 constexpr int kTmemCols = 512;                       // two accumulators of 256 columns
 constexpr int kGroupM = 16;                          // row tiles that share a sweep over the columns
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
@@ -68,20 +70,19 @@ struct Targets {
 enum Epilogue { kStats, kDz, kAdd, kStore };
 
 struct Gemm {
-    CUtensorMap a, b;
+    CUtensorMap a, b, c;  // c: kDz and kStore: out; kAdd: acc, as [splits][M][N]
     int64_t M, N, K;
     int a_mn, b_mn;      // operand is MN-major
     int tiles_m, tiles_n, splits, steps;  // steps of the sum in all
     int64_t v0;          // first vocabulary column of this piece
     Targets y;
-    float2 *part;        // kStats: [column tiles][M]
+    float2 *part;        // kStats: [halves of column tiles][M]
     float *zy;           // kStats: logit of the target
     const float *lse, *dloss;
     bf16 *out;           // kDz, kStore
     int64_t out_stride;
-    int out_vec;         // its rows are on 16-byte boundaries
-    float *acc;          // kAdd: [splits][M][N], added to unless `first`
-    int first;
+    int out_tiles;       // its rows are on 16-byte boundaries: stored as tiles
+    int first;           // kAdd: acc is written, not added to
     uint64_t wait_ns;
 };
 
@@ -141,22 +142,6 @@ __device__ __forceinline__ void add_stats(const uint32_t (&v)[32], int cols, flo
     sum += a + b;
 }
 
-template <int E>
-__device__ __forceinline__ void store_bf16(const Gemm &g, int64_t m, int64_t n, int cols, const float (&f)[32])
-{
-    bf16 *out = g.out + m * g.out_stride + n;
-    if (g.out_vec && cols >= 32) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            tide::store8(out + i, f + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < cols)
-                out[i] = __float2bfloat16_rn(f[i]);
-    }
-}
-
 template <int E, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
 {
@@ -179,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(acc_full + 8 * i, 1);
-            um::mbar_init(acc_empty + 8 * i, 4 * kBlocks);
+            um::mbar_init(acc_empty + 8 * i, kOutWarps * kBlocks);
         }
         um::mbar_init(drained, 1);
         um::fence_barrier_init();
@@ -288,12 +273,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         __syncwarp();
     } else {
-        const int quarter = warp % 4;  // a warp reads the tensor-memory lanes of its number modulo 4
-        int buf = 0, buf_phase = 0;
+        // A warp reads the tensor-memory lanes of its number modulo 4; the first four warps take the tile's
+        // columns 0 to 127, the others the rest.
+        const int quarter = warp % 4, half = (warp - 2) / 4;
+        const uint32_t out = ring + kRingBytes + (warp - 2) * kOutBytes;
+        const uint32_t out_row = out + lane * 128;
         const uint32_t acc_done = PAIR ? um::cluster_addr(acc_empty, 0) : acc_empty;
+        int buf = 0, buf_phase = 0;
         for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
-            const int64_t m = (int64_t(w.m) * kBlocks + rank) * kM + quarter * 32 + lane, n0 = int64_t(w.n) * kN;
+            const int64_t m0 = (int64_t(w.m) * kBlocks + rank) * kM + quarter * 32, m = m0 + lane;
+            const int64_t n0 = int64_t(w.n) * kN + half * (kN / 2);
             const bool row = m < g.M;
             int64_t y = -1;
             float lse = 0.f, scale = 0.f;
@@ -309,51 +299,84 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 break;
             }
             um::fence_after();
-            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + buf * kN;
+            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + buf * kN + half * (kN / 2);
             float top = -INFINITY, sum = 0.f;
-            for (int c = 0; c < kN; c += 32) {
-                const int cols = int(min(int64_t(32), g.N - n0 - c));
+#pragma unroll 1
+            for (int c = 0; c < kN / 2; c += 32) {
+                const int64_t n = n0 + c;
+                const int cols = int(min(int64_t(32), g.N - n));
                 if (cols <= 0)
                     break;
                 uint32_t v[32];
                 um::tmem_load32(d + c, v);
                 um::tmem_wait_load();
-                if (E == kAdd && w.s0 == w.s1) {  // a last piece shorter than its splits: nothing was summed
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = 0;
-                }
-                const int64_t n = n0 + c;
                 if (E == kStats) {
                     add_stats(v, cols, top, sum);
                     const int64_t at = y - n;
                     if (at >= 0 && at < cols) {
+                        uint32_t z = v[0];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j == int(at))
-                                g.zy[m] = __uint_as_float(v[j]);
+                        for (int j = 1; j < 32; ++j)
+                            z = j == int(at) ? v[j] : z;
+                        g.zy[m] = __uint_as_float(z);
                     }
-                } else if (row) {
-                    float f[32];
-                    if (E == kDz) {
-                        const int64_t at = y - g.v0 - n;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float p = exp_fast(__uint_as_float(v[j]) - lse);
-                            f[j] = y == -1 ? 0.f : (p - (j == at ? 1.f : 0.f)) * scale;
-                        }
-                        store_bf16<E>(g, m, n, cols, f);
-                    } else if (E == kStore) {
+                    continue;
+                }
+                // The tile of 128-byte rows that these columns belong to, and their place in it.
+                const bool begins = E == kAdd || c % 64 == 0, ends = E == kAdd || c % 64 == 32 || n + 32 >= g.N;
+                if (begins && (E == kAdd || g.out_tiles)) {
+                    if (lane == 0)
+                        um::stores_read();
+                    __syncwarp();
+                }
+                if (E == kAdd) {
+                    if (w.s0 == w.s1) {  // a last piece shorter than its splits: nothing was summed
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            f[j] = __uint_as_float(v[j]);
-                        store_bf16<E>(g, m, n, cols, f);
-                    } else {
-                        float *acc = g.acc + (w.split * g.M + m) * g.N + n;
+                            v[j] = 0;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        um::store_shared16(out_row + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                                           v[4 * j + 3]);
+                } else {
+                    uint32_t f[16];
+                    const int64_t at = y - g.v0 - n;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float x[2] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1])};
+                        if (E == kDz) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                x[k] = y == -1 ? 0.f : (exp_fast(x[k] - lse) - (j + k == at ? 1.f : 0.f)) * scale;
+                        }
+                        f[j / 2] = tide::pack_bf16(x[0], x[1]);
+                    }
+                    if (E == kDz || g.out_tiles) {
+                        const int k = c % 64 / 8;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            um::store_shared16(out_row + (((k + j) ^ (lane & 7)) << 4), f[4 * j], f[4 * j + 1],
+                                               f[4 * j + 2], f[4 * j + 3]);
+                    } else if (row) {
+                        uint16_t *p = reinterpret_cast<uint16_t *>(g.out) + m * g.out_stride + n;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (j < cols)
-                                acc[j] = g.first ? __uint_as_float(v[j]) : acc[j] + __uint_as_float(v[j]);
+                                p[j] = uint16_t(f[j / 2] >> (16 * (j % 2)));
+                    }
+                }
+                if (ends && (E == kAdd || g.out_tiles)) {
+                    um::fence_copies();
+                    __syncwarp();
+                    if (lane == 0 && m0 < g.M) {
+                        if (E != kAdd)
+                            um::tma_store_2d(&g.c, out, int(n0 + c / 64 * 64), int(m0));
+                        else if (g.first)
+                            um::tma_store_3d(&g.c, out, int(n), int(m0), w.split);
+                        else
+                            um::tma_add_3d(&g.c, out, int(n), int(m0), w.split);
+                        um::stores_end();
                     }
                 }
             }
@@ -366,10 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     um::mbar_arrive(acc_done + 8 * buf);
             }
             if (E == kStats && row)
-                g.part[int64_t(w.n) * g.M + m] = make_float2(top, sum);
+                g.part[(int64_t(w.n) * 2 + half) * g.M + m] = make_float2(top, sum);
             if (++buf == 2)
                 buf = 0, buf_phase ^= 1;
         }
+        if (lane == 0)
+            um::stores_read();
+        __syncwarp();
     }
     um::fence_before();
     __syncthreads();
@@ -431,11 +457,11 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
 
 // dx = sum of the splits, in order; four elements a thread where the rows allow.
 template <int N>
-__global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, bf16 *out,
-                                                    int64_t stride)
+__global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, int64_t pitch,
+                                                    bf16 *out, int64_t stride)
 {
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * N, n = T * H;
-    if (i >= n)
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * N, n = T * pitch, t = i / pitch, c = i - t * pitch;
+    if (i >= n || c >= H)
         return;
     float x[N] = {};
     for (int s = 0; s < splits; ++s) {
@@ -446,7 +472,6 @@ __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits
             x[0] += acc[s * n + i];
         }
     }
-    const int64_t t = i / H, c = i - t * H;
     if constexpr (N == 4)
         *reinterpret_cast<uint2 *>(out + t * stride + c) =
             make_uint2(tide::pack_bf16(x[0], x[1]), tide::pack_bf16(x[2], x[3]));
@@ -528,22 +553,38 @@ bool rows_aligned(const void *p, int64_t stride, int64_t rows)
     return op_aligned(p, 16) && (rows < 2 || stride % 8 == 0);
 }
 
-// Tensor map whose copies are `box_rows` rows of 64 columns; what lies outside
-// the matrix reads as 0.
-tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows)
+tide_status_t encode(CUtensorMap *map, CUtensorMapDataType type, int rank, void *p, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box)
 {
     const EncodeTiled enc = encode_tiled();
     if (!enc)
         return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(m.rows < 2 ? (m.cols + 7) / 8 * 16 : m.stride * 2)};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, step[2] = {1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box, step,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = enc(map, type, cuuint32_t(rank), p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled: %d", int(r));
     return TIDE_OK;
+}
+
+// Tensor map whose copies are `box_rows` rows of 64 columns; what lies outside
+// the matrix reads as 0 and is not written.
+tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows)
+{
+    const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(m.rows < 2 ? (m.cols + 7) / 8 * 16 : m.stride * 2)};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box);
+}
+
+// The same for fp32 sums [splits][rows][cols] with rows `pitch` apart: 32 rows of 32 columns.
+tide_status_t make_acc_map(CUtensorMap *map, float *p, int64_t splits, int64_t rows, int64_t cols, int64_t pitch)
+{
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(splits)};
+    const cuuint64_t strides[2] = {cuuint64_t(pitch * 4), cuuint64_t(rows * pitch * 4)};
+    const cuuint32_t box[3] = {32, 32, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box);
 }
 
 Gemm base(const tide_ce_t *ce)
@@ -573,6 +614,8 @@ tide_status_t launch_as(Gemm &g, const Mat &a, const Mat &b, const char *what, c
     tide_status_t s = make_map(&g.a, a, g.a_mn ? kK : kM);
     if (!s)
         s = make_map(&g.b, b, g.b_mn ? kK : Ring<PAIR>::rows_b);
+    if (!s && (E == kDz || E == kStore) && g.out_tiles)
+        s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32);
     if (s)
         return s;
     auto kernel = gemm_kernel<E, PAIR>;
@@ -614,7 +657,7 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
 struct Layout {
     int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
     int64_t part = 0, zy = 0;           // loss
-    int64_t dz = 0, acc = 0, piece = 0; // gradient
+    int64_t dz = 0, acc = 0, piece = 0, acc_pitch = 0;  // gradient
     int splits = 1;
     int64_t bytes = 0;
     int64_t take(int64_t n)
@@ -658,9 +701,10 @@ Layout layout_of(const tide_ce_t *ce, bool grad)
         l.piece = piece_of(ce);
         l.splits = splits_of(ce, l.piece);
         l.dz = l.take(ce->tokens * l.piece * 2);
-        l.acc = l.take(ce->tokens * ce->hidden * 4 * l.splits);
+        l.acc_pitch = round_up(ce->hidden, 4);
+        l.acc = l.take(ce->tokens * l.acc_pitch * 4 * l.splits);
     } else {
-        l.part = l.take((ce->vocab + kN - 1) / kN * ce->tokens * 8);
+        l.part = l.take((ce->vocab + kN - 1) / kN * 2 * ce->tokens * 8);
         l.zy = l.take(ce->tokens * 4);
     }
     l.bytes = std::max<int64_t>(l.bytes, 256);
@@ -725,7 +769,7 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
     int rows = 32;  // few rows: more slices of each
     while (rows > 1 && rows / 2 >= T)
         rows /= 2;
-    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, g.tiles_n, T, rows, g.zy, g.y, loss, lse);
+    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_n, T, rows, g.zy, g.y, loss, lse);
     return tide::op_launched("ce_loss: join");
 }
 
@@ -779,26 +823,30 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
         Gemm g = base(ce);
         g.v0 = v0;
         g.lse = lse, g.dloss = dloss;
-        g.out = dz, g.out_stride = l.piece, g.out_vec = 1;
+        g.out = dz, g.out_stride = l.piece, g.out_tiles = 1;
         s = launch<kDz>(g, x, false, wp, false, "ce_grad: dz", st);
         if (s)
             return s;
-        g.acc = acc, g.first = v0 == 0, g.splits = l.splits;
-        s = launch<kAdd>(g, dzp, false, wp, true, "ce_grad: dx", st);
+        g.first = v0 == 0, g.splits = l.splits;
+        s = make_acc_map(&g.c, acc, l.splits, T, H, l.acc_pitch);
+        if (!s)
+            s = launch<kAdd>(g, dzp, false, wp, true, "ce_grad: dx", st);
         if (s)
             return s;
         g.splits = 1;
         g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
-        g.out_vec = rows_aligned(g.out, dweight_stride, V);
+        g.out_tiles = H % 8 == 0 && rows_aligned(g.out, dweight_stride, V);  // tiles are stored by 16 bytes
         s = launch<kStore>(g, dzp, true, x, true, "ce_grad: dweight", st);
     }
     if (s)
         return s;
     bf16 *out = static_cast<bf16 *>(dx);
     if (H % 4 == 0 && op_aligned(dx, 8) && (T < 2 || dx_stride % 4 == 0))
-        round_kernel<4><<<unsigned((T * H / 4 + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, out, dx_stride);
+        round_kernel<4><<<unsigned((T * H / 4 + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, l.acc_pitch, out,
+                                                                          dx_stride);
     else
-        round_kernel<1><<<unsigned((T * H + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, out, dx_stride);
+        round_kernel<1><<<unsigned((T * l.acc_pitch + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, l.acc_pitch, out,
+                                                                                dx_stride);
     return tide::op_launched("ce_grad: rounding");
 }
 

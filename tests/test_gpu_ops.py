@@ -332,6 +332,25 @@ def test_cross_entropy_gradient_against_differences(tide):
     assert abs(diff - a.sum() - b.sum()) <= 2.0 ** -8 * (a.abs().sum() + b.abs().sum())
 
 
+@pytest.mark.parametrize("H, pad", [(100, 4), (1, 7), (65, 7), (130, 6), (63, 1)])
+def test_cross_entropy_reads_and_writes_its_columns_only(tide, H, pad):
+    """Rows on 16-byte boundaries whose length is not a multiple of 16 bytes: what lies between them is not read (it
+    is NaN) and not written."""
+    T, V = 150, 300
+    x, w, y = ce_inputs(H, T, V, H)
+    X, W = (torch.full((n, H + pad), float("nan"), dtype=BF16, device="cuda") for n in (T, V))
+    X[:, :H], W[:, :H] = x, w
+    a = tide.linear_cross_entropy(x, w, y)
+    b = tide.linear_cross_entropy(X[:, :H], W[:, :H], y)
+    assert torch.isfinite(b[0]).all() and torch.equal(a[0], b[0])
+    d = torch.full((T,), 0.01, device="cuda")
+    fx, fw = Framed((T, H), BF16, pad), Framed((V, H), BF16, pad)
+    g = tide.linear_cross_entropy_grad(x, w, y, a[1], d)
+    tide.linear_cross_entropy_grad(X[:, :H], W[:, :H], y, a[1], d, out=(fx.t, fw.t))
+    fx.check(), fw.check()
+    assert torch.equal(fx.t, g[0]) and torch.equal(fw.t, g[1])
+
+
 @pytest.mark.parametrize("T", [3, 140])
 def test_cross_entropy_targets_that_do_not_count(tide, T):
     x, w, y = ce_inputs(31, T, 600, 64)
