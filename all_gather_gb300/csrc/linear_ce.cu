@@ -9,14 +9,18 @@
 // joins a row's pairs in a fixed order.  The gradient makes the logits again,
 // a piece of the vocabulary at a time, and keeps only that piece's dz.
 //
-// All products run in one persistent kernel, one block a SM: a thread fetches
-// 64 columns of both operands at a time into a ring of swizzled tiles (TMA),
-// a thread issues the tensor-core products of 128 x 256 tiles into one of two
-// accumulators in tensor memory, and eight warps work on the other one (a
-// thread has half a row) and send their results through shared memory as tiles.  The operand whose rows are the summed dimension (W and x in
-// the gradients, dz in dW) is read as it lies, MN-major, so nothing is
-// transposed in memory.  Bound by the tensor cores for many tokens and by the
-// weight's bytes for few.
+// All products run in one persistent kernel, a pair of blocks (two SMs) on tiles
+// of 256 rows and up to 256 columns: in each block a thread fetches 64 columns
+// of both operands at a time into a ring of swizzled tiles (TMA), one thread of
+// the pair issues the tensor-core products into one of two accumulators in
+// tensor memory, and eight warps of each block work on the other one.  The rows
+// are the vocabulary's (the hidden columns', for dx) and the tile's columns are
+// tokens: 256 rows suit sizes that are large anyway, and the columns can be
+// fitted to the number of tokens, from 32.  A result warp turns its 32 x 32
+// logits over in shared memory and has a token a thread.  The operand whose
+// rows are the summed dimension (W for dx, dz and x for dW) is read as it lies,
+// MN-major, so nothing is transposed in memory.  Bound by the tensor cores for
+// many tokens and by the weight's bytes for few.
 #include <cuda_runtime.h>
 
 #include "ops_internal.h"
@@ -29,25 +33,19 @@ using tide::op_fail;
 using bf16 = __nv_bfloat16;
 namespace um = tide::umma;
 
-constexpr int kM = 128, kN = 256, kK = 64;   // a block's rows, the tile's columns, a step of the sum
+constexpr int kM = 128, kN = 256, kK = 64;  // a block's rows, the pair's columns at most, a step of the sum
+constexpr int kABytes = kM * kK * 2;        // a block's share of a step: its rows of A, and half of B's columns
 constexpr int kRingBytes = 192 * 1024;
-constexpr int kOutWarps = 8;                         // warps that work on results
-constexpr int kOutBytes = 4096;                      // a warp's 32 rows of 128 bytes on their way out
-constexpr int kSmemBytes = kRingBytes + kOutWarps * kOutBytes + 1024;  // 1024: alignment
-// A block's share of a step, and how many the ring holds.  A pair of blocks
-// works on 256 x 256 tiles: each fetches its 128 rows of A and half of B's
-// columns, so a product of the pair reads a third less than two single ones.
-template <bool PAIR>
-struct Ring {
-    static constexpr int rows_b = PAIR ? kN / 2 : kN;
-    static constexpr int a_bytes = kM * kK * 2, bytes = a_bytes + rows_b * kK * 2;
-    static constexpr int stages = kRingBytes / bytes;
-};
-constexpr int kThreads = 64 + 32 * kOutWarps;        // fetch, products, results
+constexpr int kMaxStages = 10;
+constexpr int kOutWarps = 8;                // warps that work on results
+constexpr int kOutTile = 4096;              // a warp's 32 rows of 128 bytes on their way out
+constexpr int kSmemBytes = kRingBytes + kOutWarps * kOutTile + 1024;  // 1024: alignment
+constexpr int kThreads = 64 + 32 * kOutWarps;                         // fetch, products, results
 constexpr int kTmemCols = 512;                       // two accumulators of 256 columns
 constexpr int kGroupM = 16;                          // row tiles that share a sweep over the columns
 constexpr int64_t kPieceBytes = int64_t(256) << 20;  // dz of one piece of the vocabulary
 constexpr int64_t kMinPiece = 8192;
+constexpr int kMaxSplits = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Set when a bounded wait of a product runs out; read and cleared by
@@ -67,22 +65,25 @@ struct Targets {
     }
 };
 
+// What becomes of a tile: statistics of its tokens; dz; a share of dx; dW.
 enum Epilogue { kStats, kDz, kAdd, kStore };
 
 struct Gemm {
-    CUtensorMap a, b, c;  // c: kDz and kStore: out; kAdd: acc, as [splits][M][N]
+    CUtensorMap a, b, c;  // c: kDz and kStore: out; kAdd: sums, as [splits][M][N]
     int64_t M, N, K;
     int a_mn, b_mn;      // operand is MN-major
     int tiles_m, tiles_n, splits, steps;  // steps of the sum in all
-    int64_t v0;          // first vocabulary column of this piece
+    int tile_n;          // columns of a tile: a multiple of 32, of 128 for kStore
+    int stages;          // of the ring
+    int64_t v0;          // first vocabulary row of this piece
     Targets y;
-    float2 *part;        // kStats: [halves of column tiles][M]
+    float2 *part;        // kStats: [128-row tiles][N]
     float *zy;           // kStats: logit of the target
     const float *lse, *dloss;
-    bf16 *out;           // kDz, kStore
+    bf16 *out;           // kStore
     int64_t out_stride;
     int out_tiles;       // its rows are on 16-byte boundaries: stored as tiles
-    int first;           // kAdd: acc is written, not added to
+    int first;           // kAdd: the sums are written, not added to
     uint64_t wait_ns;
 };
 
@@ -116,55 +117,71 @@ __device__ __forceinline__ Work work_of(const Gemm &g, int64_t i)
     return w;
 }
 
-// Running maximum and sum of a row over 32 more logits, of which the first
-// `cols` count.
-__device__ __forceinline__ void add_stats(const uint32_t (&v)[32], int cols, float &top, float &sum)
+// Maximum and sum of exp(z - maximum) of 32 logits, of which the first `count`
+// count.  An infinite maximum stands for itself: exp(z) is 0 or infinite.
+__device__ __forceinline__ float2 stats_of(const uint32_t (&v)[32], int count)
 {
-    float m = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        if (i < cols)
-            m = fmaxf(m, __uint_as_float(v[i]));
-    const float now = fmaxf(top, m);
-    const float at = isinf(now) ? 0.f : now;  // an infinite maximum: exp(z) itself, 0 or infinite
-    if (now != top) {
-        sum *= isinf(top) ? 0.f : exp_fast(top - at);
-        top = now;
-    }
+        if (i < count)
+            top = fmaxf(top, __uint_as_float(v[i]));
+    const float at = isinf(top) ? 0.f : top;
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-        if (i < cols)
+        if (i < count)
             a += exp_fast(__uint_as_float(v[i]) - at);
-        if (i + 1 < cols)
+        if (i + 1 < count)
             b += exp_fast(__uint_as_float(v[i + 1]) - at);
     }
-    sum += a + b;
+    return make_float2(top, a + b);
+}
+__device__ __forceinline__ float2 join(float2 a, float2 b)
+{
+    const float top = fmaxf(a.x, b.x);
+    return make_float2(top, (a.x == top ? a.y : a.y * exp_fast(a.x - top)) +
+                                (b.x == top ? b.y : b.y * exp_fast(b.x - top)));
 }
 
-template <int E, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ Gemm g)
+// A warp's 32 x 32 fp32 values turned over in its 4 KB of shared memory: from
+// a row a lane to a column a lane.  The 16-byte pieces of a row are swizzled by
+// its number, so neither side meets a bank twice.
+__device__ __forceinline__ void turn_over(uint32_t tile, int lane, uint32_t (&v)[32])
 {
-    using R = Ring<PAIR>;
-    constexpr int kStages = R::stages, kBlocks = PAIR ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        um::store_shared16(tile + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
+                           v[4 * j + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+        v[r] = um::load_shared4(tile + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
+    __syncwarp();
+}
+
+template <int E>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_kernel(const __grid_constant__ Gemm g)
+{
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
-    __shared__ uint64_t bars[2 * kStages + 5];
+    __shared__ uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
-    const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages;
-    const uint32_t acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
+    const uint32_t full = um::smem_addr(bars), empty = full + 8 * kMaxStages;
+    const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? int(um::cluster_rank()) : 0;  // of a pair, block 0 issues the products
+    const int rank = int(um::cluster_rank());  // block 0 of a pair issues the products
+    const int cols_b = g.tile_n / 2, stage_bytes = kABytes + cols_b * kK * 2;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             um::mbar_init(full + 8 * i, 1);
             um::mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(acc_full + 8 * i, 1);
-            um::mbar_init(acc_empty + 8 * i, kOutWarps * kBlocks);
+            um::mbar_init(acc_empty + 8 * i, kOutWarps * 2);
         }
         um::mbar_init(drained, 1);
         um::fence_barrier_init();
@@ -173,15 +190,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         um::prefetch_map(&g.b);
     }
     if (warp == 1)
-        um::tmem_alloc<PAIR>(um::smem_addr(&tmem_slot), kTmemCols);
+        um::tmem_alloc(um::smem_addr(&tmem_slot), kTmemCols);
     um::fence_before();
     __syncthreads();
-    if constexpr (PAIR)
-        um::cluster_sync();
+    um::cluster_sync();
     um::fence_after();
     const uint32_t tmem = tmem_slot;
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
-    const int64_t first = blockIdx.x / kBlocks, step = gridDim.x / kBlocks;
+    const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -189,40 +205,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             bool ok = true;
             for (int64_t i = first; ok && i < works; i += step) {
                 const Work w = work_of(g, i);
-                const int m = (w.m * kBlocks + rank) * kM, n = w.n * kN + rank * R::rows_b;
+                const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
                 for (int s = w.s0; s < w.s1; ++s) {
                     if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
                         break;
-                    const uint32_t a = ring + stage * R::bytes, b = a + R::a_bytes;
-                    uint32_t bar = full + 8 * stage;
+                    const uint32_t a = ring + stage * stage_bytes, b = a + kABytes;
+                    // Both blocks' copies count at block 0's barrier.
+                    const uint32_t bar = um::cluster_addr(full + 8 * stage, 0);
                     if (rank == 0)
-                        um::mbar_expect(bar, R::bytes * kBlocks);
-                    if constexpr (PAIR)
-                        bar = um::cluster_addr(bar, 0);
-                    auto load = [&](uint32_t dst, const CUtensorMap *map, int x, int y) {
-                        if constexpr (PAIR)
-                            um::tma_load_2d_pair(dst, map, x, y, bar);
-                        else
-                            um::tma_load_2d(dst, map, x, y, bar);
-                    };
+                        um::mbar_expect(full + 8 * stage, uint32_t(stage_bytes) * 2);
                     if (g.a_mn) {
                         for (int j = 0; j < kM / 64; ++j)
-                            load(a + j * 64 * kK * 2, &g.a, m + j * 64, s * kK);
+                            um::tma_load_2d(a + j * 64 * kK * 2, &g.a, m + j * 64, s * kK, bar);
                     } else {
-                        load(a, &g.a, s * kK, m);
+                        um::tma_load_2d(a, &g.a, s * kK, m, bar);
                     }
                     if (g.b_mn) {
-                        for (int j = 0; j < R::rows_b / 64; ++j)
-                            load(b + j * 64 * kK * 2, &g.b, n + j * 64, s * kK);
+                        for (int j = 0; j < cols_b / 64; ++j)
+                            um::tma_load_2d(b + j * 64 * kK * 2, &g.b, n + j * 64, s * kK, bar);
                     } else {
-                        load(b, &g.b, s * kK, n);
+                        um::tma_load_2d(b, &g.b, s * kK, n, bar);
                     }
-                    if (++stage == kStages)
+                    if (++stage == g.stages)
                         stage = 0, ++turns;
                 }
             }
-            if (!ok && rank == 0) {  // wait for the copies in flight before the block's memory goes
-                for (int k = 0; k < kStages; ++k) {
+            if (!ok && rank == 0) {  // wait for the copies in flight before the pair's memory goes
+                for (int k = 0; k < g.stages; ++k) {
                     const int times = turns + (k < stage);
                     const uint64_t t0 = um::now_ns();
                     while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) &&
@@ -234,13 +243,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = um::instr_desc(kM * kBlocks, kN, g.a_mn, g.b_mn);
+            const uint32_t idesc = um::instr_desc(kM * 2, g.tile_n, g.a_mn, g.b_mn);
             const uint32_t a_step = (g.a_mn ? 2048 : 32) >> 4, b_step = (g.b_mn ? 2048 : 32) >> 4;  // 16 of the sum
             int stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int64_t i = first; ok && i < works; i += step) {
                 const Work w = work_of(g, i);
-                if (!(ok = um::mbar_wait<PAIR>(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
+                if (!(ok = um::mbar_wait<true>(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
                     break;
                 um::fence_after();
                 const uint32_t d = tmem + buf * kN;
@@ -248,24 +257,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     if (!(ok = um::mbar_wait(full + 8 * stage, phase, &gave_up, g.wait_ns)))
                         break;
                     um::fence_after();
-                    const uint32_t base = ring + stage * R::bytes;
+                    const uint32_t base = ring + stage * stage_bytes;
                     const uint64_t a = um::operand_desc(base, g.a_mn, 64 * kK * 2);
-                    const uint64_t b = um::operand_desc(base + R::a_bytes, g.b_mn, 64 * kK * 2);
+                    const uint64_t b = um::operand_desc(base + kABytes, g.b_mn, 64 * kK * 2);
 #pragma unroll
                     for (int k = 0; k < kK / 16; ++k)
-                        um::mma_bf16<PAIR>(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
-                    um::mma_commit<PAIR>(empty + 8 * stage);
-                    if (++stage == kStages)
+                        um::mma_bf16(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
+                    um::mma_commit(empty + 8 * stage);
+                    if (++stage == g.stages)
                         stage = 0, phase ^= 1;
                 }
                 if (ok)
-                    um::mma_commit<PAIR>(acc_full + 8 * buf);
+                    um::mma_commit(acc_full + 8 * buf);
                 if (++buf == 2)
                     buf = 0, buf_phase ^= 1;
             }
             if (!ok) {  // wait for the products in flight before the accumulators and tiles go
                 g_timed_out = 1;
-                um::mma_commit<PAIR>(drained);
+                um::mma_commit(drained);
                 const uint64_t t0 = um::now_ns();
                 while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < g.wait_ns) {
                 }
@@ -273,63 +282,90 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         __syncwarp();
     } else {
-        // A warp reads the tensor-memory lanes of its number modulo 4; the first four warps take the tile's
-        // columns 0 to 127, the others the rest.
+        // A warp reads the tensor-memory lanes of its number modulo 4; the first four warps take the first half of
+        // the tile's columns, the others the rest.
         const int quarter = warp % 4, half = (warp - 2) / 4;
-        const uint32_t out = ring + kRingBytes + (warp - 2) * kOutBytes;
-        const uint32_t out_row = out + lane * 128;
-        const uint32_t acc_done = PAIR ? um::cluster_addr(acc_empty, 0) : acc_empty;
+        const int half_n = E == kStore ? g.tile_n / 2 : (g.tile_n / 2 + 31) / 32 * 32;
+        const int width = half ? g.tile_n - half_n : half_n;
+        const uint32_t outs = ring + kRingBytes, out = outs + (warp - 2) * kOutTile, out_row = out + lane * 128;
+        const uint32_t acc_done = um::cluster_addr(acc_empty, 0);
         int buf = 0, buf_phase = 0;
         for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
-            const int64_t m0 = (int64_t(w.m) * kBlocks + rank) * kM + quarter * 32, m = m0 + lane;
-            const int64_t n0 = int64_t(w.n) * kN + half * (kN / 2);
-            const bool row = m < g.M;
-            int64_t y = -1;
-            float lse = 0.f, scale = 0.f;
-            if ((E == kStats || E == kDz) && row)
-                y = g.y.get(m);
-            if (E == kDz && row && y != -1) {
-                lse = g.lse[m];
-                scale = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[m];
-            }
-            const bool ready = um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
-            if (!__all_sync(0xffffffffu, ready)) {
+            const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
+            const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
+            const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
+            bool ready = um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
+            // The warps that meet at a barrier below leave together, should one's wait have run out.
+            ready = E == kStats ? um::group_all(1 + half, 128, ready) : __all_sync(0xffffffffu, ready);
+            if (!ready) {
                 g_timed_out = 1;
                 break;
             }
             um::fence_after();
-            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + buf * kN + half * (kN / 2);
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
+            const uint32_t d = tmem + (uint32_t(quarter * 32) << 16) + buf * kN + half * half_n;
+            float2 stats[4];  // kStats: of the lane's token in each 32 columns
+#pragma unroll
             for (int c = 0; c < kN / 2; c += 32) {
                 const int64_t n = n0 + c;
-                const int cols = int(min(int64_t(32), g.N - n));
+                const int cols = c < width ? int(min(int64_t(32), g.N - n)) : 0;
+                stats[c / 32] = make_float2(-INFINITY, 0.f);
                 if (cols <= 0)
-                    break;
+                    continue;
                 uint32_t v[32];
                 um::tmem_load32(d + c, v);
                 um::tmem_wait_load();
-                if (E == kStats) {
-                    add_stats(v, cols, top, sum);
-                    const int64_t at = y - n;
-                    if (at >= 0 && at < cols) {
-                        uint32_t z = v[0];
-#pragma unroll
-                        for (int j = 1; j < 32; ++j)
-                            z = j == int(at) ? v[j] : z;
-                        g.zy[m] = __uint_as_float(z);
+                if (E == kStats || E == kDz) {
+                    if (E == kDz) {
+                        if (lane == 0)
+                            um::stores_read();
+                        __syncwarp();
                     }
-                    continue;
-                }
-                // The tile of 128-byte rows that these columns belong to, and their place in it.
-                const bool begins = E == kAdd || c % 64 == 0, ends = E == kAdd || c % 64 == 32 || n + 32 >= g.N;
-                if (begins && (E == kAdd || g.out_tiles)) {
+                    turn_over(out, lane, v);  // v[r]: vocabulary row m0 + r of the lane's token
+                    const int64_t t = n + lane;
+                    const int64_t y = lane < cols ? g.y.get(t) : -1, at = y - g.v0 - m0;
+                    if (E == kStats) {
+                        stats[c / 32] = stats_of(v, rows);
+                        if (at >= 0 && at < rows) {
+                            uint32_t z = v[0];
+#pragma unroll
+                            for (int j = 1; j < 32; ++j)
+                                z = j == int(at) ? v[j] : z;
+                            g.zy[t] = __uint_as_float(z);
+                        }
+                    } else {
+                        float lse = 0.f, scale = 0.f;
+                        if (y != -1) {
+                            lse = g.lse[t];
+                            scale = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[t];
+                        }
+                        uint32_t f[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float x[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                x[k] = y == -1 ? 0.f
+                                               : (exp_fast(__uint_as_float(v[j + k]) - lse) -
+                                                  (j + k == at ? 1.f : 0.f)) * scale;
+                            f[j / 2] = tide::pack_bf16(x[0], x[1]);
+                        }
+                        // 64-byte rows, their 16-byte pieces swizzled by bits 1 and 2 of the row's number
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            um::store_shared16(out + lane * 64 + ((j ^ (lane / 2 & 3)) << 4), f[4 * j], f[4 * j + 1],
+                                               f[4 * j + 2], f[4 * j + 3]);
+                        um::fence_copies();
+                        __syncwarp();
+                        if (lane == 0 && rows > 0) {
+                            um::tma_store_2d(&g.c, out, int(m0), int(n));
+                            um::stores_end();
+                        }
+                    }
+                } else if (E == kAdd) {
                     if (lane == 0)
                         um::stores_read();
                     __syncwarp();
-                }
-                if (E == kAdd) {
                     if (w.s0 == w.s1) {  // a last piece shorter than its splits: nothing was summed
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -339,26 +375,39 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     for (int j = 0; j < 8; ++j)
                         um::store_shared16(out_row + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
                                            v[4 * j + 3]);
+                    um::fence_copies();
+                    __syncwarp();
+                    if (lane == 0 && rows > 0) {
+                        if (g.first)
+                            um::tma_store_3d(&g.c, out, int(n), int(m0), w.split);
+                        else
+                            um::tma_add_3d(&g.c, out, int(n), int(m0), w.split);
+                        um::stores_end();
+                    }
                 } else {
                     uint32_t f[16];
-                    const int64_t at = y - g.v0 - n;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float x[2] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1])};
-                        if (E == kDz) {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                x[k] = y == -1 ? 0.f : (exp_fast(x[k] - lse) - (j + k == at ? 1.f : 0.f)) * scale;
+                    for (int j = 0; j < 16; ++j)
+                        f[j] = tide::pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    if (g.out_tiles) {  // 64 columns a tile
+                        if (c % 64 == 0) {
+                            if (lane == 0)
+                                um::stores_read();
+                            __syncwarp();
                         }
-                        f[j / 2] = tide::pack_bf16(x[0], x[1]);
-                    }
-                    if (E == kDz || g.out_tiles) {
-                        const int k = c % 64 / 8;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            um::store_shared16(out_row + (((k + j) ^ (lane & 7)) << 4), f[4 * j], f[4 * j + 1],
-                                               f[4 * j + 2], f[4 * j + 3]);
-                    } else if (row) {
+                            um::store_shared16(out_row + (((c % 64 / 8 + j) ^ (lane & 7)) << 4), f[4 * j],
+                                               f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        if (c % 64 == 32 || n + 32 >= g.N) {
+                            um::fence_copies();
+                            __syncwarp();
+                            if (lane == 0 && rows > 0) {
+                                um::tma_store_2d(&g.c, out, int(n0 + c / 64 * 64), int(m0));
+                                um::stores_end();
+                            }
+                        }
+                    } else if (lane < rows) {
                         uint16_t *p = reinterpret_cast<uint16_t *>(g.out) + m * g.out_stride + n;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -366,30 +415,29 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                                 p[j] = uint16_t(f[j / 2] >> (16 * (j % 2)));
                     }
                 }
-                if (ends && (E == kAdd || g.out_tiles)) {
-                    um::fence_copies();
-                    __syncwarp();
-                    if (lane == 0 && m0 < g.M) {
-                        if (E != kAdd)
-                            um::tma_store_2d(&g.c, out, int(n0 + c / 64 * 64), int(m0));
-                        else if (g.first)
-                            um::tma_store_3d(&g.c, out, int(n), int(m0), w.split);
-                        else
-                            um::tma_add_3d(&g.c, out, int(n), int(m0), w.split);
-                        um::stores_end();
-                    }
-                }
             }
             um::fence_before();
             __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR)
-                    um::mbar_arrive_cluster(acc_done + 8 * buf);
-                else
-                    um::mbar_arrive(acc_done + 8 * buf);
+            if (lane == 0)
+                um::mbar_arrive_cluster(acc_done + 8 * buf);
+            if (E == kStats) {  // join the block's four shares of 32 rows, 32 tokens a warp
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    um::store_shared8(out + (k * 32 + lane) * 8, __float_as_uint(stats[k].x),
+                                      __float_as_uint(stats[k].y));
+                um::group_sync(1 + half, 128);
+                float2 s = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t x, y;
+                    um::load_shared8(outs + (half * 4 + k) * kOutTile + (quarter * 32 + lane) * 8, x, y);
+                    s = join(s, make_float2(__uint_as_float(x), __uint_as_float(y)));
+                }
+                const int64_t t = n0 + quarter * 32 + lane;
+                if (quarter * 32 < width && t < g.N)
+                    g.part[(int64_t(w.m) * 2 + rank) * g.N + t] = s;
+                um::group_sync(1 + half, 128);
             }
-            if (E == kStats && row)
-                g.part[(int64_t(w.n) * 2 + half) * g.M + m] = make_float2(top, sum);
             if (++buf == 2)
                 buf = 0, buf_phase ^= 1;
         }
@@ -399,11 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     um::fence_before();
     __syncthreads();
-    if constexpr (PAIR)
-        um::cluster_sync();
+    um::cluster_sync();
     um::fence_after();
     if (warp == 1)
-        um::tmem_free<PAIR>(tmem, kTmemCols);
+        um::tmem_free(tmem, kTmemCols);
 }
 
 // Rows that the tiled copies cannot take (16-byte boundaries) go into the
@@ -424,10 +471,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
     __shared__ float2 slices[256];
     const int row = threadIdx.x % rows, slice = threadIdx.x / rows, n = 256 / rows;
     const int64_t t = int64_t(blockIdx.x) * rows + row;
-    auto join = [](float2 a, float2 b) {
-        const float top = fmaxf(a.x, b.x);
-        return make_float2(top, (a.x == top ? a.y : a.y * expf(a.x - top)) + (b.x == top ? b.y : b.y * expf(b.x - top)));
-    };
     float2 s = make_float2(-INFINITY, 0.f);
     if (t < T) {
         int i = slice;
@@ -455,28 +498,27 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
     loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - zy[t];
 }
 
-// dx = sum of the splits, in order; four elements a thread where the rows allow.
-template <int N>
+// dx [T, H] = sum of the splits, in order, of the sums [H][T] (rows `pitch`
+// apart): blocks of 32 x 32, turned over in shared memory.
 __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, int64_t pitch,
                                                     bf16 *out, int64_t stride)
 {
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * N, n = T * pitch, t = i / pitch, c = i - t * pitch;
-    if (i >= n || c >= H)
-        return;
-    float x[N] = {};
-    for (int s = 0; s < splits; ++s) {
-        if constexpr (N == 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(acc + s * n + i);
-            x[0] += a.x, x[1] += a.y, x[2] += a.z, x[3] += a.w;
-        } else {
-            x[0] += acc[s * n + i];
-        }
+    __shared__ float tile[32][33];
+    const int64_t t0 = int64_t(blockIdx.x) * 32, h0 = int64_t(blockIdx.y) * 32;
+    const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
+#pragma unroll
+    for (int r = row; r < 32; r += 8) {
+        float x = 0.f;
+        if (t0 + lane < T && h0 + r < H)
+            for (int s = 0; s < splits; ++s)
+                x += acc[(s * H + h0 + r) * pitch + t0 + lane];
+        tile[r][lane] = x;
     }
-    if constexpr (N == 4)
-        *reinterpret_cast<uint2 *>(out + t * stride + c) =
-            make_uint2(tide::pack_bf16(x[0], x[1]), tide::pack_bf16(x[2], x[3]));
-    else
-        out[t * stride + c] = __float2bfloat16_rn(x[0]);
+    __syncthreads();
+#pragma unroll
+    for (int r = row; r < 32; r += 8)
+        if (t0 + r < T && h0 + lane < H)
+            out[(t0 + r) * stride + h0 + lane] = __float2bfloat16_rn(tile[lane][r]);
 }
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -554,28 +596,29 @@ bool rows_aligned(const void *p, int64_t stride, int64_t rows)
 }
 
 tide_status_t encode(CUtensorMap *map, CUtensorMapDataType type, int rank, void *p, const cuuint64_t *dims,
-                     const cuuint64_t *strides, const cuuint32_t *box)
+                     const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle)
 {
     const EncodeTiled enc = encode_tiled();
     if (!enc)
         return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r = enc(map, type, cuuint32_t(rank), p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled: %d", int(r));
     return TIDE_OK;
 }
 
-// Tensor map whose copies are `box_rows` rows of 64 columns; what lies outside
-// the matrix reads as 0 and is not written.
-tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows)
+// Tensor map whose copies are `box_rows` rows of `box_cols` columns (64, or 32);
+// what lies outside the matrix reads as 0 and is not written.
+tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows, int box_cols = 64)
 {
     const cuuint64_t dims[2] = {cuuint64_t(m.cols), cuuint64_t(m.rows)};
     const cuuint64_t strides[1] = {cuuint64_t(m.rows < 2 ? (m.cols + 7) / 8 * 16 : m.stride * 2)};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box);
+    const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box,
+                  box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // The same for fp32 sums [splits][rows][cols] with rows `pitch` apart: 32 rows of 32 columns.
@@ -584,7 +627,7 @@ tide_status_t make_acc_map(CUtensorMap *map, float *p, int64_t splits, int64_t r
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(splits)};
     const cuuint64_t strides[2] = {cuuint64_t(pitch * 4), cuuint64_t(rows * pitch * 4)};
     const cuuint32_t box[3] = {32, 32, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box);
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 Gemm base(const tide_ce_t *ce)
@@ -596,48 +639,21 @@ Gemm base(const tide_ce_t *ce)
     return g;
 }
 
-// Whether pairs of blocks take a product of M rows.  A pair's tiles have 256
-// rows, a block's 128: where M just spills into another 256, single blocks
-// waste less.
-bool takes_pairs(int64_t M)
+// Columns of a tile and shares of the sum for a product of `tiles_m` row tiles,
+// N columns and `steps` steps: those of the shortest rounds.  A step takes as
+// long as its columns and a fixed part, no less than what the fetch of its rows
+// takes, and a tile's end another four steps'.
+void shape_of(int64_t tiles_m, int64_t N, int64_t steps, int unit, int max_splits, int *tile_n, int *splits)
 {
-    const int64_t blocks = (M + kM - 1) / kM, pairs = (blocks + 1) / 2;
-    return pairs * 2 * 9 <= blocks * 10;
-}
-
-template <int E, bool PAIR>
-tide_status_t launch_as(Gemm &g, const Mat &a, const Mat &b, const char *what, cudaStream_t st)
-{
-    constexpr int blocks = PAIR ? 2 : 1;
-    g.tiles_m = int((g.M + blocks * kM - 1) / (blocks * kM));
-    g.tiles_n = int((g.N + kN - 1) / kN);
-    tide_status_t s = make_map(&g.a, a, g.a_mn ? kK : kM);
-    if (!s)
-        s = make_map(&g.b, b, g.b_mn ? kK : Ring<PAIR>::rows_b);
-    if (!s && (E == kDz || E == kStore) && g.out_tiles)
-        s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32);
-    if (s)
-        return s;
-    auto kernel = gemm_kernel<E, PAIR>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e == cudaSuccess) {
-        const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(unsigned(std::min<int64_t>(works, tide::op_sm_count() / blocks)) * blocks);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
-        cfg.stream = st;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = blocks;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kernel, g);
-    }
-    if (e != cudaSuccess)
-        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return tide::op_launched(what);
+    const int64_t pairs = std::max(tide::op_sm_count() / 2, 1);
+    double best = 1e300;
+    for (int n = kN; n >= std::min(unit, 128); n -= unit)
+        for (int s = 1; s <= max_splits && s <= steps / 4 + 1; ++s) {
+            const int64_t rounds = (tiles_m * ((N + n - 1) / n) * s + pairs - 1) / pairs;
+            const double time = double(rounds) * (double(steps) / s * (std::max(n, 96) + 32) + 4 * 288);
+            if (time < best * 0.99)
+                best = time, *tile_n = n, *splits = s;
+        }
 }
 
 // C[M, N] = sum over k of A B.  An operand is given with its rows as the tile's
@@ -650,7 +666,26 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
     g.N = b_mn ? b.cols : b.rows;
     g.K = a_mn ? a.rows : a.cols;
     g.steps = int((g.K + kK - 1) / kK);
-    return takes_pairs(g.M) ? launch_as<E, true>(g, a, b, what, st) : launch_as<E, false>(g, a, b, what, st);
+    g.tiles_m = int((g.M + 2 * kM - 1) / (2 * kM));
+    if (E != kAdd)
+        shape_of(g.tiles_m, g.N, g.steps, E == kStore ? 128 : 32, 1, &g.tile_n, &g.splits);
+    g.tiles_n = int((g.N + g.tile_n - 1) / g.tile_n);
+    g.stages = std::min(kMaxStages, kRingBytes / (kABytes + g.tile_n / 2 * kK * 2));
+    tide_status_t s = make_map(&g.a, a, a_mn ? kK : kM);
+    if (!s)
+        s = make_map(&g.b, b, b_mn ? kK : g.tile_n / 2);
+    if (!s && E == kStore && g.out_tiles)
+        s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32);
+    if (s)
+        return s;
+    auto kernel = gemm_kernel<E>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
+    const unsigned grid = unsigned(std::min<int64_t>(works, std::max(tide::op_sm_count() / 2, 1))) * 2;
+    kernel<<<grid, kThreads, kSmemBytes, st>>>(g);
+    return tide::op_launched(what);
 }
 
 // Where a call's scratch data lies in its workspace, in bytes.
@@ -658,7 +693,7 @@ struct Layout {
     int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
     int64_t part = 0, zy = 0;           // loss
     int64_t dz = 0, acc = 0, piece = 0, acc_pitch = 0;  // gradient
-    int splits = 1;
+    int splits = 1, tile_n = kN;        // of dx
     int64_t bytes = 0;
     int64_t take(int64_t n)
     {
@@ -667,27 +702,6 @@ struct Layout {
         return at;
     }
 };
-
-// Shares of the vocabulary piece that dx's sum is split into: its tiles alone
-// may be fewer than the SMs, or just over a whole number of rounds.
-int splits_of(const tide_ce_t *ce, int64_t piece)
-{
-    const int blocks = takes_pairs(ce->tokens) ? 2 : 1;
-    const int64_t sms = std::max(tide::op_sm_count() / blocks, 1);
-    const int64_t tiles = ((ce->tokens + blocks * kM - 1) / (blocks * kM)) * ((ce->hidden + kN - 1) / kN);
-    const int64_t steps = (std::min(piece, ce->vocab) + kK - 1) / kK;
-    int best = 1;
-    double best_time = 1e30;
-    for (int s = 1; s <= 64 && s <= steps / 4 + 1; ++s) {
-        if (s > 1 && ce->tokens * ce->hidden * 4 * s > kPieceBytes)
-            break;
-        // rounds of steps, and two steps' time a share for the tile's own start and end
-        const double time = double((tiles * s + sms - 1) / sms) * (double(steps) / s + 4.0);
-        if (time < best_time * 0.98)
-            best = s, best_time = time;
-    }
-    return best;
-}
 
 Layout layout_of(const tide_ce_t *ce, bool grad)
 {
@@ -699,12 +713,14 @@ Layout layout_of(const tide_ce_t *ce, bool grad)
         l.w = l.take(ce->vocab * l.pitch * 2);
     if (grad) {
         l.piece = piece_of(ce);
-        l.splits = splits_of(ce, l.piece);
+        l.acc_pitch = round_up(ce->tokens, 4);
+        const int64_t sum = std::max<int64_t>(l.acc_pitch * ce->hidden * 4, 1);
+        shape_of((ce->hidden + 2 * kM - 1) / (2 * kM), ce->tokens, (std::min(l.piece, ce->vocab) + kK - 1) / kK, 32,
+                 int(std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, kPieceBytes / sum))), &l.tile_n, &l.splits);
         l.dz = l.take(ce->tokens * l.piece * 2);
-        l.acc_pitch = round_up(ce->hidden, 4);
-        l.acc = l.take(ce->tokens * l.acc_pitch * 4 * l.splits);
+        l.acc = l.take(sum * l.splits);
     } else {
-        l.part = l.take((ce->vocab + kN - 1) / kN * 2 * ce->tokens * 8);
+        l.part = l.take((ce->vocab + 2 * kM - 1) / (2 * kM) * 2 * ce->tokens * 8);
         l.zy = l.take(ce->tokens * 4);
     }
     l.bytes = std::max<int64_t>(l.bytes, 256);
@@ -763,13 +779,13 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
     Gemm g = base(ce);
     g.part = reinterpret_cast<float2 *>(ws + l.part);
     g.zy = reinterpret_cast<float *>(ws + l.zy);
-    s = launch<kStats>(g, x, false, w, false, "ce_loss", st);
+    s = launch<kStats>(g, w, false, x, false, "ce_loss", st);
     if (s)
         return s;
     int rows = 32;  // few rows: more slices of each
     while (rows > 1 && rows / 2 >= T)
         rows /= 2;
-    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_n, T, rows, g.zy, g.y, loss, lse);
+    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_m, T, rows, g.zy, g.y, loss, lse);
     return tide::op_launched("ce_loss: join");
 }
 
@@ -823,30 +839,25 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
         Gemm g = base(ce);
         g.v0 = v0;
         g.lse = lse, g.dloss = dloss;
-        g.out = dz, g.out_stride = l.piece, g.out_tiles = 1;
-        s = launch<kDz>(g, x, false, wp, false, "ce_grad: dz", st);
-        if (s)
-            return s;
-        g.first = v0 == 0, g.splits = l.splits;
-        s = make_acc_map(&g.c, acc, l.splits, T, H, l.acc_pitch);
+        s = make_map(&g.c, dzp, 32, 32);
         if (!s)
-            s = launch<kAdd>(g, dzp, false, wp, true, "ce_grad: dx", st);
+            s = launch<kDz>(g, wp, false, x, false, "ce_grad: dz", st);
         if (s)
             return s;
-        g.splits = 1;
+        g.first = v0 == 0, g.splits = l.splits, g.tile_n = l.tile_n;
+        s = make_acc_map(&g.c, acc, l.splits, H, T, l.acc_pitch);
+        if (!s)
+            s = launch<kAdd>(g, wp, true, dzp, false, "ce_grad: dx", st);
+        if (s)
+            return s;
         g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
         g.out_tiles = H % 8 == 0 && rows_aligned(g.out, dweight_stride, V);  // tiles are stored by 16 bytes
         s = launch<kStore>(g, dzp, true, x, true, "ce_grad: dweight", st);
     }
     if (s)
         return s;
-    bf16 *out = static_cast<bf16 *>(dx);
-    if (H % 4 == 0 && op_aligned(dx, 8) && (T < 2 || dx_stride % 4 == 0))
-        round_kernel<4><<<unsigned((T * H / 4 + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, l.acc_pitch, out,
-                                                                          dx_stride);
-    else
-        round_kernel<1><<<unsigned((T * l.acc_pitch + 255) / 256), 256, 0, st>>>(acc, l.splits, T, H, l.acc_pitch, out,
-                                                                                dx_stride);
+    round_kernel<<<dim3(unsigned((T + 31) / 32), unsigned((H + 31) / 32)), 256, 0, st>>>(
+        acc, l.splits, T, H, l.acc_pitch, static_cast<bf16 *>(dx), dx_stride);
     return tide::op_launched("ce_grad: rounding");
 }
 
