@@ -200,18 +200,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0, turns = 0;  // ring position, and how often the ring went round
-            bool ok = true;
-            for (int64_t i = first; ok && i < works; i += step) {
-                const Work w = work_of(g, i);
-                const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
-                for (int s = w.s0; s < w.s1; ++s) {
-                    if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
-                        break;
-                    const uint32_t a = ring + stage * stage_bytes, b = a + kABytes;
-                    // Both blocks' copies count at block 0's barrier.
-                    const uint32_t bar = um::cluster_addr(full + 8 * stage, 0);
+        const bool leader = um::elected();
+        const uint32_t full0 = um::cluster_addr(full, 0);  // both blocks' copies count at block 0's barriers
+        int stage = 0, turns = 0;                          // ring position, and how often the ring went round
+        bool ok = true;
+        for (int64_t i = first; ok && i < works; i += step) {
+            const Work w = work_of(g, i);
+            const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
+            for (int s = w.s0; s < w.s1; ++s) {
+                if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
+                    break;
+                if (leader) {
+                    const uint32_t a = ring + stage * stage_bytes, b = a + kABytes, bar = full0 + 8 * stage;
                     if (rank == 0)
                         um::mbar_expect(full + 8 * stage, uint32_t(stage_bytes) * 2);
                     if (g.a_mn) {
@@ -226,25 +226,28 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                     } else {
                         um::tma_load_2d(b, &g.b, s * kK, n, bar);
                     }
-                    if (++stage == g.stages)
-                        stage = 0, ++turns;
                 }
+                __syncwarp();
+                if (++stage == g.stages)
+                    stage = 0, ++turns;
             }
-            if (!ok && rank == 0) {  // wait for the copies in flight before the pair's memory goes
-                for (int k = 0; k < g.stages; ++k) {
-                    const int times = turns + (k < stage);
-                    const uint64_t t0 = um::now_ns();
-                    while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) &&
-                           um::now_ns() - t0 < g.wait_ns) {
-                    }
+        }
+        if (!ok && rank == 0 && leader) {  // wait for the copies in flight before the pair's memory goes
+            for (int k = 0; k < g.stages; ++k) {
+                const int times = turns + (k < stage);
+                const uint64_t t0 = um::now_ns();
+                while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) && um::now_ns() - t0 < g.wait_ns) {
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const bool leader = um::elected();
             const uint32_t idesc = um::instr_desc(kM * 2, g.tile_n, g.a_mn, g.b_mn);
             const uint32_t a_step = (g.a_mn ? 2048 : 32) >> 4, b_step = (g.b_mn ? 2048 : 32) >> 4;  // 16 of the sum
+            const uint64_t a0 = um::operand_desc(ring, g.a_mn, 64 * kK * 2);
+            const uint64_t b0 = um::operand_desc(ring + kABytes, g.b_mn, 64 * kK * 2);
             int stage = 0, phase = 0, buf = 0, buf_phase = 0;
             bool ok = true;
             for (int64_t i = first; ok && i < works; i += step) {
@@ -257,22 +260,24 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                     if (!(ok = um::mbar_wait(full + 8 * stage, phase, &gave_up, g.wait_ns)))
                         break;
                     um::fence_after();
-                    const uint32_t base = ring + stage * stage_bytes;
-                    const uint64_t a = um::operand_desc(base, g.a_mn, 64 * kK * 2);
-                    const uint64_t b = um::operand_desc(base + kABytes, g.b_mn, 64 * kK * 2);
+                    if (leader) {
+                        const uint32_t at = uint32_t(stage * stage_bytes) >> 4;
 #pragma unroll
-                    for (int k = 0; k < kK / 16; ++k)
-                        um::mma_bf16(d, a + k * a_step, b + k * b_step, idesc, s > w.s0 || k > 0);
-                    um::mma_commit(empty + 8 * stage);
+                        for (int k = 0; k < kK / 16; ++k)
+                            um::mma_bf16(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc, s > w.s0 || k > 0);
+                        um::mma_commit(empty + 8 * stage);
+                    }
+                    __syncwarp();
                     if (++stage == g.stages)
                         stage = 0, phase ^= 1;
                 }
-                if (ok)
+                if (ok && leader)
                     um::mma_commit(acc_full + 8 * buf);
+                __syncwarp();
                 if (++buf == 2)
                     buf = 0, buf_phase ^= 1;
             }
-            if (!ok) {  // wait for the products in flight before the accumulators and tiles go
+            if (!ok && leader) {  // wait for the products in flight before the accumulators and tiles go
                 g_timed_out = 1;
                 um::mma_commit(drained);
                 const uint64_t t0 = um::now_ns();
@@ -295,9 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
             const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
             const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
-            bool ready = um::mbar_wait(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
-            // The warps that meet at a barrier below leave together, should one's wait have run out.
-            ready = E == kStats ? um::group_all(1 + half, 128, ready) : __all_sync(0xffffffffu, ready);
+            bool ready = um::mbar_wait<false, 100>(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
+            if (E == kStats)  // the warps that meet at a barrier below leave together, should one's wait have run out
+                ready = um::group_all(1 + half, 128, ready);
             if (!ready) {
                 g_timed_out = 1;
                 break;

@@ -78,25 +78,41 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Waits until the barrier's phase of this parity is over, for at most
-// budget_ns; gives up at once when another role of the block has.  A wait that
-// runs out raises the block's flag.
-template <bool CLUSTER = false>
+// One lane of the converged warp (always the same one).
+__device__ __forceinline__ bool elected()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+
+// The whole warp waits until the barrier's phase of this parity is over, for at
+// most budget_ns; gives up when another warp of the block has.  A wait that
+// runs out raises the block's flag.  SLEEP ns between tries.
+template <bool CLUSTER = false, int SLEEP = 0>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up, uint64_t budget_ns)
 {
-    auto done = [&] { return CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity); };
+    auto done = [&] { return __all_sync(0xffffffffu, CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)); };
     if (done())
         return true;
     const uint64_t t0 = now_ns();
-    while (!done()) {
-        if (*gave_up)
-            return false;
-        if (now_ns() - t0 > budget_ns) {
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {  // the clock is slower to read than most waits
+            if (done())
+                return true;
+            if (SLEEP)
+                __nanosleep(SLEEP);
+        }
+        if (__any_sync(0xffffffffu, *gave_up || now_ns() - t0 > budget_ns)) {
             *gave_up = 1;
             return false;
         }
     }
-    return true;
 }
 
 // For a pair of blocks that work on one product: the bytes count at a barrier
