@@ -38,7 +38,7 @@ constexpr int kABytes = kM * kK * 2;        // a block's share of a step: its ro
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 10;
 constexpr int kOutWarps = 8;                // warps that work on results
-constexpr int kOutTile = 4096;              // a warp's 32 rows of 128 bytes on their way out
+constexpr int kOutTile = 4096;              // a warp's results on their way out
 constexpr int kSmemBytes = kRingBytes + kOutWarps * kOutTile + 1024;  // 1024: alignment
 constexpr int kThreads = 64 + 32 * kOutWarps;                         // fetch, products, results
 constexpr int kTmemCols = 512;                       // two accumulators of 256 columns
@@ -290,16 +290,32 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         // A warp reads the tensor-memory lanes of its number modulo 4; the first four warps take the first half of
         // the tile's columns, the others the rest.
         const int quarter = warp % 4, half = (warp - 2) / 4;
-        const int half_n = E == kStore ? g.tile_n / 2 : (g.tile_n / 2 + 31) / 32 * 32;
+        const int half_n = (g.tile_n / 2 + 31) / 32 * 32;
         const int width = half ? g.tile_n - half_n : half_n;
-        const uint32_t outs = ring + kRingBytes, out = outs + (warp - 2) * kOutTile, out_row = out + lane * 128;
+        const uint32_t outs = ring + kRingBytes, out = outs + (warp - 2) * kOutTile;
         const uint32_t acc_done = um::cluster_addr(acc_empty, 0);
-        int buf = 0, buf_phase = 0;
+        int buf = 0, buf_phase = 0, out_at = 0;
         for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
             const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
             const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
+            // The lane's token of each 32 columns: target (as a row of the warp's), lse and factor, before the wait.
+            int64_t hit[4];
+            float lse[4], scale[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t t = n0 + k * 32 + lane;
+                int64_t y = -1;
+                if ((E == kStats || E == kDz) && k * 32 < width && t < g.N)
+                    y = g.y.get(t);
+                hit[k] = y - g.v0 - m0;
+                lse[k] = INFINITY, scale[k] = 0.f;  // an ignored token: exp(z - lse) = 0
+                if (E == kDz && y != -1) {
+                    lse[k] = g.lse[t];
+                    scale[k] = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[t];
+                }
+            }
             bool ready = um::mbar_wait<false, 100>(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
             if (E == kStats)  // the warps that meet at a barrier below leave together, should one's wait have run out
                 ready = um::group_all(1 + half, 128, ready);
@@ -320,56 +336,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 uint32_t v[32];
                 um::tmem_load32(d + c, v);
                 um::tmem_wait_load();
-                if (E == kStats || E == kDz) {
-                    if (E == kDz) {
-                        if (lane == 0)
-                            um::stores_read();
-                        __syncwarp();
-                    }
+                if (E == kStats) {
                     turn_over(out, lane, v);  // v[r]: vocabulary row m0 + r of the lane's token
-                    const int64_t t = n + lane;
-                    const int64_t y = lane < cols ? g.y.get(t) : -1, at = y - g.v0 - m0;
-                    if (E == kStats) {
-                        stats[c / 32] = stats_of(v, rows);
-                        if (at >= 0 && at < rows) {
-                            uint32_t z = v[0];
+                    const int64_t at = hit[c / 32];
+                    stats[c / 32] = stats_of(v, rows);
+                    if (at >= 0 && at < rows) {
+                        uint32_t z = v[0];
 #pragma unroll
-                            for (int j = 1; j < 32; ++j)
-                                z = j == int(at) ? v[j] : z;
-                            g.zy[t] = __uint_as_float(z);
-                        }
-                    } else {
-                        float lse = 0.f, scale = 0.f;
-                        if (y != -1) {
-                            lse = g.lse[t];
-                            scale = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[t];
-                        }
-                        uint32_t f[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            float x[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                x[k] = y == -1 ? 0.f
-                                               : (exp_fast(__uint_as_float(v[j + k]) - lse) -
-                                                  (j + k == at ? 1.f : 0.f)) * scale;
-                            f[j / 2] = tide::pack_bf16(x[0], x[1]);
-                        }
-                        // 64-byte rows, their 16-byte pieces swizzled by bits 1 and 2 of the row's number
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            um::store_shared16(out + lane * 64 + ((j ^ (lane / 2 & 3)) << 4), f[4 * j], f[4 * j + 1],
-                                               f[4 * j + 2], f[4 * j + 3]);
-                        um::fence_copies();
-                        __syncwarp();
-                        if (lane == 0 && rows > 0) {
-                            um::tma_store_2d(&g.c, out, int(m0), int(n));
-                            um::stores_end();
-                        }
+                        for (int j = 1; j < 32; ++j)
+                            z = j == int(at) ? v[j] : z;
+                        g.zy[n + lane] = __uint_as_float(z);
                     }
                 } else if (E == kAdd) {
                     if (lane == 0)
-                        um::stores_read();
+                        um::stores_read<0>();
                     __syncwarp();
                     if (w.s0 == w.s1) {  // a last piece shorter than its splits: nothing was summed
 #pragma unroll
@@ -378,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        um::store_shared16(out_row + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                                           v[4 * j + 3]);
+                        um::store_shared16(out + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+                                           v[4 * j + 2], v[4 * j + 3]);
                     um::fence_copies();
                     __syncwarp();
                     if (lane == 0 && rows > 0) {
@@ -390,34 +370,62 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                         um::stores_end();
                     }
                 } else {
-                    uint32_t f[16];
+                    // Tiles of 32 rows of 64 bytes, two in turn, their 16-byte pieces swizzled by bits 1 and 2 of the
+                    // row's number.
+                    const uint32_t tile = out + out_at * (kOutTile / 2);
+                    if (E == kDz || g.out_tiles) {
+                        if (lane == 0)
+                            um::stores_read<1>();
+                        __syncwarp();
+                    }
+                    if (E == kDz) {
+                        // Lane j has the target, lse and factor of token n + j; everyone gets them in turn.
+                        const int64_t at = hit[c / 32];
+                        const uint32_t hits = __ballot_sync(0xffffffffu, at >= 0 && at < 32);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        f[j] = tide::pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                    if (g.out_tiles) {  // 64 columns a tile
-                        if (c % 64 == 0) {
-                            if (lane == 0)
-                                um::stores_read();
-                            __syncwarp();
+                        for (int j = 0; j < 32; ++j) {
+                            const float l = __shfl_sync(0xffffffffu, lse[c / 32], j);
+                            const float f = __shfl_sync(0xffffffffu, scale[c / 32], j);
+                            float p = exp_fast(__uint_as_float(v[j]) - l);
+                            if (hits >> j & 1)  // this token's target is one of the warp's rows
+                                p -= __shfl_sync(0xffffffffu, int(at), j) == lane ? 1.f : 0.f;
+                            v[j] = __float_as_uint(p * f);
                         }
+                        // A row of the tile is a token: two bytes of it a lane.
+                        const uint32_t piece = uint32_t(lane) / 8, byte = uint32_t(lane) % 8 * 2;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            um::store_shared16(out_row + (((c % 64 / 8 + j) ^ (lane & 7)) << 4), f[4 * j],
-                                               f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-                        if (c % 64 == 32 || n + 32 >= g.N) {
-                            um::fence_copies();
-                            __syncwarp();
-                            if (lane == 0 && rows > 0) {
-                                um::tma_store_2d(&g.c, out, int(n0 + c / 64 * 64), int(m0));
-                                um::stores_end();
-                            }
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t f = tide::pack_bf16(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                            const uint32_t to = tile + j * 64 + ((piece ^ (j / 2 & 3)) << 4) + byte;
+                            um::store_shared2(to, uint16_t(f));
+                            um::store_shared2(to + 64, uint16_t(f >> 16));
                         }
-                    } else if (lane < rows) {
-                        uint16_t *p = reinterpret_cast<uint16_t *>(g.out) + m * g.out_stride + n;
+                    } else {
+                        uint32_t f[16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < cols)
-                                p[j] = uint16_t(f[j / 2] >> (16 * (j % 2)));
+                        for (int j = 0; j < 16; ++j)
+                            f[j] = tide::pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        if (g.out_tiles) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                um::store_shared16(tile + lane * 64 + ((j ^ (lane / 2 & 3)) << 4), f[4 * j],
+                                                   f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        } else if (lane < rows) {
+                            uint16_t *p = reinterpret_cast<uint16_t *>(g.out) + m * g.out_stride + n;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j < cols)
+                                    p[j] = uint16_t(f[j / 2] >> (16 * (j % 2)));
+                        }
+                    }
+                    if (E == kDz || g.out_tiles) {
+                        um::fence_copies();
+                        __syncwarp();
+                        if (lane == 0 && rows > 0) {
+                            um::tma_store_2d(&g.c, tile, int(E == kDz ? m0 : n), int(E == kDz ? n : m0));
+                            um::stores_end();
+                        }
+                        out_at ^= 1;
                     }
                 }
             }
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 buf = 0, buf_phase ^= 1;
         }
         if (lane == 0)
-            um::stores_read();
+            um::stores_read<0>();
         __syncwarp();
     }
     um::fence_before();
@@ -514,9 +522,21 @@ __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits
 #pragma unroll
     for (int r = row; r < 32; r += 8) {
         float x = 0.f;
-        if (t0 + lane < T && h0 + r < H)
-            for (int s = 0; s < splits; ++s)
-                x += acc[(s * H + h0 + r) * pitch + t0 + lane];
+        if (t0 + lane < T && h0 + r < H) {
+            const float *p = acc + (h0 + r) * pitch + t0 + lane;
+            int s = 0;
+            for (; s + 4 <= splits; s += 4) {
+                float a[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    a[k] = p[(s + k) * H * pitch];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x += a[k];
+            }
+            for (; s < splits; ++s)
+                x += p[s * H * pitch];
+        }
         tile[r][lane] = x;
     }
     __syncthreads();
@@ -680,7 +700,7 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
     if (!s)
         s = make_map(&g.b, b, b_mn ? kK : g.tile_n / 2);
     if (!s && E == kStore && g.out_tiles)
-        s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32);
+        s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32, 32);
     if (s)
         return s;
     auto kernel = gemm_kernel<E>;
@@ -787,8 +807,8 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
     s = launch<kStats>(g, w, false, x, false, "ce_loss", st);
     if (s)
         return s;
-    int rows = 32;  // few rows: more slices of each
-    while (rows > 1 && rows / 2 >= T)
+    int rows = 32;  // few rows: more slices of each, and more blocks
+    while (rows > 1 && T / rows < 128)
         rows /= 2;
     join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_m, T, rows, g.zy, g.y, loss, lse);
     return tide::op_launched("ce_loss: join");

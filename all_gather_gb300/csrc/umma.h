@@ -146,10 +146,18 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src,
                  : "memory");
 }
 __device__ __forceinline__ void stores_end() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Until the thread's stores have read their shared memory.
-__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// Until all but the thread's last N groups have read their shared memory.
+template <int N>
+__device__ __forceinline__ void stores_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 // Makes shared memory that this thread wrote visible to the copy engine.
 __device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void store_shared2(uint32_t addr, uint16_t a)
+{
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(a) : "memory");
+}
 __device__ __forceinline__ uint32_t load_shared4(uint32_t addr)
 {
     uint32_t x;
