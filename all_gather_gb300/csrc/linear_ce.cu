@@ -89,11 +89,12 @@ struct Gemm {
 
 // exp of a difference of logits.  The difference is taken before the factor
 // log2(e): folded into one multiply-add with a rounded log2(e) z it would be
-// off by the rounding of z, and overflow for the largest z.
+// off by the rounding of z, and overflow for the largest z.  Results under
+// 2^-126 are 0 (ftz), which spares the instruction's scaling of subnormals.
 __device__ __forceinline__ float exp_fast(float x)
 {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
     return y;
 }
 
@@ -386,10 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                         for (int j = 0; j < 32; ++j) {
                             const float l = __shfl_sync(0xffffffffu, lse[c / 32], j);
                             const float f = __shfl_sync(0xffffffffu, scale[c / 32], j);
-                            float p = exp_fast(__uint_as_float(v[j]) - l);
-                            if (hits >> j & 1)  // this token's target is one of the warp's rows
-                                p -= __shfl_sync(0xffffffffu, int(at), j) == lane ? 1.f : 0.f;
-                            v[j] = __float_as_uint(p * f);
+                            v[j] = __float_as_uint(exp_fast(__uint_as_float(v[j]) - l) * f);
+                        }
+                        if (hits) {  // targets among the warp's rows: apart, so that the loop above has no branches
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (hits >> j & 1) {
+                                    const int r = __shfl_sync(0xffffffffu, int(at), j);
+                                    const float f = __shfl_sync(0xffffffffu, scale[c / 32], j);
+                                    if (lane == r)
+                                        v[j] = __float_as_uint(__uint_as_float(v[j]) - f);
+                                }
                         }
                         // A row of the tile is a token: two bytes of it a lane.
                         const uint32_t piece = uint32_t(lane) / 8, byte = uint32_t(lane) % 8 * 2;
