@@ -532,17 +532,8 @@ __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits
         float x = 0.f;
         if (t0 + lane < T && h0 + r < H) {
             const float *p = acc + (h0 + r) * pitch + t0 + lane;
-            int s = 0;
-            for (; s + 4 <= splits; s += 4) {
-                float a[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    a[k] = p[(s + k) * H * pitch];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x += a[k];
-            }
-            for (; s < splits; ++s)
+#pragma unroll 4
+            for (int s = 0; s < splits; ++s)
                 x += p[s * H * pitch];
         }
         tile[r][lane] = x;

@@ -11,14 +11,18 @@
 // hold values a hundred times its others, which a common integer step would
 // round to zero.
 //
-// Both are bound by memory (bf16: 8 bytes an element forward, 10 backward).
-// Sixteen lanes take one block, eight elements each, so a block's maximum is
-// four exchanges and every load and store is a whole vector; a warp takes two
-// neighbouring blocks of a row.  Rows that are not on 16-byte boundaries, or
-// whose length is not a multiple of 8, take the same kernel with
-// element-wise loads and stores.
+// Both are bound by memory (bf16: 8 bytes an element forward, 10 backward); the
+// forward has some 25 instructions an element to hide under it, so it works on
+// pairs of values where it can.  Sixteen lanes take one block, eight elements
+// each, so a block's maximum is four exchanges and every load and store is a
+// whole vector; a warp takes two neighbouring blocks of a row and steps down
+// the rows, with the next row's loads on their way.  Rows that are not on
+// 16-byte boundaries, or whose length is not a multiple of 8, take the same
+// kernel with single elements, 16 columns apart in a lane.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "ops_internal.h"
 
@@ -34,36 +38,91 @@ using tide::to_f32;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = TIDE_CKPT8_BLOCK;
+constexpr int kWarpsPerSm = 64;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // 1 / (1 + exp(-g)) from exp(-|g|), so that nothing overflows and small
-// results keep their precision.  bf16 takes the fast exponential and division
-// (about 2^-21), far below its rounding.
+// results keep their precision.  bf16 takes the fast exponential and reciprocal
+// (about 2^-22), far below its rounding; the exponential is made 2^24 too large
+// and scaled back, which keeps results under 2^-126 without the instruction's
+// own scaling.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float g)
 {
-    const float e = sizeof(T) == 2 ? __expf(-fabsf(g)) : expf(-fabsf(g));
-    const float n = g < 0.f ? e : 1.f;
-    return sizeof(T) == 2 ? __fdividef(n, 1.f + e) : n / (1.f + e);
-}
-
-// Eight elements from column `c`; columns from `cols` on read as 0.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_cols(const T *row, int64_t c, int64_t cols, float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = 0.f;
-    if constexpr (VEC) {
-        if (c < cols)
-            load8(row + c, v);
+    if constexpr (sizeof(T) == 2) {
+        float e, r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(fabsf(g), -1.4426950408889634f, 24.f)));
+        e *= 5.9604644775390625e-8f;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return (g < 0.f ? e : 1.f) * r;
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                v[i] = to_f32(row[c + i]);
+        const float e = expf(-fabsf(g));
+        return (g < 0.f ? e : 1.f) / (1.f + e);
     }
 }
+
+// A lane's eight elements of a block as they lie in memory.  VEC: columns c to
+// c + 7; otherwise c, c + 16, ..., c + 112.  Columns from `cols` on read as 0.
+template <bool VEC, typename T>
+struct Eight {
+    float f[8];
+    __device__ __forceinline__ void load(const T *row, int64_t c, int64_t cols)
+    {
+        if constexpr (VEC) {
+            if (c < cols) {
+                load8(row + c, f);
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = !VEC && c + 16 * i < cols ? to_f32(row[c + 16 * i]) : 0.f;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = f[i];
+    }
+    // Largest magnitude as bits; infinities and NaN are above all others.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            t = max(t, __float_as_uint(f[i]) & 0x7fffffffu);
+        return t;
+    }
+};
+template <>
+struct Eight<true, __nv_bfloat16> {  // packed until they are needed
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *row, int64_t c, int64_t cols)
+    {
+        w = c < cols ? *reinterpret_cast<const uint4 *>(row + c) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ uint32_t top() const
+    {
+        auto mag = [](uint32_t x) {
+            x &= 0x7fff7fffu;
+            return *reinterpret_cast<const __nv_bfloat162 *>(&x);
+        };
+        const __nv_bfloat162 t =
+            __hmax2_nan(__hmax2_nan(mag(w.x), mag(w.y)), __hmax2_nan(mag(w.z), mag(w.w)));
+        const uint32_t b = *reinterpret_cast<const uint32_t *>(&t);
+        return max(b << 16, b & 0xffff0000u);
+    }
+};
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_cols(T *row, int64_t c, int64_t cols, const float (&v)[8])
 {
@@ -73,8 +132,8 @@ __device__ __forceinline__ void store_cols(T *row, int64_t c, int64_t cols, cons
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                row[c + i] = from_f32<T>(v[i]);
+            if (c + 16 * i < cols)
+                row[c + 16 * i] = from_f32<T>(v[i]);
     }
 }
 template <bool VEC>
@@ -87,8 +146,8 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t *row, int64_t c, int64
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                w[i / 4] |= uint32_t(row[c + i]) << (8 * (i % 4));
+            if (c + 16 * i < cols)
+                w[i / 4] |= uint32_t(row[c + 16 * i]) << (8 * (i % 4));
     }
     return make_uint2(w[0], w[1]);
 }
@@ -101,53 +160,46 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int64_t c, int64_t col
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c + i < cols)
-                row[c + i] = uint8_t((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+            if (c + 16 * i < cols)
+                row[c + 16 * i] = uint8_t((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
     }
 }
 
-// Codes of a lane's eight values and the exponent of their block (16 lanes).
-__device__ __forceinline__ uint2 encode(const float (&v)[8], int &exponent)
+__device__ __forceinline__ uint32_t block_max(uint32_t x)
 {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
 #pragma unroll
     for (int o = 8; o > 0; o /= 2)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    bool odd = top >= kInfBits;  // infinities or NaN in the block: they do not count
-    if (__any_sync(0xffffffffu, odd)) {
-        top = 0;
+        x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// Codes of a lane's eight values and the exponent of their block (16 lanes),
+// whose largest magnitude is `top`.
+__device__ __forceinline__ uint2 encode(float (&v)[8], uint32_t top, int &exponent)
+{
+    if (__any_sync(0xffffffffu, top >= kInfBits)) {  // infinities or NaN: they do not count, and become NaN
+        uint32_t t = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-            top = max(top, b < kInfBits ? b : 0u);
+            t = max(t, b < kInfBits ? b : 0u);
+            if (b >= kInfBits)
+                v[i] = __int_as_float(0x7fffffff);
         }
-#pragma unroll
-        for (int o = 8; o > 0; o /= 2)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = block_max(t);
     }
     // amax = f 2^(E - 127), 1 <= f < 2, and 448 = 1.75 2^8: e - 127 = E - 127 - 8, one more if f > 1.75.
     // Subnormal amax has E = 0 and ends at the smallest exponent either way.
-    int e = int(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
-    e = top == 0 ? 127 : max(e, 1);
+    const int e = top == 0 ? 127 : max(int((top + 0x1fffffu) >> 23) - 8, 1);
     exponent = e;
     const float scale = __uint_as_float(uint32_t(254 - e) << 23);  // 2^(127 - e), e in [1, 247]
     uint32_t w[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float x = v[4 * k + i];
-            y[i] = x * scale;
-            if (odd && (__float_as_uint(x) & 0x7fffffffu) >= kInfBits)
-                y[i] = __int_as_float(0x7fffffff);
-        }
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-        w[k] = lo | hi << 16;
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * k + 1] * scale), "f"(v[4 * k] * scale));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * k + 3] * scale), "f"(v[4 * k + 2] * scale));
+        w[k] = uint32_t(hi) << 16 | lo;
     }
     return make_uint2(w[0], w[1]);
 }
@@ -167,7 +219,9 @@ __device__ __forceinline__ void decode(uint2 q, int exponent, float (&v)[8])
 
 template <typename T>
 struct SwigluArgs {
-    int64_t rows, cols, blocks, pairs;  // blocks of a row, and pairs of blocks
+    int64_t rows, cols;
+    int64_t row_step;   // rows from one of a warp to its next
+    int blocks, pairs;  // blocks of a row, and pairs of blocks
     const T *gate, *up, *dh;
     int64_t gate_stride, up_stride, dh_stride;
     T *h, *dgate, *dup;
@@ -175,68 +229,102 @@ struct SwigluArgs {
     uint8_t *g8, *ge, *u8, *ue;
 };
 
+// A lane's place: its warp's first row, its block and its first column.
+struct Place {
+    int64_t row;
+    int block;
+    int64_t c;
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ Place place_of(const SwigluArgs<T> &a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    Place p;
+    p.row = warp / a.pairs;
+    p.block = 2 * int(warp - p.row * a.pairs) + lane / 16;
+    p.c = int64_t(p.block) * kBlock + (VEC ? 8 : 1) * (lane % 16);
+    return p;
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) swiglu_forward_kernel(const SwigluArgs<T> a)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (item >= a.rows * a.pairs)
+    const Place p = place_of<VEC>(a);
+    if (p.row >= a.row_step)
         return;
-    const int64_t row = item / a.pairs, b = 2 * (item - row * a.pairs) + lane / 16;
-    const int64_t c = b * kBlock + 8 * (lane % 16);
-    float g[8], u[8], h[8];
-    load_cols<VEC>(a.gate + row * a.gate_stride, c, a.cols, g);
-    load_cols<VEC>(a.up + row * a.up_stride, c, a.cols, u);
-    int eg, eu;
-    const uint2 qg = encode(g, eg), qu = encode(u, eu);
+    const bool writes = threadIdx.x % 16 == 0 && p.block < a.blocks;
+    Eight<VEC, T> gate, up;
+    gate.load(a.gate + p.row * a.gate_stride, p.c, a.cols);
+    up.load(a.up + p.row * a.up_stride, p.c, a.cols);
+    for (int64_t row = p.row; row < a.rows; row += a.row_step) {
+        float g[8], u[8], h[8];
+        gate.get(g);
+        up.get(u);
+        const uint32_t tg = block_max(gate.top()), tu = block_max(up.top());
+        const int64_t next = row + a.row_step;
+        if (next < a.rows) {
+            gate.load(a.gate + next * a.gate_stride, p.c, a.cols);
+            up.load(a.up + next * a.up_stride, p.c, a.cols);
+        }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        h[i] = g[i] * sigmoid<T>(g[i]) * u[i];
-    store_cols<VEC>(a.h + row * a.h_stride, c, a.cols, h);
-    store_codes<VEC>(a.g8 + row * a.cols, c, a.cols, qg);
-    store_codes<VEC>(a.u8 + row * a.cols, c, a.cols, qu);
-    if (lane % 16 == 0 && b < a.blocks) {
-        a.ge[row * a.blocks + b] = uint8_t(eg);
-        a.ue[row * a.blocks + b] = uint8_t(eu);
+        for (int i = 0; i < 8; ++i)
+            h[i] = g[i] * sigmoid<T>(g[i]) * u[i];
+        store_cols<VEC>(a.h + row * a.h_stride, p.c, a.cols, h);
+        int eg, eu;
+        const uint2 qg = encode(g, tg, eg), qu = encode(u, tu, eu);
+        store_codes<VEC>(a.g8 + row * a.cols, p.c, a.cols, qg);
+        store_codes<VEC>(a.u8 + row * a.cols, p.c, a.cols, qu);
+        if (writes) {
+            a.ge[row * a.blocks + p.block] = uint8_t(eg);
+            a.ue[row * a.blocks + p.block] = uint8_t(eu);
+        }
     }
 }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluArgs<T> a)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (item >= a.rows * a.pairs)
+    const Place p = place_of<VEC>(a);
+    if (p.row >= a.row_step || p.block >= a.blocks)
         return;
-    const int64_t row = item / a.pairs, b = 2 * (item - row * a.pairs) + lane / 16;
-    const int64_t c = b * kBlock + 8 * (lane % 16);
-    if (b >= a.blocks)
-        return;
-    float g[8], u[8], d[8], x[8];
-    const uint2 qg = load_codes<VEC>(a.g8 + row * a.cols, c, a.cols);
-    const uint2 qu = load_codes<VEC>(a.u8 + row * a.cols, c, a.cols);
-    load_cols<VEC>(a.dh + row * a.dh_stride, c, a.cols, d);
-    decode(qg, a.ge[row * a.blocks + b], g);
-    decode(qu, a.ue[row * a.blocks + b], u);
-    float s[8];
+    Eight<VEC, T> dh;
+    uint2 qg, qu;
+    int eg, eu;
+    auto load = [&](int64_t row) {
+        qg = load_codes<VEC>(a.g8 + row * a.cols, p.c, a.cols);
+        qu = load_codes<VEC>(a.u8 + row * a.cols, p.c, a.cols);
+        dh.load(a.dh + row * a.dh_stride, p.c, a.cols);
+        eg = a.ge[row * a.blocks + p.block];
+        eu = a.ue[row * a.blocks + p.block];
+    };
+    load(p.row);
+    for (int64_t row = p.row; row < a.rows; row += a.row_step) {
+        float g[8], u[8], d[8], x[8], s[8];
+        dh.get(d);
+        decode(qg, eg, g);
+        decode(qu, eu, u);
+        if (row + a.row_step < a.rows)
+            load(row + a.row_step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        s[i] = sigmoid<T>(g[i]);
-        x[i] = d[i] * u[i] * s[i] * __fmaf_rn(g[i], 1.f - s[i], 1.f);
+        for (int i = 0; i < 8; ++i) {
+            s[i] = sigmoid<T>(g[i]);
+            x[i] = d[i] * u[i] * s[i] * __fmaf_rn(g[i], 1.f - s[i], 1.f);
+        }
+        store_cols<VEC>(a.dgate + row * a.dgate_stride, p.c, a.cols, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s[i] *= g[i];
+            x[i] = d[i] * s[i];
+        }
+        store_cols<VEC>(a.dup + row * a.dup_stride, p.c, a.cols, x);
+        if (!a.h)
+            continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = s[i] * u[i];
+        store_cols<VEC>(a.h + row * a.h_stride, p.c, a.cols, x);
     }
-    store_cols<VEC>(a.dgate + row * a.dgate_stride, c, a.cols, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        s[i] *= g[i];
-        x[i] = d[i] * s[i];
-    }
-    store_cols<VEC>(a.dup + row * a.dup_stride, c, a.cols, x);
-    if (!a.h)
-        return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        x[i] = s[i] * u[i];
-    store_cols<VEC>(a.h + row * a.h_stride, c, a.cols, x);
 }
 
 size_t elem_bytes(int dtype) { return dtype == TIDE_DTYPE_F32 ? 4 : 2; }
@@ -249,7 +337,7 @@ tide_status_t check_shape(int64_t rows, int64_t cols, int32_t dtype, const tide_
         return op_fail(TIDE_ERR_INVALID_ARG, "rows %lld, cols %lld", (long long)rows, (long long)cols);
     if (rows > 0 && cols > 0) {
         const int64_t pairs = (cols + 2 * kBlock - 1) / (2 * kBlock);
-        if (pairs > int64_t(0x7fffffff) * kWarps / rows)
+        if (pairs > 0x3fffffff || pairs > int64_t(0x7fffffff) * kWarps / rows)
             return op_fail(TIDE_ERR_INVALID_ARG, "rows %lld x cols %lld is over one launch", (long long)rows,
                            (long long)cols);
         if (!ckpt || !ckpt->gate_codes || !ckpt->gate_exps || !ckpt->up_codes || !ckpt->up_exps)
@@ -288,8 +376,11 @@ SwigluArgs<T> make_args(int64_t rows, int64_t cols, const tide_ckpt8_t *k)
     SwigluArgs<T> a = {};
     a.rows = rows;
     a.cols = cols;
-    a.blocks = (cols + kBlock - 1) / kBlock;
+    a.blocks = int((cols + kBlock - 1) / kBlock);
     a.pairs = (a.blocks + 1) / 2;
+    // As many warps as the SMs hold, and some more to even out their ends.
+    const int64_t warps = int64_t(std::max(tide::op_sm_count(), 1)) * kWarpsPerSm;
+    a.row_step = std::min(rows, std::max<int64_t>(1, warps / a.pairs));
     a.g8 = static_cast<uint8_t *>(k->gate_codes);
     a.ge = static_cast<uint8_t *>(k->gate_exps);
     a.u8 = static_cast<uint8_t *>(k->up_codes);
@@ -305,7 +396,7 @@ tide_status_t forward(int64_t rows, int64_t cols, bool vec, const void *gate, in
     a.gate = static_cast<const T *>(gate), a.gate_stride = gs;
     a.up = static_cast<const T *>(up), a.up_stride = us;
     a.h = static_cast<T *>(h), a.h_stride = hs;
-    const unsigned grid = unsigned((a.rows * a.pairs + kWarps - 1) / kWarps);
+    const unsigned grid = unsigned((a.row_step * a.pairs + kWarps - 1) / kWarps);
     if (vec)
         swiglu_forward_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
     else
@@ -322,7 +413,7 @@ tide_status_t backward(int64_t rows, int64_t cols, bool vec, const tide_ckpt8_t 
     a.dgate = static_cast<T *>(dgate), a.dgate_stride = gs;
     a.dup = static_cast<T *>(dup), a.dup_stride = us;
     a.h = static_cast<T *>(h), a.h_stride = hs;
-    const unsigned grid = unsigned((a.rows * a.pairs + kWarps - 1) / kWarps);
+    const unsigned grid = unsigned((a.row_step * a.pairs + kWarps - 1) / kWarps);
     if (vec)
         swiglu_backward_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
     else
