@@ -702,13 +702,12 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
         s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32, 32);
     if (s)
         return s;
-    auto kernel = gemm_kernel<E>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const cudaError_t e = tide::op_allow_smem<gemm_kernel<E>>(kSmemBytes);
     if (e != cudaSuccess)
         return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
     const unsigned grid = unsigned(std::min<int64_t>(works, std::max(tide::op_sm_count() / 2, 1))) * 2;
-    kernel<<<grid, kThreads, kSmemBytes, st>>>(g);
+    gemm_kernel<E><<<grid, kThreads, kSmemBytes, st>>>(g);
     return tide::op_launched(what);
 }
 

@@ -48,6 +48,21 @@ inline int op_sm_count()
     return n;
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory; asked for once on each device.
+template <auto KERNEL>
+cudaError_t op_allow_smem(int bytes)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1))
+        return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // Sizes are kept below 2^60 elements so that byte offsets fit 64 bits.
 constexpr int64_t kMaxExtent = int64_t(1) << 60;
 inline bool op_extent_ok(int64_t n, int64_t stride)

@@ -15,7 +15,7 @@
 // 16 consecutive columns; unrotated columns: 16 consecutive), one unit a lane,
 // so the rotation needs no exchange between lanes and the two sums of a head
 // are butterflies over G = 4 to 32 lanes.  A warp takes 32 / G heads of one
-// token at a time (a step).  Persistent warps copy their next kDepth - 1 steps
+// token at a time (a step).  Persistent warps copy their next three (or two) steps
 // into shared memory (cp.async, every lane its own vectors, so nothing waits
 // for another warp), which keeps enough bytes on their way from few warps with
 // many registers; a token's angles come along with its first step.  Products
@@ -131,7 +131,14 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
     return d;
 }
 
-constexpr int kDepth = 4;  // steps of a warp's ring
+// Steps of a warp's ring: four, or three where four would leave a SM one block
+// instead of two (fp32 gradients, 18 KB a warp: 1003 tokens of 7 + 3 heads of 96
+// 14.3 us with four, 12.3 with three).
+template <typename T>
+__host__ __device__ constexpr int depth_of(int tensors)
+{
+    return sizeof(T) * tensors > 4 ? 3 : 4;
+}
 
 __device__ __forceinline__ void copy16(void *dst, const void *src)
 {
@@ -282,11 +289,11 @@ __device__ __forceinline__ float inv_rms(const f32x2 (&v)[8], float inv_d, float
     return rsqrtf(__fmaf_rn(group_sum<G>(lo_of(ss) + hi_of(ss)), inv_d, eps));
 }
 
-// Bytes of a warp's ring: kDepth steps of `tensors` tensors, and kDepth rows of angles.
+// Bytes of a warp's ring: steps of `tensors` tensors, and as many rows of angles.
 template <typename T>
 __host__ __device__ constexpr int ring_bytes(int tensors, int G)
 {
-    return kDepth * (tensors * 2 * int(sizeof(T)) / 2 * 512 + G * 64);
+    return depth_of<T>(tensors) * (tensors * 2 * int(sizeof(T)) / 2 * 512 + G * 64);
 }
 
 // Pieces that a lane's unit does not have read as 0 out of every slot.
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_forward_kernel(const QkArgs<T>
 {
     constexpr int kRows = 32 / G;       // heads of a step
     constexpr int kVec = sizeof(T) / 2; // 16-byte pieces of eight elements
-    constexpr int kSlot = 2 * kVec * 32;
+    constexpr int kSlot = 2 * kVec * 32, kDepth = depth_of<T>(1);
     extern __shared__ uint4 smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
     uint4 *ring = smem + warp * (ring_bytes<T>(1, G) / 16);
@@ -442,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_backward_kernel(const QkArgs<T
 {
     constexpr int kRows = 32 / G;
     constexpr int kVec = sizeof(T) / 2;
-    constexpr int kSlot = 4 * kVec * 32;
+    constexpr int kSlot = 4 * kVec * 32, kDepth = depth_of<T>(2);
     extern __shared__ uint4 smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / G;
     uint4 *ring = smem + warp * (ring_bytes<T>(2, G) / 16);
@@ -736,9 +743,11 @@ __global__ void __launch_bounds__(1024) qk_weight_grad_kernel(const float *pq, i
         return;
     const int col = blockIdx.x * 32 + threadIdx.x;
     float x = 0.f;
-    if (col < D)
+    if (col < D) {
+#pragma unroll 4
         for (int i = threadIdx.y; i < n; i += 32)
             x += p[int64_t(i) * D + col];
+    }
     sums[threadIdx.y][threadIdx.x] = x;
     __syncthreads();
     x = group_sum<32>(sums[threadIdx.x][threadIdx.y]);
@@ -910,30 +919,29 @@ QkArgs<T> make_args(const tide_qk_t *qk)
     return a;
 }
 
-// Starts a vector kernel with its rings, after letting it have them (once for
-// each kernel and device).
-template <typename K, typename T>
-tide_status_t launch_vec(K kernel, const QkArgs<T> &a, unsigned grid, int smem, const char *what, cudaStream_t st)
+// Starts a vector kernel with its rings.
+template <auto KERNEL, typename T>
+tide_status_t launch_vec(const QkArgs<T> &a, unsigned grid, int smem, const char *what, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = tide::op_allow_smem<KERNEL>(smem);
     if (e != cudaSuccess)
         return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    kernel<<<grid, kThreads, size_t(smem), st>>>(a);
+    KERNEL<<<grid, kThreads, size_t(smem), st>>>(a);
     return tide::op_launched(what);
 }
 template <typename T, int G>
 tide_status_t launch_forward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
 {
     constexpr int smem = kWarps * ring_bytes<T>(1, G);
-    return il ? launch_vec(qk_forward_kernel<T, G, true>, a, grid, smem, "qk_norm_rope", st)
-              : launch_vec(qk_forward_kernel<T, G, false>, a, grid, smem, "qk_norm_rope", st);
+    return il ? launch_vec<qk_forward_kernel<T, G, true>>(a, grid, smem, "qk_norm_rope", st)
+              : launch_vec<qk_forward_kernel<T, G, false>>(a, grid, smem, "qk_norm_rope", st);
 }
 template <typename T, int G>
 tide_status_t launch_backward(const QkArgs<T> &a, bool il, unsigned grid, cudaStream_t st)
 {
     constexpr int smem = std::max(kWarps * ring_bytes<T>(2, G), kThreads * 16 * 4);
-    return il ? launch_vec(qk_backward_kernel<T, G, true>, a, grid, smem, "qk_norm_rope_grad", st)
-              : launch_vec(qk_backward_kernel<T, G, false>, a, grid, smem, "qk_norm_rope_grad", st);
+    return il ? launch_vec<qk_backward_kernel<T, G, true>>(a, grid, smem, "qk_norm_rope_grad", st)
+              : launch_vec<qk_backward_kernel<T, G, false>>(a, grid, smem, "qk_norm_rope_grad", st);
 }
 
 template <typename T, bool GRAD>
