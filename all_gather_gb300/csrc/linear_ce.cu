@@ -5,9 +5,17 @@
 //   dz = (exp(z - lse) - [v = target]) dloss,  dx = dz W,  dW = dz^T x
 //
 // The loss takes tiles of the logits as they are made: each tile leaves, for
-// each of its rows, its maximum m and sum s of exp(z - m), and a second kernel
-// joins a row's pairs in a fixed order.  The gradient makes the logits again,
-// a piece of the vocabulary at a time, and keeps only that piece's dz.
+// each of its tokens, its maximum m and sum s of exp(z - m), and a second kernel
+// joins a token's pairs in a fixed order.  That kernel also takes the target's
+// logit, as a dot product of its own: the tensor cores cut the last bits of
+// their sums towards zero, which averages out in lse but not in a single logit.
+//
+// The gradient makes the logits again, a piece of the vocabulary at a time, and
+// keeps only that piece's dz, rounded to bf16: the products take operands of
+// one type, and its error is that of rounding x or W once more.  dz is kept
+// relative to the largest |dloss|, which the results are multiplied by at their
+// end: the usual dloss, the same for all tokens, would else put its own
+// rounding on every term, where it does not average out.
 //
 // All products run in one persistent kernel, a pair of blocks (two SMs) on tiles
 // of 256 rows and up to 256 columns: in each block a thread fetches 64 columns
@@ -78,8 +86,7 @@ struct Gemm {
     int64_t v0;          // first vocabulary row of this piece
     Targets y;
     float2 *part;        // kStats: [128-row tiles][N]
-    float *zy;           // kStats: logit of the target
-    const float *lse, *dloss;
+    const float *lse, *dloss, *unit;  // unit: what dz is relative to
     bf16 *out;           // kStore
     int64_t out_stride;
     int out_tiles;       // its rows are on 16-byte boundaries: stored as tiles
@@ -295,26 +302,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         const int width = half ? g.tile_n - half_n : half_n;
         const uint32_t outs = ring + kRingBytes, out = outs + (warp - 2) * kOutTile;
         const uint32_t acc_done = um::cluster_addr(acc_empty, 0);
+        const float unit = E == kStore ? *g.unit : 1.f;
         int buf = 0, buf_phase = 0, out_at = 0;
         for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
             const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
             const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
-            // The lane's token of each 32 columns: target (as a row of the warp's), lse and factor, before the wait.
+            // kDz: the lane's token of each 32 columns, before the wait: target (as a row of the warp's), lse, factor.
             int64_t hit[4];
             float lse[4], scale[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t t = n0 + k * 32 + lane;
                 int64_t y = -1;
-                if ((E == kStats || E == kDz) && k * 32 < width && t < g.N)
+                if (E == kDz && k * 32 < width && t < g.N)
                     y = g.y.get(t);
                 hit[k] = y - g.v0 - m0;
                 lse[k] = INFINITY, scale[k] = 0.f;  // an ignored token: exp(z - lse) = 0
                 if (E == kDz && y != -1) {
                     lse[k] = g.lse[t];
-                    scale[k] = y == -2 ? __int_as_float(0x7fffffff) : g.dloss[t];
+                    scale[k] = y == -2 ? __int_as_float(0x7fffffff) : __fdiv_rn(g.dloss[t], *g.unit);
                 }
             }
             bool ready = um::mbar_wait<false, 100>(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
@@ -339,15 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 um::tmem_wait_load();
                 if (E == kStats) {
                     turn_over(out, lane, v);  // v[r]: vocabulary row m0 + r of the lane's token
-                    const int64_t at = hit[c / 32];
                     stats[c / 32] = stats_of(v, rows);
-                    if (at >= 0 && at < rows) {
-                        uint32_t z = v[0];
-#pragma unroll
-                        for (int j = 1; j < 32; ++j)
-                            z = j == int(at) ? v[j] : z;
-                        g.zy[n + lane] = __uint_as_float(z);
-                    }
                 } else if (E == kAdd) {
                     if (lane == 0)
                         um::stores_read<0>();
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                         uint32_t f[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            f[j] = tide::pack_bf16(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            f[j] = tide::pack_bf16(__uint_as_float(v[2 * j]) * unit, __uint_as_float(v[2 * j + 1]) * unit);
                         if (g.out_tiles) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -484,14 +484,44 @@ __global__ void __launch_bounds__(256) align_kernel(const bf16 *in, int64_t stri
             out[r * pitch + c] = in[r * stride + c];
 }
 
-// Joins a row's pairs (maximum, sum): `rows` neighbouring rows a block, 256 /
-// rows slices of the column tiles each.
-__global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles, int64_t T, int rows, const float *zy,
-                                                   Targets y, float *loss, float *lse)
+// Joins the pairs (maximum, sum) of `rows` neighbouring tokens a block, 256 /
+// rows slices of the vocabulary tiles each, and takes their targets' logits, a
+// warp a token or, where there are fewer than eight, a part of one.
+__global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles, int64_t T, int rows, Targets y,
+                                                   const bf16 *x, int64_t x_stride, const bf16 *w, int64_t w_stride,
+                                                   int H, float *loss, float *lse)
 {
     __shared__ float2 slices[256];
+    __shared__ float dots[32];
+    const int64_t t0 = int64_t(blockIdx.x) * rows;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int parts = rows < 8 ? 8 / rows : 1;
+    for (int r = rows < 8 ? warp % rows : warp; r < rows; r += 8) {
+        const int64_t v = t0 + r < T ? y.get(t0 + r) : -1;
+        float z = 0.f;
+        if (v >= 0) {
+            const bf16 *a = x + (t0 + r) * x_stride, *b = w + v * w_stride;
+            const int mine = rows < 8 ? warp / rows : 0, whole = H / 8;
+            for (int i = mine * 32 + lane; i < whole; i += 32 * parts) {
+                float p[8], q[8];
+                tide::load8(a + 8 * i, p);
+                tide::load8(b + 8 * i, q);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    z = __fmaf_rn(p[k], q[k], z);
+            }
+            if (mine == 0 && whole * 8 + lane < H)
+                z = __fmaf_rn(tide::to_f32(a[whole * 8 + lane]), tide::to_f32(b[whole * 8 + lane]), z);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0)
+            dots[rows < 8 ? warp : r] = z;
+    }
+
     const int row = threadIdx.x % rows, slice = threadIdx.x / rows, n = 256 / rows;
-    const int64_t t = int64_t(blockIdx.x) * rows + row;
+    const int64_t t = t0 + row;
     float2 s = make_float2(-INFINITY, 0.f);
     if (t < T) {
         int i = slice;
@@ -511,19 +541,52 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
         if (slice < half)
             slices[threadIdx.x] = s = join(s, slices[threadIdx.x + half * rows]);
     }
+    __syncthreads();
     if (slice > 0 || t >= T)
         return;
+    float z = dots[row];
+    for (int k = 1; k < parts; ++k)  // rows < 8: parts of a token are `rows` warps apart
+        z += dots[row + k * rows];
     const float l = logf(s.y) + (isinf(s.x) ? 0.f : s.x);
     const int64_t v = y.get(t);
     lse[t] = l;
-    loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - zy[t];
+    loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - z;
+}
+
+// What dz is kept relative to: the largest finite |dloss| of the tokens that
+// count, 1 if that is 0.
+__global__ void __launch_bounds__(1024) unit_kernel(const float *dloss, Targets y, int64_t T, float *unit)
+{
+    __shared__ float tops[32];
+    float top = 0.f;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+        const float d = fabsf(dloss[t]);
+        if (d > top && d < INFINITY && y.get(t) != -1)
+            top = d;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (threadIdx.x % 32 == 0)
+        tops[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = tops[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (threadIdx.x == 0)
+            *unit = top > 0.f ? top : 1.f;
+    }
 }
 
 // dx [T, H] = sum of the splits, in order, of the sums [H][T] (rows `pitch`
-// apart): blocks of 32 x 32, turned over in shared memory.
+// apart), times their unit: blocks of 32 x 32, turned over in shared memory.
 __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits, int64_t T, int64_t H, int64_t pitch,
-                                                    bf16 *out, int64_t stride)
+                                                    const float *unit_, bf16 *out, int64_t stride)
 {
+    const float unit = *unit_;
     __shared__ float tile[32][33];
     const int64_t t0 = int64_t(blockIdx.x) * 32, h0 = int64_t(blockIdx.y) * 32;
     const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
@@ -536,7 +599,7 @@ __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits
             for (int s = 0; s < splits; ++s)
                 x += p[s * H * pitch];
         }
-        tile[r][lane] = x;
+        tile[r][lane] = x * unit;
     }
     __syncthreads();
 #pragma unroll
@@ -714,8 +777,8 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
 // Where a call's scratch data lies in its workspace, in bytes.
 struct Layout {
     int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
-    int64_t part = 0, zy = 0;           // loss
-    int64_t dz = 0, acc = 0, piece = 0, acc_pitch = 0;  // gradient
+    int64_t part = 0;                   // loss
+    int64_t dz = 0, acc = 0, unit = 0, piece = 0, acc_pitch = 0;  // gradient
     int splits = 1, tile_n = kN;        // of dx
     int64_t bytes = 0;
     int64_t take(int64_t n)
@@ -742,9 +805,9 @@ Layout layout_of(const tide_ce_t *ce, bool grad)
                  int(std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, kPieceBytes / sum))), &l.tile_n, &l.splits);
         l.dz = l.take(ce->tokens * l.piece * 2);
         l.acc = l.take(sum * l.splits);
+        l.unit = l.take(4);
     } else {
         l.part = l.take((ce->vocab + 2 * kM - 1) / (2 * kM) * 2 * ce->tokens * 8);
-        l.zy = l.take(ce->tokens * 4);
     }
     l.bytes = std::max<int64_t>(l.bytes, 256);
     return l;
@@ -801,14 +864,14 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
         return s;
     Gemm g = base(ce);
     g.part = reinterpret_cast<float2 *>(ws + l.part);
-    g.zy = reinterpret_cast<float *>(ws + l.zy);
     s = launch<kStats>(g, w, false, x, false, "ce_loss", st);
     if (s)
         return s;
     int rows = 32;  // few rows: more slices of each, and more blocks
     while (rows > 1 && T / rows < 128)
         rows /= 2;
-    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_m, T, rows, g.zy, g.y, loss, lse);
+    join_kernel<<<unsigned((T + rows - 1) / rows), 256, 0, st>>>(g.part, 2 * g.tiles_m, T, rows, g.y, x.p, x.stride, w.p,
+                                                               w.stride, int(H), loss, lse);
     return tide::op_launched("ce_loss: join");
 }
 
@@ -855,13 +918,17 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
     if (!s)
         s = align_rows(w, ws, l.w, l.pitch, st);
     bf16 *dz = reinterpret_cast<bf16 *>(ws + l.dz);
-    float *acc = reinterpret_cast<float *>(ws + l.acc);
+    float *acc = reinterpret_cast<float *>(ws + l.acc), *unit = reinterpret_cast<float *>(ws + l.unit);
+    if (s)
+        return s;
+    unit_kernel<<<1, 1024, 0, st>>>(dloss, base(ce).y, T, unit);
+    s = tide::op_launched("ce_grad: unit");
     for (int64_t v0 = 0; !s && v0 < V; v0 += l.piece) {
         const int64_t n = std::min(l.piece, V - v0);
         const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece};
         Gemm g = base(ce);
         g.v0 = v0;
-        g.lse = lse, g.dloss = dloss;
+        g.lse = lse, g.dloss = dloss, g.unit = unit;
         s = make_map(&g.c, dzp, 32, 32);
         if (!s)
             s = launch<kDz>(g, wp, false, x, false, "ce_grad: dz", st);
@@ -880,7 +947,7 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
     if (s)
         return s;
     round_kernel<<<dim3(unsigned((T + 31) / 32), unsigned((H + 31) / 32)), 256, 0, st>>>(
-        acc, l.splits, T, H, l.acc_pitch, static_cast<bf16 *>(dx), dx_stride);
+        acc, l.splits, T, H, l.acc_pitch, unit, static_cast<bf16 *>(dx), dx_stride);
     return tide::op_launched("ce_grad: rounding");
 }
 
