@@ -87,7 +87,7 @@ class CeDesc(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("hidden", ctypes.c_int64),
                 ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
                 ("weight_stride", ctypes.c_int64), ("targets", ctypes.c_void_p), ("target_bytes", ctypes.c_int32),
-                ("ignore_index", ctypes.c_int64)]
+                ("ignore_index", ctypes.c_int64), ("debug", ctypes.c_uint32)]
 
 
 class Ckpt8Desc(ctypes.Structure):

@@ -92,6 +92,7 @@ struct Gemm {
     int out_tiles;       // its rows are on 16-byte boundaries: stored as tiles
     int first;           // kAdd: the sums are written, not added to
     uint64_t wait_ns;
+    int skip_fill;       // TIDE_DEBUG_SKIP_FILL
 };
 
 // exp of a difference of logits.  The difference is taken before the factor
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
             for (int s = w.s0; s < w.s1; ++s) {
                 if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
                     break;
-                if (leader) {
+                if (leader && !(g.skip_fill && i == 0 && s == 0)) {
                     const uint32_t a = ring + stage * stage_bytes, b = a + kABytes, bar = full0 + 8 * stage;
                     if (rank == 0)
                         um::mbar_expect(full + 8 * stage, uint32_t(stage_bytes) * 2);
@@ -618,6 +619,8 @@ tide_status_t check_desc(const tide_ce_t *ce)
         ce->hidden < 1 || ce->hidden > (1 << 20))
         return op_fail(TIDE_ERR_INVALID_ARG, "tokens %lld, vocab %lld, hidden %lld", (long long)ce->tokens,
                        (long long)ce->vocab, (long long)ce->hidden);
+    if (ce->debug & ~(TIDE_DEBUG_SHORT_WAIT | TIDE_DEBUG_SKIP_FILL))
+        return op_fail(TIDE_ERR_INVALID_ARG, "unknown debug bits 0x%x", ce->debug);
     if (ce->target_bytes != 4 && ce->target_bytes != 8)
         return op_fail(TIDE_ERR_INVALID_ARG, "target_bytes %d: need 4 or 8", ce->target_bytes);
     if (!tide::op_extent_ok(ce->tokens, ce->x_stride) || !tide::op_extent_ok(ce->vocab, ce->weight_stride) ||
@@ -722,7 +725,8 @@ Gemm base(const tide_ce_t *ce)
     Gemm g = {};
     g.y = {ce->targets, ce->target_bytes, ce->ignore_index, ce->vocab};
     g.splits = 1;
-    g.wait_ns = tide::kWaitBudgetNs;
+    g.wait_ns = ce->debug & TIDE_DEBUG_SHORT_WAIT ? tide::kShortWaitBudgetNs : tide::kWaitBudgetNs;
+    g.skip_fill = (ce->debug & TIDE_DEBUG_SKIP_FILL) != 0;
     return g;
 }
 

@@ -26,6 +26,7 @@ _INT_BYTES = {torch.int32: 4, torch.int64: 8}
 ROPE_SCALINGS = {None: 0, "linear": 1, "by_parts": 2}
 _BF16, _F32 = torch.bfloat16, torch.float32
 _raw_stream, _current_device, _empty = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty
+_empty_like, _CONTIGUOUS = torch.empty_like, torch.contiguous_format
 
 # These wrappers run once for every layer and token, in front of kernels of a
 # few microseconds: each attribute is read once, checks are plain comparisons,
@@ -58,6 +59,11 @@ def _like(t, dtype, dev, shape, name):
         raise TypeError(f"{name} is {t.dtype} on {t.device}, expected {dtype} on CUDA device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _new(t):
+    """A contiguous tensor like `t` (half the time of t.new_empty)."""
+    return _empty_like(t, memory_format=_CONTIGUOUS)
 
 
 def _scratch(n: int, workspace, device):
@@ -140,7 +146,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     qh, kh = _heads(q, "q"), _heads(k, "k")
     desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     if out is None:
-        q_out, k_out = q.new_empty(qs), k.new_empty(ks)
+        q_out, k_out = _new(q), _new(k)
     else:
         q_out, k_out = out
         _like(q_out, q.dtype, dev, qs, "q_out")
@@ -158,9 +164,9 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
     _like(dq_out, dtype, dev, qs, "dq_out")
     _like(dk_out, dtype, dev, ks, "dk_out")
     if out is None:
-        dq, dk = q.new_empty(qs), k.new_empty(ks)
-        dqw = None if q_weight is None else q.new_empty(qs[2])
-        dkw = None if k_weight is None else k.new_empty(qs[2])
+        dq, dk = _new(q), _new(k)
+        dqw = None if q_weight is None else _new(q_weight)
+        dkw = None if k_weight is None else _new(k_weight)
     else:
         dq, dk, dqw, dkw = out
         _like(dq, dtype, dev, qs, "dq")
@@ -240,7 +246,7 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
     _per_token(lse, dev, T, "lse")
     _per_token(dloss, dev, T, "dloss")
     if out is None:
-        dx, dw = x.new_empty(x.shape), weight.new_empty(weight.shape)
+        dx, dw = _new(x), _new(weight)
     else:
         dx, dw = out
         _like(dx, _BF16, dev, x.shape, "dx")
@@ -292,7 +298,7 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
     rows, cols = shape
     if out is None:
         device = gate.device
-        h, ckpt, hs = gate.new_empty(shape), new_ckpt8(rows, cols, device), cols
+        h, ckpt, hs = _new(gate), new_ckpt8(rows, cols, device), cols
         desc = _b.Ckpt8Desc(*[t.data_ptr() for t in ckpt])
     else:
         h, ckpt = out
@@ -313,8 +319,8 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
     rows, cols = shape
     desc = _ckpt_desc(ckpt, rows, cols, dev)
     if out is None:
-        dgate, dup = dh.new_empty(shape), dh.new_empty(shape)
-        h = dh.new_empty(shape) if need_h else None
+        dgate, dup = _new(dh), _new(dh)
+        h = _new(dh) if need_h else None
     else:
         dgate, dup, h = out
         for t, name in ((dgate, "dgate"), (dup, "dup"), (h, "h")):

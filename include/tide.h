@@ -468,6 +468,9 @@ typedef struct {
     const void *targets;     /* device integers [T] */
     int32_t target_bytes;    /* 4 or 8 */
     int64_t ignore_index;    /* tokens with this target count for nothing */
+    uint32_t debug;          /* 0, or TIDE_DEBUG_SHORT_WAIT (device-side waits of at most 50 ms instead of 4 s)
+                                and TIDE_DEBUG_SKIP_FILL (the first fill of the first product is left out, so
+                                that its wait expires: exercises the TIMEOUT status, the outputs are incomplete) */
 } tide_ce_t;
 
 /*
@@ -539,7 +542,8 @@ TIDE_API tide_status_t tide_swiglu_ckpt8_grad(int64_t rows, int64_t cols, int32_
  * Read and clear the operators' status word of the current device
  * (synchronises `stream`): TIDE_ERR_TIMEOUT if a bounded device-side wait of
  * tide_ce_loss or tide_ce_grad expired there since the last such read (the
- * outputs of that call are then incomplete), else TIDE_OK.
+ * outputs of that call are then incomplete), else TIDE_OK.  Not to be called
+ * during a capture.
  */
 TIDE_API tide_status_t tide_ops_device_status(void *stream);
 

@@ -414,6 +414,33 @@ def test_cross_entropy_workspace_contents_do_not_matter(tide):
     assert tide.ops.device_status() == tide.TIDE_OK
 
 
+@pytest.mark.parametrize("grad", [False, True])
+def test_cross_entropy_wait_that_runs_out(tide, grad):
+    """A fill that never comes ends its product's waits after 50 ms each; the status says so once, and the next call
+    is whole again."""
+    from all_gather_gb300 import _binding as b
+    x, w, y = ce_inputs(71, 300, 2000, 128)
+    want = tide.linear_cross_entropy(x, w, y)
+    assert tide.ops.device_status() == tide.TIDE_OK
+    desc = tide.ops._ce_desc(x, w, y, -100)[0]
+    desc.debug = tide.TIDE_DEBUG_SHORT_WAIT | tide.TIDE_DEBUG_SKIP_FILL
+    stream = torch.cuda.current_stream().cuda_stream
+    a, c = torch.empty_like(want[0]), torch.empty_like(want[0])
+    if grad:
+        n = b.tide_ce_grad_workspace(desc)
+        ws, dx, dw = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(x), torch.empty_like(w)
+        b.tide_ce_grad(desc, want[1].data_ptr(), want[0].data_ptr(), dx.data_ptr(), 128, dw.data_ptr(), 128,
+                       ws.data_ptr(), n, stream)
+    else:
+        n = b.tide_ce_loss_workspace(desc)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        b.tide_ce_loss(desc, a.data_ptr(), c.data_ptr(), ws.data_ptr(), n, stream)
+    assert tide.ops.device_status() == tide.TIDE_ERR_TIMEOUT
+    assert tide.ops.device_status() == tide.TIDE_OK
+    again = tide.linear_cross_entropy(x, w, y)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 def test_cross_entropy_drawn_shapes(tide):
     r = random.Random(5)
     for i in range(25):

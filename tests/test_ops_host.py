@@ -108,7 +108,7 @@ def ce(b, **kw):
     (dict(tokens=-1), 1, "tokens"), (dict(tokens=1 << 31), 1, "tokens"), (dict(vocab=0), 1, "vocab"),
     (dict(vocab=1 << 31), 1, "vocab"), (dict(hidden=0), 1, "hidden"), (dict(hidden=(1 << 20) + 1), 1, "hidden"),
     (dict(x_stride=63), 1, "x_stride"), (dict(weight_stride=63), 1, "weight_stride"),
-    (dict(target_bytes=1), 1, "target_bytes"), (dict(x=None), 1, "NULL"), (dict(weight=None), 1, "NULL"),
+    (dict(target_bytes=1), 1, "target_bytes"), (dict(debug=1), 1, "debug"), (dict(debug=8), 1, "debug"), (dict(x=None), 1, "NULL"), (dict(weight=None), 1, "NULL"),
     (dict(targets=None), 1, "NULL"), (dict(x=A + 1), 2, "aligned"), (dict(weight=A + 1), 2, "aligned"),
     (dict(targets=A + 4), 2, "aligned")])
 def test_ce_descriptor_refusals(tide, b, kw, status, match):
@@ -187,7 +187,7 @@ def test_wrappers_refuse_the_wrong_kind_of_tensor(tide):
 def test_structs_have_the_header_s_layout(b):
     assert ctypes.sizeof(b.Heads) == 24 and ctypes.sizeof(b.Ckpt8Desc) == 32
     assert ctypes.sizeof(b.QkDesc) == 8 + 16 + 8 + 16 + 16 + 16 and b.QkDesc.table.offset == 32
-    assert ctypes.sizeof(b.CeDesc) == 80 and b.CeDesc.ignore_index.offset == 72
+    assert ctypes.sizeof(b.CeDesc) == 88 and b.CeDesc.ignore_index.offset == 72
 
 
 def test_reference_gradients_against_differences():
