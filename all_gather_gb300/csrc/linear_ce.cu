@@ -31,6 +31,9 @@
 // many tokens and by the weight's bytes for few.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "ops_internal.h"
 #include "umma.h"
 
@@ -79,7 +82,7 @@ enum Epilogue { kStats, kDz, kAdd, kStore };
 struct Gemm {
     CUtensorMap a, b, c;  // c: kDz and kStore: out; kAdd: sums, as [splits][M][N]
     int64_t M, N, K;
-    int a_mn, b_mn;      // operand is MN-major
+    int one_copy;        // MN-major operands: blocks of 64 columns come in one copy (3-d maps)
     int tiles_m, tiles_n, splits, steps;  // steps of the sum in all
     int tile_n;          // columns of a tile: a multiple of 32, of 128 for kStore
     int stages;          // of the ring
@@ -172,6 +175,7 @@ __device__ __forceinline__ void turn_over(uint32_t tile, int lane, uint32_t (&v)
 template <int E>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_kernel(const __grid_constant__ Gemm g)
 {
+    constexpr bool kAMn = E == kAdd || E == kStore, kBMn = E == kStore;  // operands that are MN-major
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
     __shared__ uint64_t bars[2 * kMaxStages + 5];
@@ -208,39 +212,54 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
+    // The two loops below set the pace of every step of the sum, a few hundred cycles: operand layouts are known at
+    // compile time, addresses run along, and whether MN-major blocks come in one copy is settled outside.
     if (warp == 0) {
         const bool leader = um::elected();
         const uint32_t full0 = um::cluster_addr(full, 0);  // both blocks' copies count at block 0's barriers
+        const uint32_t tx = uint32_t(stage_bytes) * 2;
         int stage = 0, turns = 0;                          // ring position, and how often the ring went round
         bool ok = true;
-        for (int64_t i = first; ok && i < works; i += step) {
-            const Work w = work_of(g, i);
-            const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
-            for (int s = w.s0; s < w.s1; ++s) {
-                if (!(ok = um::mbar_wait(empty + 8 * stage, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
-                    break;
-                if (leader && !(g.skip_fill && i == 0 && s == 0)) {
-                    const uint32_t a = ring + stage * stage_bytes, b = a + kABytes, bar = full0 + 8 * stage;
-                    if (rank == 0)
-                        um::mbar_expect(full + 8 * stage, uint32_t(stage_bytes) * 2);
-                    if (g.a_mn) {
-                        for (int j = 0; j < kM / 64; ++j)
-                            um::tma_load_2d(a + j * 64 * kK * 2, &g.a, m + j * 64, s * kK, bar);
-                    } else {
-                        um::tma_load_2d(a, &g.a, s * kK, m, bar);
+        auto fetch = [&](auto copies) {
+            constexpr bool one_copy = decltype(copies)::value;
+            uint32_t at = ring, bar = 0;  // the stage's memory, and its barrier's offset
+            for (int64_t i = first; i < works; i += step) {
+                const Work w = work_of(g, i);
+                const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
+                for (int k = w.s0 * kK; k < w.s1 * kK; k += kK) {
+                    if (!(ok = um::mbar_wait(empty + bar, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
+                        return;
+                    if (leader) {
+                        if (rank == 0)
+                            um::mbar_expect(full + bar, tx);
+                        if (!kAMn) {
+                            um::tma_load_2d(at, &g.a, k, m, full0 + bar);
+                        } else if (one_copy) {
+                            um::tma_load_3d(at, &g.a, 0, k, m / 64, full0 + bar);
+                        } else {
+                            for (int j = 0; j < kM / 64; ++j)
+                                um::tma_load_2d(at + j * 64 * kK * 2, &g.a, m + j * 64, k, full0 + bar);
+                        }
+                        if (!kBMn) {
+                            um::tma_load_2d(at + kABytes, &g.b, k, n, full0 + bar);
+                        } else if (one_copy) {
+                            um::tma_load_3d(at + kABytes, &g.b, 0, k, n / 64, full0 + bar);
+                        } else {
+                            for (int j = 0; j < cols_b / 64; ++j)
+                                um::tma_load_2d(at + kABytes + j * 64 * kK * 2, &g.b, n + j * 64, k, full0 + bar);
+                        }
                     }
-                    if (g.b_mn) {
-                        for (int j = 0; j < cols_b / 64; ++j)
-                            um::tma_load_2d(b + j * 64 * kK * 2, &g.b, n + j * 64, s * kK, bar);
-                    } else {
-                        um::tma_load_2d(b, &g.b, s * kK, n, bar);
-                    }
+                    at += stage_bytes, bar += 8;
+                    if (++stage == g.stages)
+                        stage = 0, ++turns, at = ring, bar = 0;
                 }
-                __syncwarp();
-                if (++stage == g.stages)
-                    stage = 0, ++turns;
             }
-        }
+        };
+        if ((kAMn || kBMn) && g.one_copy)
+            fetch(std::true_type{});
+        else
+            fetch(std::false_type{});
+        __syncwarp();
         if (!ok && rank == 0 && leader) {  // wait for the copies in flight before the pair's memory goes
             for (int k = 0; k < g.stages; ++k) {
                 const int times = turns + (k < stage);
@@ -253,39 +272,45 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     } else if (warp == 1) {
         if (rank == 0) {
             const bool leader = um::elected();
-            const uint32_t idesc = um::instr_desc(kM * 2, g.tile_n, g.a_mn, g.b_mn);
-            const uint32_t a_step = (g.a_mn ? 2048 : 32) >> 4, b_step = (g.b_mn ? 2048 : 32) >> 4;  // 16 of the sum
-            const uint64_t a0 = um::operand_desc(ring, g.a_mn, 64 * kK * 2);
-            const uint64_t b0 = um::operand_desc(ring + kABytes, g.b_mn, 64 * kK * 2);
+            const uint32_t idesc = um::instr_desc(kM * 2, g.tile_n, kAMn, kBMn);
+            constexpr uint32_t a_step = (kAMn ? 2048 : 32) >> 4, b_step = (kBMn ? 2048 : 32) >> 4;  // 16 of the sum
+            const uint64_t a0 = um::operand_desc(ring, kAMn, 64 * kK * 2);
+            const uint64_t b0 = um::operand_desc(ring + kABytes, kBMn, 64 * kK * 2);
+            const uint32_t stage_units = uint32_t(stage_bytes) >> 4;
             int stage = 0, phase = 0, buf = 0, buf_phase = 0;
+            uint32_t at = 0, bar = 0;
             bool ok = true;
+            if (g.skip_fill && first == 0)  // nothing arrives at this barrier before the end
+                ok = um::mbar_wait(drained, 0, &gave_up, g.wait_ns);
             for (int64_t i = first; ok && i < works; i += step) {
                 const Work w = work_of(g, i);
                 if (!(ok = um::mbar_wait<true>(acc_empty + 8 * buf, buf_phase ^ 1, &gave_up, g.wait_ns)))
                     break;
                 um::fence_after();
                 const uint32_t d = tmem + buf * kN;
+                bool add = false;
                 for (int s = w.s0; s < w.s1; ++s) {
-                    if (!(ok = um::mbar_wait(full + 8 * stage, phase, &gave_up, g.wait_ns)))
+                    if (!(ok = um::mbar_wait(full + bar, phase, &gave_up, g.wait_ns)))
                         break;
                     um::fence_after();
                     if (leader) {
-                        const uint32_t at = uint32_t(stage * stage_bytes) >> 4;
 #pragma unroll
                         for (int k = 0; k < kK / 16; ++k)
-                            um::mma_bf16(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc, s > w.s0 || k > 0);
-                        um::mma_commit(empty + 8 * stage);
+                            um::mma_bf16(d, a0 + at + k * a_step, b0 + at + k * b_step, idesc, add || k > 0);
+                        um::mma_commit(empty + bar);
                     }
-                    __syncwarp();
+                    add = true;
+                    at += stage_units, bar += 8;
                     if (++stage == g.stages)
-                        stage = 0, phase ^= 1;
+                        stage = 0, phase ^= 1, at = 0, bar = 0;
                 }
+                __syncwarp();
                 if (ok && leader)
                     um::mma_commit(acc_full + 8 * buf);
-                __syncwarp();
                 if (++buf == 2)
                     buf = 0, buf_phase ^= 1;
             }
+            __syncwarp();
             if (!ok && leader) {  // wait for the products in flight before the accumulators and tiles go
                 g_timed_out = 1;
                 um::mma_commit(drained);
@@ -303,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         const int width = half ? g.tile_n - half_n : half_n;
         const uint32_t outs = ring + kRingBytes, out = outs + (warp - 2) * kOutTile;
         const uint32_t acc_done = um::cluster_addr(acc_empty, 0);
-        const float unit = E == kStore ? *g.unit : 1.f;
+        const float unit = E == kStore || E == kDz ? *g.unit : 1.f;
         int buf = 0, buf_phase = 0, out_at = 0;
         for (int64_t i = first; i < works; i += step) {
             const Work w = work_of(g, i);
@@ -323,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 lse[k] = INFINITY, scale[k] = 0.f;  // an ignored token: exp(z - lse) = 0
                 if (E == kDz && y != -1) {
                     lse[k] = g.lse[t];
-                    scale[k] = y == -2 ? __int_as_float(0x7fffffff) : __fdiv_rn(g.dloss[t], *g.unit);
+                    scale[k] = y == -2 ? __int_as_float(0x7fffffff) : __fdiv_rn(g.dloss[t], unit);
                 }
             }
             bool ready = um::mbar_wait<false, 100>(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
@@ -678,6 +703,8 @@ EncodeTiled encode_tiled()
 struct Mat {
     const bf16 *p;
     int64_t rows, cols, stride;
+    int64_t readable = 0;  // columns that may be read, if more than cols
+    int64_t blocks_of_64() const { return readable ? readable / 64 : cols % 64 ? 0 : cols / 64; }
 };
 
 bool rows_aligned(const void *p, int64_t stride, int64_t rows)
@@ -709,6 +736,18 @@ tide_status_t make_map(CUtensorMap *map, const Mat &m, int box_rows, int box_col
     const cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16 *>(m.p), dims, strides, box,
                   box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// An MN-major operand whose copies are `blocks` blocks of 64 columns by 64 rows:
+// one copy where the plain map takes one a block.  Its last block of columns is
+// whole, so they have to be a multiple of 64 that may be read.
+tide_status_t make_block_map(CUtensorMap *map, const Mat &m, int blocks)
+{
+    const cuuint64_t dims[3] = {64, cuuint64_t(m.rows), cuuint64_t(m.blocks_of_64())};
+    const cuuint64_t strides[2] = {cuuint64_t(m.rows < 2 ? m.blocks_of_64() * 128 : m.stride * 2), 128};
+    const cuuint32_t box[3] = {64, kK, cuuint32_t(blocks)};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(m.p), dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // The same for fp32 sums [splits][rows][cols] with rows `pitch` apart: 32 rows of 32 columns.
@@ -747,12 +786,12 @@ void shape_of(int64_t tiles_m, int64_t N, int64_t steps, int unit, int max_split
         }
 }
 
-// C[M, N] = sum over k of A B.  An operand is given with its rows as the tile's
-// dimension (K-major) or, mn, with its rows as the summed one.
+// C[M, N] = sum over k of A B.  A K-major operand is given with its rows as the
+// tile's dimension, an MN-major one with its rows as the summed one.
 template <int E>
-tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, const char *what, cudaStream_t st)
+tide_status_t launch(Gemm &g, const Mat &a, const Mat &b, const char *what, cudaStream_t st)
 {
-    g.a_mn = a_mn, g.b_mn = b_mn;
+    constexpr bool a_mn = E == kAdd || E == kStore, b_mn = E == kStore;
     g.M = a_mn ? a.cols : a.rows;
     g.N = b_mn ? b.cols : b.rows;
     g.K = a_mn ? a.rows : a.cols;
@@ -762,9 +801,10 @@ tide_status_t launch(Gemm &g, const Mat &a, bool a_mn, const Mat &b, bool b_mn, 
         shape_of(g.tiles_m, g.N, g.steps, E == kStore ? 128 : 32, 1, &g.tile_n, &g.splits);
     g.tiles_n = int((g.N + g.tile_n - 1) / g.tile_n);
     g.stages = std::min(kMaxStages, kRingBytes / (kABytes + g.tile_n / 2 * kK * 2));
-    tide_status_t s = make_map(&g.a, a, a_mn ? kK : kM);
+    g.one_copy = a_mn && a.blocks_of_64() > 0 && (!b_mn || b.blocks_of_64() > 0);
+    tide_status_t s = g.one_copy ? make_block_map(&g.a, a, kM / 64) : make_map(&g.a, a, a_mn ? kK : kM);
     if (!s)
-        s = make_map(&g.b, b, b_mn ? kK : g.tile_n / 2);
+        s = g.one_copy && b_mn ? make_block_map(&g.b, b, g.tile_n / 128) : make_map(&g.b, b, b_mn ? kK : g.tile_n / 2);
     if (!s && E == kStore && g.out_tiles)
         s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32, 32);
     if (s)
@@ -868,7 +908,7 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
         return s;
     Gemm g = base(ce);
     g.part = reinterpret_cast<float2 *>(ws + l.part);
-    s = launch<kStats>(g, w, false, x, false, "ce_loss", st);
+    s = launch<kStats>(g, w, x, "ce_loss", st);
     if (s)
         return s;
     int rows = 32;  // few rows: more slices of each, and more blocks
@@ -929,24 +969,24 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
     s = tide::op_launched("ce_grad: unit");
     for (int64_t v0 = 0; !s && v0 < V; v0 += l.piece) {
         const int64_t n = std::min(l.piece, V - v0);
-        const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece};
+        const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece, l.piece};
         Gemm g = base(ce);
         g.v0 = v0;
         g.lse = lse, g.dloss = dloss, g.unit = unit;
         s = make_map(&g.c, dzp, 32, 32);
         if (!s)
-            s = launch<kDz>(g, wp, false, x, false, "ce_grad: dz", st);
+            s = launch<kDz>(g, wp, x, "ce_grad: dz", st);
         if (s)
             return s;
         g.first = v0 == 0, g.splits = l.splits, g.tile_n = l.tile_n;
         s = make_acc_map(&g.c, acc, l.splits, H, T, l.acc_pitch);
         if (!s)
-            s = launch<kAdd>(g, wp, true, dzp, false, "ce_grad: dx", st);
+            s = launch<kAdd>(g, wp, dzp, "ce_grad: dx", st);
         if (s)
             return s;
         g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
         g.out_tiles = H % 8 == 0 && rows_aligned(g.out, dweight_stride, V);  // tiles are stored by 16 bytes
-        s = launch<kStore>(g, dzp, true, x, true, "ce_grad: dweight", st);
+        s = launch<kStore>(g, dzp, x, "ce_grad: dweight", st);
     }
     if (s)
         return s;

@@ -469,8 +469,8 @@ typedef struct {
     int32_t target_bytes;    /* 4 or 8 */
     int64_t ignore_index;    /* tokens with this target count for nothing */
     uint32_t debug;          /* 0, or TIDE_DEBUG_SHORT_WAIT (device-side waits of at most 50 ms instead of 4 s)
-                                and TIDE_DEBUG_SKIP_FILL (the first fill of the first product is left out, so
-                                that its wait expires: exercises the TIMEOUT status, the outputs are incomplete) */
+                                and TIDE_DEBUG_SKIP_FILL (the first tile of every product waits for a fill that
+                                never comes: exercises the TIMEOUT status, the outputs are incomplete) */
 } tide_ce_t;
 
 /*
