@@ -778,18 +778,29 @@ Gemm base(const tide_ce_t *ce)
 // Columns of a tile and shares of the sum for a product of `tiles_m` row tiles,
 // N columns and `steps` steps: those of the shortest rounds.  A step takes as
 // long as its columns and a fixed part, no less than what the fetch of its rows
-// takes, and a tile's end another four steps'.
+// takes, and a tile's end another four steps'.  Shares are tried where they
+// fill one to eight rounds.
 void shape_of(int64_t tiles_m, int64_t N, int64_t steps, int unit, int max_splits, int *tile_n, int *splits)
 {
     const int64_t pairs = std::max(tide::op_sm_count() / 2, 1);
+    const int most = int(std::min<int64_t>(max_splits, steps / 4 + 1));
     double best = 1e300;
-    for (int n = kN; n >= std::min(unit, 128); n -= unit)
-        for (int s = 1; s <= max_splits && s <= steps / 4 + 1; ++s) {
-            const int64_t rounds = (tiles_m * ((N + n - 1) / n) * s + pairs - 1) / pairs;
-            const double time = double(rounds) * (double(steps) / s * (std::max(n, 96) + 32) + 4 * 288);
+    for (int n = kN; n >= std::min(unit, 128); n -= unit) {
+        const int64_t tiles = std::max<int64_t>(1, tiles_m * ((N + n - 1) / n));
+        const double step = std::max(n, 96) + 32;
+        int last = 0;
+        for (int r = 0; r <= 8; ++r) {  // r = 0: one share
+            const int s = r == 0 ? 1 : int(std::min<int64_t>(most, r * pairs / tiles));
+            if (s <= last)
+                continue;
+            last = s;
+            const double time = double((tiles * s + pairs - 1) / pairs) * (double(steps) / s * step + 4 * 288);
             if (time < best * 0.99)
                 best = time, *tile_n = n, *splits = s;
+            if (s == most)
+                break;
         }
+    }
 }
 
 // C[M, N] = sum over k of A B.  A K-major operand is given with its rows as the

@@ -116,6 +116,15 @@ def test_ce_descriptor_refusals(tide, b, kw, status, match):
     refused(tide, status, match, b.tide_ce_grad, ce(b, **kw), A, A, A, 64, A, 64, A, 1 << 40)
 
 
+@pytest.mark.parametrize("T, V, H", [(0, 1, 1), (0, 100, 64), (1, 1, 1), (1, 131072, 4096), (70000, 1000, 7), (3, 2000001, 65)])
+def test_ce_workspace_sizes(tide, b, T, V, H):
+    """Sizes are whole for every shape, no tokens among them, and the gradient's holds a piece of dz and a share of dx."""
+    d = ce(b, tokens=T, vocab=V, hidden=H, x_stride=H, weight_stride=H)
+    assert 256 <= b.tide_ce_loss_workspace(d) and b.tide_ce_loss_workspace(d) % 256 == 0
+    n = b.tide_ce_grad_workspace(d)
+    assert n >= 256 and n % 256 == 0 and n >= T * min(V, 8192) * 2 + T * H * 4
+
+
 def test_ce_tensor_refusals(tide, b):
     f, g = b.tide_ce_loss, b.tide_ce_grad
     refused(tide, 1, "loss or lse is NULL", f, ce(b), 0, A, A, 1 << 40)
