@@ -507,13 +507,41 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
 }
 
 // Rows that the tiled copies cannot take (16-byte boundaries) go into the
-// workspace first, `pitch` elements apart.
+// workspace first, `pitch` elements (a multiple of 8) apart; what lies between
+// them is not read as part of a row.
 __global__ void __launch_bounds__(256) align_kernel(const bf16 *in, int64_t stride, int64_t rows, int64_t cols,
                                                     bf16 *out, int64_t pitch)
 {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256)
-            out[r * pitch + c] = in[r * stride + c];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const bf16 *row = in + r * stride;
+        for (int64_t c = 8 * threadIdx.x; c < cols; c += 8 * 256) {
+            uint32_t w[4];
+            tide::load16_any(row + c, row + cols, w);
+            *reinterpret_cast<uint4 *>(out + r * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// The way back: rows `pitch` elements apart to rows on any boundary, by aligned
+// 16-byte pieces between a row's first and last few elements.
+__global__ void __launch_bounds__(256) unalign_kernel(const bf16 *in, int64_t pitch, int64_t rows, int64_t cols,
+                                                      bf16 *out, int64_t stride)
+{
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const bf16 *from = in + r * pitch;
+        bf16 *to = out + r * stride;
+        const int64_t head = min(cols, int64_t((16 - (reinterpret_cast<uintptr_t>(to) & 15)) % 16 / 2));
+        const int64_t whole = (cols - head) / 8, tail = head + 8 * whole;
+        for (int64_t i = threadIdx.x; i < whole; i += 256) {
+            uint32_t w[4];
+            tide::load16_any(from + head + 8 * i, from + cols, w);
+            *reinterpret_cast<uint4 *>(to + head + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (threadIdx.x < head)
+            to[threadIdx.x] = from[threadIdx.x];
+        if (tail + threadIdx.x < cols)
+            to[tail + threadIdx.x] = from[tail + threadIdx.x];
+    }
 }
 
 // Joins the pairs (maximum, sum) of `rows` neighbouring tokens a block, 256 /
@@ -1001,9 +1029,22 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
             s = launch<kAdd>(g, wp, dzp, "ce_grad: dx", st);
         if (s)
             return s;
-        g.out = static_cast<bf16 *>(dweight) + v0 * dweight_stride, g.out_stride = dweight_stride;
+        bf16 *dwp = static_cast<bf16 *>(dweight) + v0 * dweight_stride;
+        g.out = dwp, g.out_stride = dweight_stride;
         g.out_tiles = H % 8 == 0 && rows_aligned(g.out, dweight_stride, V);  // tiles are stored by 16 bytes
+        // Rows on other boundaries go through the weight's aligned copy, if there is one: this piece of it has been
+        // used.  Single stores from the result warps take eight times as long (20 x 50001 x 2047: 989 us in all, 278 this way).
+        const bool staged = !g.out_tiles && l.w >= 0;
+        if (staged) {
+            g.out = reinterpret_cast<bf16 *>(ws + l.w) + v0 * l.pitch, g.out_stride = l.pitch;
+            g.out_tiles = 1;
+        }
         s = launch<kStore>(g, dzp, x, "ce_grad: dweight", st);
+        if (!s && staged) {
+            unalign_kernel<<<unsigned(std::min<int64_t>(n, 1 << 20)), 256, 0, st>>>(g.out, l.pitch, n, H, dwp,
+                                                                                  dweight_stride);
+            s = tide::op_launched("ce_grad: dweight's rows");
+        }
     }
     if (s)
         return s;

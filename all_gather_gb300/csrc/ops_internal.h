@@ -112,4 +112,37 @@ __device__ __forceinline__ void store8(float *p, const float *f)
     reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// Rows that do not start on 16-byte boundaries, by whole aligned pieces.
+
+// Bytes `phase` (0 to 15) to phase + 15 of 32.
+__device__ __forceinline__ void shift_bytes(const uint32_t (&w)[8], uint32_t phase, uint32_t (&out)[4])
+{
+    uint32_t a[6], b[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i)
+        a[i] = phase & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        b[i] = phase & 4 ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = __funnelshift_r(b[i], b[i + 1], 8 * (phase & 3));
+}
+
+// The 16 bytes at `p`, of which those before `end` count (at least one; the rest
+// is whatever lies there or 0): read as the aligned 16-byte pieces that hold a
+// byte that counts, so that nothing is touched that shares no piece with one.
+__device__ __forceinline__ void load16_any(const void *p, const void *end, uint32_t (&out)[4])
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t phase = uint32_t(at & 15);
+    const uint4 *q = reinterpret_cast<const uint4 *>(at - phase);
+    const uint4 x = q[0];
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (phase && reinterpret_cast<uintptr_t>(q + 1) < reinterpret_cast<uintptr_t>(end))
+        y = q[1];
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    shift_bytes(w, phase, out);
+}
+
 }  // namespace tide

@@ -890,11 +890,14 @@ int heads_per_item(int heads, int rows, int64_t tokens, int64_t warps)
     return int((steps + std::min(steps, want) - 1) / std::min(steps, want)) * rows;
 }
 
-// Blocks of the backward for queries and for keys: two a SM, shared by their
+// Blocks of the backward for queries and for keys, shared by their
 // steps of four heads and one more for each token's own work.
-void grad_blocks(const tide_qk_t *qk, int sms, int *q, int *k)
+// per_sm: two for the vector kernel; eight for the generic one, whose warps keep
+// nothing in flight beyond their own head.
+constexpr int kVecPerSm = 2, kGenericPerSm = 8;
+void grad_blocks(const tide_qk_t *qk, int sms, int per_sm, int *q, int *k)
 {
-    const int64_t all = int64_t(sms) * 2;
+    const int64_t all = int64_t(sms) * per_sm;
     const int64_t wq = qk->q_heads ? qk->q_heads + 4 : 0, wk = qk->k_heads ? qk->k_heads + 4 : 0;
     int64_t nq = wq + wk ? (all * wq + wq + wk - 1) / (wq + wk) : 0;
     int64_t nk = all - nq;
@@ -1014,7 +1017,7 @@ tide_status_t backward(const tide_qk_t *qk, const tide_heads_t *dqo, const tide_
         vec = vec && (!p.w || vec_rows(qk, in[i], p.heads)) && vec_rows(qk, grad[i], p.heads) &&
               vec_rows(qk, out[i], p.heads);
     }
-    grad_blocks(qk, tide::op_sm_count(), &a.part[0].blocks, &a.part[1].blocks);
+    grad_blocks(qk, tide::op_sm_count(), vec ? kVecPerSm : kGenericPerSm, &a.part[0].blocks, &a.part[1].blocks);
     a.part[0].partial = partial;
     a.part[1].partial = partial + int64_t(a.part[0].blocks) * a.D;
     const unsigned grid = unsigned(a.part[0].blocks + a.part[1].blocks);
@@ -1107,7 +1110,7 @@ int64_t tide_qk_norm_rope_grad_workspace(const tide_qk_t *qk)
     if (!qk->q_weight && !qk->k_weight)
         return 0;
     int nq, nk;
-    grad_blocks(qk, tide::op_sm_count(), &nq, &nk);
+    grad_blocks(qk, tide::op_sm_count(), kGenericPerSm, &nq, &nk);  // what rows will be on is not known here
     return std::max<int64_t>(256, (int64_t(nq) + nk) * qk->head_dim * 4);
 }
 

@@ -332,6 +332,27 @@ def test_cross_entropy_gradient_against_differences(tide):
     assert abs(diff - a.sum() - b.sum()) <= 2.0 ** -8 * (a.abs().sum() + b.abs().sum())
 
 
+@pytest.mark.parametrize("shift", [0, 1, 3, 5])
+@pytest.mark.parametrize("H", [1, 3, 9, 63, 101, 2047])
+def test_cross_entropy_rows_on_any_boundary(tide, H, shift):
+    """Rows that start on every 2-byte boundary, in and out: the same bits as from aligned rows."""
+    T, V = 30, 270
+    x, w, y = ce_inputs(H + shift, T, V, H)
+    d = torch.full((T,), 0.01, device="cuda")
+    pitch = -(-H // 8) * 8
+    X, W = (torch.zeros((n, pitch), dtype=BF16, device="cuda") for n in (T, V))
+    X[:, :H], W[:, :H] = x, w
+    loss, lse = tide.linear_cross_entropy(X[:, :H], W[:, :H], y)
+    want = tide.linear_cross_entropy_grad(X[:, :H], W[:, :H], y, lse, d)
+    fx, fw = (torch.zeros(n * H + shift, dtype=BF16, device="cuda")[shift:].view(n, H) for n in (T, V))
+    fx.copy_(x), fw.copy_(w)
+    assert torch.equal(tide.linear_cross_entropy(fx, fw, y)[0], loss)
+    ox, ow = Framed((T, H), BF16, 0, shift), Framed((V, H), BF16, 0, shift)
+    tide.linear_cross_entropy_grad(fx, fw, y, lse, d, out=(ox.t, ow.t))
+    ox.check(), ow.check()
+    assert torch.equal(ox.t, want[0]) and torch.equal(ow.t, want[1])
+
+
 @pytest.mark.parametrize("H, pad", [(100, 4), (1, 7), (65, 7), (130, 6), (63, 1)])
 def test_cross_entropy_reads_and_writes_its_columns_only(tide, H, pad):
     """Rows on 16-byte boundaries whose length is not a multiple of 16 bytes: what lies between them is not read (it
