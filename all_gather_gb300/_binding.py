@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -380,6 +381,42 @@ def tide_qk_norm_rope_grad(qk: QkDesc, dq_out: Heads, dk_out: Heads, q: Optional
     _check(load_library().tide_qk_norm_rope_grad(qk, dq_out, dk_out, q, k, dq, dk, dq_weight or None,
                                                  dk_weight or None, workspace or None, workspace_bytes,
                                                  stream or None), "tide_qk_norm_rope_grad")
+
+
+class PackedCalls:
+    """The operators that run for every token, with their structures as packed bytes: a third of the time of filling
+    ctypes structures.  Layouts are those of tide_qk_t, tide_heads_t and tide_ckpt8_t.  Calls return the status."""
+
+    qk = struct.Struct("qiiiiqPPiiifPP").pack
+    heads = struct.Struct("Pqq").pack
+    ckpt8 = struct.Struct("PPPP").pack
+
+    def __init__(self):
+        lib = load_library()
+        raw, vp, i64, i32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+        def function(name, *argtypes):
+            f = lib[name]  # an object of its own, with argument types of its own
+            f.argtypes, f.restype = argtypes, ctypes.c_int
+            return f
+
+        self.qk_norm_rope = function("tide_qk_norm_rope", *[raw] * 5, vp)
+        self.qk_norm_rope_grad = function("tide_qk_norm_rope_grad", *[raw] * 7, vp, vp, vp, i64, vp)
+        self.qk_norm_rope_grad_workspace = function("tide_qk_norm_rope_grad_workspace", raw)
+        self.qk_norm_rope_grad_workspace.restype = i64
+        self.swiglu_ckpt8 = function("tide_swiglu_ckpt8", i64, i64, i32, vp, i64, vp, i64, vp, i64, raw, vp)
+        self.swiglu_ckpt8_grad = function("tide_swiglu_ckpt8_grad", i64, i64, i32, raw, vp, i64, vp, i64, vp, i64, vp,
+                                          i64, vp)
+
+
+_packed: Optional[PackedCalls] = None
+
+
+def packed_calls() -> PackedCalls:
+    global _packed
+    if _packed is None:
+        _packed = PackedCalls()
+    return _packed
 
 
 def _size(n: int, where: str) -> int:

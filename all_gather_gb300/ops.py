@@ -95,6 +95,9 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
     return out
 
 
+_packed_qk, _packed_heads, _packed_ckpt8 = _b.PackedCalls.qk, _b.PackedCalls.heads, _b.PackedCalls.ckpt8
+
+
 def _heads(t, name):
     """A tensor of heads, with the dtype, device and shape already checked where it has to agree with another."""
     st = t.stride()
@@ -102,7 +105,7 @@ def _heads(t, name):
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     if st[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name} has no contiguous last dimension")
-    return _b.Heads(t.data_ptr(), st[0], st[1])
+    return _packed_heads(t.data_ptr(), st[0], st[1])
 
 
 def _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved):
@@ -128,14 +131,14 @@ def _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved):
         if positions.shape != (T,) or not positions.is_contiguous():
             raise ValueError(f"positions must be contiguous of shape ({T},)")
         tp, pp = table.data_ptr(), positions.data_ptr()
-    wq = wk = None
+    wq = wk = 0
     if q_weight is not None:
         _like(q_weight, dtype, dev, (D,), "q_weight")
         wq = q_weight.data_ptr()
     if k_weight is not None:
         _like(k_weight, dtype, dev, (D,), "k_weight")
         wk = k_weight.data_ptr()
-    return _b.QkDesc(T, Hq, ks[1], D, R, P, tp, pp, pos_bytes, dt, 1 if interleaved else 0, eps, wq, wk), dev, qs, ks
+    return _packed_qk(T, Hq, ks[1], D, R, P, tp, pp, pos_bytes, dt, 1 if interleaved else 0, eps, wq, wk), dev, qs, ks
 
 
 def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -151,7 +154,10 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
         q_out, k_out = out
         _like(q_out, q.dtype, dev, qs, "q_out")
         _like(k_out, q.dtype, dev, ks, "k_out")
-    _b.tide_qk_norm_rope(desc, qh, kh, _heads(q_out, "q_out"), _heads(k_out, "k_out"), _stream(stream))
+    status = _b.packed_calls().qk_norm_rope(desc, qh, kh, _heads(q_out, "q_out"), _heads(k_out, "k_out"),
+                                            _stream(stream))
+    if status:
+        _b._check(status, "tide_qk_norm_rope")
     return q_out, k_out
 
 
@@ -176,14 +182,17 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
                 raise ValueError(f"{name} goes with its weight: both or neither")
             if w is not None:
                 _like(d, dtype, dev, (qs[2],), name)
-    ws = n = 0
+    lib, ws, n = _b.packed_calls(), 0, 0
     if q_weight is not None or k_weight is not None or workspace is not None:
-        _keep, ws, n = _scratch(_b.tide_qk_norm_rope_grad_workspace(desc), workspace, q.device)
-    _b.tide_qk_norm_rope_grad(desc, _heads(dq_out, "dq_out"), _heads(dk_out, "dk_out"),
-                              None if q_weight is None else _heads(q, "q"),
-                              None if k_weight is None else _heads(k, "k"), _heads(dq, "dq"), _heads(dk, "dk"),
-                              0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(), ws, n,
-                              _stream(stream))
+        need = _b._size(lib.qk_norm_rope_grad_workspace(desc), "tide_qk_norm_rope_grad_workspace")
+        _keep, ws, n = _scratch(need, workspace, q.device)
+    status = lib.qk_norm_rope_grad(desc, _heads(dq_out, "dq_out"), _heads(dk_out, "dk_out"),
+                                   None if q_weight is None else _heads(q, "q"),
+                                   None if k_weight is None else _heads(k, "k"), _heads(dq, "dq"), _heads(dk, "dk"),
+                                   0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(), ws, n,
+                                   _stream(stream))
+    if status:
+        _b._check(status, "tide_qk_norm_rope_grad")
     return dq, dk, dqw, dkw
 
 
@@ -278,7 +287,7 @@ def _ckpt_desc(ckpt, rows, cols, dev):
         if t.dtype is not dt or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
             raise ValueError(f"a checkpoint tensor is {t.dtype} {tuple(t.shape)} on {t.device}: need contiguous {dt} "
                              f"{shape} on CUDA device {dev}")
-    return _b.Ckpt8Desc(g8.data_ptr(), ge.data_ptr(), u8.data_ptr(), ue.data_ptr())
+    return _packed_ckpt8(g8.data_ptr(), ge.data_ptr(), u8.data_ptr(), ue.data_ptr())
 
 
 def new_ckpt8(rows: int, cols: int, device="cuda") -> Ckpt8:
@@ -299,13 +308,15 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
     if out is None:
         device = gate.device
         h, ckpt, hs = _new(gate), new_ckpt8(rows, cols, device), cols
-        desc = _b.Ckpt8Desc(*[t.data_ptr() for t in ckpt])
+        desc = _packed_ckpt8(*[t.data_ptr() for t in ckpt])
     else:
         h, ckpt = out
         _like(h, dtype, dev, shape, "h")
         hs, desc = _rows(h, "h"), _ckpt_desc(ckpt, rows, cols, dev)
-    _b.tide_swiglu_ckpt8(rows, cols, dt, gate.data_ptr(), gs, up.data_ptr(), us, h.data_ptr(), hs, desc,
-                         _stream(stream))
+    status = _b.packed_calls().swiglu_ckpt8(rows, cols, dt, gate.data_ptr(), gs, up.data_ptr(), us, h.data_ptr(), hs,
+                                            desc, _stream(stream))
+    if status:
+        _b._check(status, "tide_swiglu_ckpt8")
     return h, ckpt
 
 
@@ -326,9 +337,12 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
         for t, name in ((dgate, "dgate"), (dup, "dup"), (h, "h")):
             if t is not None:
                 _like(t, dtype, dev, shape, name)
-    _b.tide_swiglu_ckpt8_grad(rows, cols, dt, desc, dh.data_ptr(), ds, dgate.data_ptr(), _rows(dgate, "dgate"),
-                              dup.data_ptr(), _rows(dup, "dup"), 0 if h is None else h.data_ptr(),
-                              0 if h is None else _rows(h, "h"), _stream(stream))
+    status = _b.packed_calls().swiglu_ckpt8_grad(rows, cols, dt, desc, dh.data_ptr(), ds, dgate.data_ptr(),
+                                                 _rows(dgate, "dgate"), dup.data_ptr(), _rows(dup, "dup"),
+                                                 0 if h is None else h.data_ptr(), 0 if h is None else _rows(h, "h"),
+                                                 _stream(stream))
+    if status:
+        _b._check(status, "tide_swiglu_ckpt8_grad")
     return dgate, dup, h
 
 

@@ -199,6 +199,14 @@ def test_structs_have_the_header_s_layout(b):
     assert ctypes.sizeof(b.CeDesc) == 88 and b.CeDesc.ignore_index.offset == 72
 
 
+def test_packed_structs_have_the_same_bytes(b):
+    p = b.PackedCalls
+    assert p.heads(A, 128, 64) == bytes(b.Heads(A, 128, 64))
+    assert p.ckpt8(A, A + 1, A + 2, A + 3) == bytes(b.Ckpt8Desc(A, A + 1, A + 2, A + 3))
+    v = (7, 2, 1, 64, 32, 10, A, A + 8, 8, 1, 1, 1e-6, A + 16, 0)
+    assert p.qk(*v) == bytes(b.QkDesc(*v))
+
+
 def test_reference_gradients_against_differences():
     """The reference's own gradients, by central differences in 64 bits (error about h^2)."""
     torch.manual_seed(0)
