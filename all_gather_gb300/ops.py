@@ -5,9 +5,10 @@ Thin wrappers of the ``tide_*`` entry points of the same names
 (``include/tide.h`` has the formulas): they check types and shapes, allocate
 the outputs that are not passed in ``out`` and the scratch memory, and launch
 on ``stream`` (default: the current stream).  Nothing is computed in Python.
-A tensor that another stream may still be using is the caller's to order, as
-with any asynchronous call; tensors allocated here belong to the current
-stream, so pass ``out`` and ``workspace`` to run on another one.
+A call with a ``stream`` is that call with the stream made current: what it
+allocates, outputs and scratch memory, belongs to that stream, and is not
+handed out again before the work on it is done.  A tensor that another stream
+may still be using is the caller's to order, as with any asynchronous call.
 
 Every operator has its gradient as a function of its own that takes and
 returns plain tensors; gradients of parameters have the parameter's type and
@@ -33,10 +34,28 @@ _empty_like, _CONTIGUOUS = torch.empty_like, torch.contiguous_format
 # and names that only an error needs are put together there.
 
 
-def _stream(stream) -> int:
-    if stream is None:
-        return _raw_stream(_current_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _stream() -> int:
+    return _raw_stream(_current_device())
+
+
+class _current:
+    """Makes ``stream`` (a torch stream or a raw handle) the current one, which is the one that memory is allocated for."""
+
+    def __init__(self, stream):
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+        self.other = None
+        if raw != _stream():
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(raw) if raw > 1 else torch.cuda.default_stream()
+            self.other = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *error):
+        if self.other is not None:
+            self.other.__exit__(*error)
 
 
 def _dtype(dtype, name):
@@ -83,6 +102,10 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
                original: float = 8192.0, device=None, out=None, stream=None):
     """fp32 [max_position, rotary_dim]: cosines, then sines, of every position's angles.
     ``scaling``: None, "linear" (positions divided by ``factor``) or "by_parts"."""
+    if stream is not None:
+        with _current(stream):
+            return rope_table(max_position, rotary_dim, base, scaling, factor, low_freq_factor, high_freq_factor, original,
+                              device, out)
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling {scaling!r}: need one of {list(ROPE_SCALINGS)}")
     if out is None:
@@ -91,7 +114,7 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
           or tuple(out.shape) != (max_position, rotary_dim)):
         raise ValueError(f"out must be a contiguous float32 CUDA tensor [{max_position}, {rotary_dim}]")
     _b.tide_rope_table(max_position, rotary_dim, base, ROPE_SCALINGS[scaling], factor, low_freq_factor,
-                       high_freq_factor, original, out.data_ptr(), _stream(stream))
+                       high_freq_factor, original, out.data_ptr(), _stream())
     return out
 
 
@@ -146,6 +169,9 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     """(q_out, k_out): queries [T, Hq, D] and keys [T, Hk, D] normed for each head (where a weight [D] is given) and
     their first ``table.shape[1]`` columns rotated by the angles of ``positions`` [T] (where a table is given).
     ``out = (q_out, k_out)`` may be (q, k) themselves."""
+    if stream is not None:
+        with _current(stream):
+            return qk_norm_rope(q, k, table, positions, q_weight, k_weight, eps, interleaved, out)
     qh, kh = _heads(q, "q"), _heads(k, "k")
     desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     if out is None:
@@ -155,7 +181,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
         _like(q_out, q.dtype, dev, qs, "q_out")
         _like(k_out, q.dtype, dev, ks, "k_out")
     status = _b.packed_calls().qk_norm_rope(desc, qh, kh, _heads(q_out, "q_out"), _heads(k_out, "k_out"),
-                                            _stream(stream))
+                                            _stream())
     if status:
         _b._check(status, "tide_qk_norm_rope")
     return q_out, k_out
@@ -165,6 +191,10 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
                       eps: float = 1e-6, interleaved: bool = False, out=None, workspace=None, stream=None):
     """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` from its outputs' gradients and its inputs.  A weight
     that is None has no gradient (None), and its ``q`` or ``k`` is used for its shape only."""
+    if stream is not None:
+        with _current(stream):
+            return qk_norm_rope_grad(dq_out, dk_out, q, k, table, positions, q_weight, k_weight, eps, interleaved, out,
+                                     workspace)
     desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     dtype = q.dtype
     _like(dq_out, dtype, dev, qs, "dq_out")
@@ -190,7 +220,7 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
                                    None if q_weight is None else _heads(q, "q"),
                                    None if k_weight is None else _heads(k, "k"), _heads(dq, "dq"), _heads(dk, "dk"),
                                    0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(), ws, n,
-                                   _stream(stream))
+                                   _stream())
     if status:
         _b._check(status, "tide_qk_norm_rope_grad")
     return dq, dk, dqw, dkw
@@ -235,6 +265,9 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None,
     """(loss, lse), both fp32 [T]: every token's cross entropy of the logits ``x @ weight.T`` (x [T, H], weight
     [V, H], bf16) and the log of its sum of exponentials, which :func:`linear_cross_entropy_grad` takes.  The logits
     are not written to memory.  An ignored token's loss is 0."""
+    if stream is not None:
+        with _current(stream):
+            return linear_cross_entropy(x, weight, targets, ignore_index, out, workspace)
     desc, dev, T = _ce_desc(x, weight, targets, ignore_index)
     if out is None:
         loss, lse = _empty(T, dtype=_F32, device=x.device), _empty(T, dtype=_F32, device=x.device)
@@ -243,7 +276,7 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None,
         _per_token(loss, dev, T, "loss")
         _per_token(lse, dev, T, "lse")
     _keep, ws, n = _scratch(_b.tide_ce_loss_workspace(desc), workspace, x.device)
-    _b.tide_ce_loss(desc, loss.data_ptr(), lse.data_ptr(), ws, n, _stream(stream))
+    _b.tide_ce_loss(desc, loss.data_ptr(), lse.data_ptr(), ws, n, _stream())
     return loss, lse
 
 
@@ -251,6 +284,9 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
                               stream=None):
     """(dx, dweight) of :func:`linear_cross_entropy` from its lse and the gradient ``dloss`` (fp32 [T]) of its losses
     (the mean over n tokens: 1 / n everywhere).  bf16, like x and weight."""
+    if stream is not None:
+        with _current(stream):
+            return linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index, out, workspace)
     desc, dev, T = _ce_desc(x, weight, targets, ignore_index)
     _per_token(lse, dev, T, "lse")
     _per_token(dloss, dev, T, "dloss")
@@ -262,7 +298,7 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
         _like(dw, _BF16, dev, weight.shape, "dweight")
     _keep, ws, n = _scratch(_b.tide_ce_grad_workspace(desc), workspace, x.device)
     _b.tide_ce_grad(desc, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), _rows(dx, "dx"), dw.data_ptr(),
-                    _rows(dw, "dweight"), ws, n, _stream(stream))
+                    _rows(dw, "dweight"), ws, n, _stream())
     return dx, dw
 
 
@@ -299,6 +335,9 @@ def new_ckpt8(rows: int, cols: int, device="cuda") -> Ckpt8:
 
 def swiglu_ckpt8(gate, up, out=None, stream=None):
     """(h, ckpt): h = silu(gate) * up ([rows, cols], bf16 or fp32) and gate and up in 8 bits.  ``out = (h, ckpt)``."""
+    if stream is not None:
+        with _current(stream):
+            return swiglu_ckpt8(gate, up, out)
     dtype, shape = gate.dtype, gate.shape
     dt = _dtype(dtype, "gate")
     dev = _device(gate, "gate")
@@ -314,7 +353,7 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
         _like(h, dtype, dev, shape, "h")
         hs, desc = _rows(h, "h"), _ckpt_desc(ckpt, rows, cols, dev)
     status = _b.packed_calls().swiglu_ckpt8(rows, cols, dt, gate.data_ptr(), gs, up.data_ptr(), us, h.data_ptr(), hs,
-                                            desc, _stream(stream))
+                                            desc, _stream())
     if status:
         _b._check(status, "tide_swiglu_ckpt8")
     return h, ckpt
@@ -323,6 +362,9 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
 def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=None):
     """(dgate, dup, h) of SwiGLU at the checkpoint's values; h, recomputed, is for the weight gradient of the
     projection that follows (None without ``need_h``).  ``out = (dgate, dup, h)``."""
+    if stream is not None:
+        with _current(stream):
+            return swiglu_ckpt8_grad(ckpt, dh, out, need_h)
     dtype, shape = dh.dtype, dh.shape
     dt = _dtype(dtype, "dh")
     dev = _device(dh, "dh")
@@ -340,7 +382,7 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
     status = _b.packed_calls().swiglu_ckpt8_grad(rows, cols, dt, desc, dh.data_ptr(), ds, dgate.data_ptr(),
                                                  _rows(dgate, "dgate"), dup.data_ptr(), _rows(dup, "dup"),
                                                  0 if h is None else h.data_ptr(), 0 if h is None else _rows(h, "h"),
-                                                 _stream(stream))
+                                                 _stream())
     if status:
         _b._check(status, "tide_swiglu_ckpt8_grad")
     return dgate, dup, h
@@ -348,4 +390,7 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
 
 def device_status(stream=None) -> int:
     """Reads and clears the operators' status word: TIDE_OK, or TIDE_ERR_TIMEOUT if a bounded wait expired."""
-    return _b.tide_ops_device_status(_stream(stream))
+    if stream is not None:
+        with _current(stream):
+            return device_status()
+    return _b.tide_ops_device_status(_stream())

@@ -1,0 +1,111 @@
+"""The torch wrappers' own work, on the CPU with stand-ins for the library and
+the streams: where memory is allocated, what is refused, what autograd sees."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+BF16 = torch.bfloat16
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it lies on a CUDA device."""
+    dev = 0
+
+    def get_device(self):
+        return self.dev
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+class OnGpu1(OnGpu):
+    dev = 1
+
+
+def put(t, kind=OnGpu):
+    return t.as_subclass(kind)
+
+
+class Library:
+    """Takes every call for a success; keeps the name and the arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*a):
+            if "workspace" in name:
+                return 256
+            self.calls.append((name, a))
+            return 0
+        return call
+
+
+@pytest.fixture
+def world(monkeypatch):
+    """Device 0 is current, with stream 5; allocations note the stream that was current."""
+    from all_gather_gb300 import _binding as b, ops
+    w = types.SimpleNamespace(current=5, allocated=[], lib=Library(), ops=ops)
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, w.current = w.current, s.cuda_stream
+        yield
+        w.current = before
+
+    def noting(f):
+        def alloc(*a, **kw):
+            w.allocated.append(w.current)
+            kw.pop("device", None)
+            return f(*a, **kw).as_subclass(OnGpu)
+        return alloc
+
+    monkeypatch.setattr(ops, "_current_device", lambda: 0)
+    monkeypatch.setattr(ops, "_raw_stream", lambda d: w.current)
+    monkeypatch.setattr(ops, "_empty", noting(torch.empty))
+    monkeypatch.setattr(ops, "_empty_like", noting(torch.empty_like))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw: types.SimpleNamespace(cuda_stream=raw))
+    monkeypatch.setattr(b, "packed_calls", lambda: w.lib)
+    for name in ("tide_ce_loss", "tide_ce_grad", "tide_ce_loss_workspace", "tide_ce_grad_workspace", "tide_rope_table"):
+        monkeypatch.setattr(b, name, getattr(w.lib, name))
+    return w
+
+
+def calls(ops, kind=OnGpu):
+    """Every operator on tensors of `kind`: name -> function of further arguments."""
+    bf = lambda *s: put(torch.zeros(s, dtype=BF16), kind)  # noqa: E731
+    q, k, wt = bf(4, 2, 64), bf(4, 1, 64), bf(64)
+    table, pos = put(torch.zeros(10, 64), kind), put(torch.zeros(4, dtype=torch.int64), kind)
+    x, w, y = bf(4, 64), bf(100, 64), put(torch.zeros(4, dtype=torch.int64), kind)
+    per = put(torch.zeros(4), kind)
+    ckpt = ops.Ckpt8(*(put(torch.zeros(s, dtype=t), kind) for s, t in (
+        ((4, 64), torch.float8_e4m3fn), ((4, 1), torch.uint8)) * 2))
+    return {
+        "qk_norm_rope": lambda **kw: ops.qk_norm_rope(q, k, table, pos, wt, wt, **kw),
+        "qk_norm_rope_grad": lambda **kw: ops.qk_norm_rope_grad(q, k, q, k, table, pos, wt, wt, **kw),
+        "linear_cross_entropy": lambda **kw: ops.linear_cross_entropy(x, w, y, **kw),
+        "linear_cross_entropy_grad": lambda **kw: ops.linear_cross_entropy_grad(x, w, y, per, per, **kw),
+        "swiglu_ckpt8": lambda **kw: ops.swiglu_ckpt8(x, x, **kw),
+        "swiglu_ckpt8_grad": lambda **kw: ops.swiglu_ckpt8_grad(ckpt, x, **kw),
+    }
+
+
+NAMES = ("qk_norm_rope", "qk_norm_rope_grad", "linear_cross_entropy", "linear_cross_entropy_grad", "swiglu_ckpt8",
+         "swiglu_ckpt8_grad")
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("passed", [None, 5, 7, "object"])
+def test_memory_belongs_to_the_stream_of_the_work(world, name, passed):
+    """Outputs and scratch memory are allocated with the launch's stream current: memory that is given back while the
+    work runs then goes to later work on that stream only."""
+    stream = types.SimpleNamespace(cuda_stream=7) if passed == "object" else passed
+    calls(world.ops)[name](stream=stream)
+    want = 5 if passed in (None, 5) else 7
+    assert world.allocated and set(world.allocated) == {want}
+    assert [a[-1] for _, a in world.lib.calls] == [want]
+    assert world.current == 5
