@@ -66,9 +66,12 @@ def _dtype(dtype, name):
 
 
 def _device(t, name) -> int:
+    """The current device, which is where a call launches: a tensor on another one is refused."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} is not on a CUDA device")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on CUDA device {dev}, and device {_current_device()} is current")
     return dev
 
 
@@ -85,13 +88,13 @@ def _new(t):
     return _empty_like(t, memory_format=_CONTIGUOUS)
 
 
-def _scratch(n: int, workspace, device):
-    """Scratch memory: (tensor that keeps it alive, pointer, bytes)."""
+def _scratch(n: int, workspace, like):
+    """Scratch memory on the device of `like`: (tensor that keeps it alive, pointer, bytes)."""
     if workspace is None:
-        workspace = _empty(n, dtype=torch.uint8, device=device)
+        workspace = _empty(n, dtype=torch.uint8, device=like.device)
         return workspace, workspace.data_ptr(), n
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -109,10 +112,11 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling {scaling!r}: need one of {list(ROPE_SCALINGS)}")
     if out is None:
-        out = torch.empty((max_position, rotary_dim), dtype=torch.float32, device=device or "cuda")
+        out = _empty((max_position, rotary_dim), dtype=torch.float32, device="cuda" if device is None else device)
     elif (out.dtype != torch.float32 or not out.is_cuda or not out.is_contiguous()
           or tuple(out.shape) != (max_position, rotary_dim)):
         raise ValueError(f"out must be a contiguous float32 CUDA tensor [{max_position}, {rotary_dim}]")
+    _device(out, "out")
     _b.tide_rope_table(max_position, rotary_dim, base, ROPE_SCALINGS[scaling], factor, low_freq_factor,
                        high_freq_factor, original, out.data_ptr(), _stream())
     return out
@@ -140,8 +144,7 @@ def _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved):
     T, Hq, D = qs
     if k.dtype is not dtype or k.get_device() != dev or ks[0] != T or ks[2] != D:
         raise ValueError("q and k must agree in type, device, tokens and head_dim")
-    if dev < 0:
-        raise ValueError("q is not on a CUDA device")
+    _device(q, "q")
     R = P = tp = pp = 0
     pos_bytes = 8
     if table is not None:
@@ -215,7 +218,7 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
     lib, ws, n = _b.packed_calls(), 0, 0
     if q_weight is not None or k_weight is not None or workspace is not None:
         need = _b._size(lib.qk_norm_rope_grad_workspace(desc), "tide_qk_norm_rope_grad_workspace")
-        _keep, ws, n = _scratch(need, workspace, q.device)
+        _keep, ws, n = _scratch(need, workspace, q)
     status = lib.qk_norm_rope_grad(desc, _heads(dq_out, "dq_out"), _heads(dk_out, "dk_out"),
                                    None if q_weight is None else _heads(q, "q"),
                                    None if k_weight is None else _heads(k, "k"), _heads(dq, "dq"), _heads(dk, "dk"),
@@ -275,7 +278,7 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None,
         loss, lse = out
         _per_token(loss, dev, T, "loss")
         _per_token(lse, dev, T, "lse")
-    _keep, ws, n = _scratch(_b.tide_ce_loss_workspace(desc), workspace, x.device)
+    _keep, ws, n = _scratch(_b.tide_ce_loss_workspace(desc), workspace, x)
     _b.tide_ce_loss(desc, loss.data_ptr(), lse.data_ptr(), ws, n, _stream())
     return loss, lse
 
@@ -296,7 +299,7 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
         dx, dw = out
         _like(dx, _BF16, dev, x.shape, "dx")
         _like(dw, _BF16, dev, weight.shape, "dweight")
-    _keep, ws, n = _scratch(_b.tide_ce_grad_workspace(desc), workspace, x.device)
+    _keep, ws, n = _scratch(_b.tide_ce_grad_workspace(desc), workspace, x)
     _b.tide_ce_grad(desc, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), _rows(dx, "dx"), dw.data_ptr(),
                     _rows(dw, "dweight"), ws, n, _stream())
     return dx, dw

@@ -109,3 +109,24 @@ def test_memory_belongs_to_the_stream_of_the_work(world, name, passed):
     assert world.allocated and set(world.allocated) == {want}
     assert [a[-1] for _, a in world.lib.calls] == [want]
     assert world.current == 5
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_on_another_device_than_the_current_are_refused(world, name):
+    """A call launches on the current device: tensors of another one are refused before anything is allocated."""
+    with pytest.raises(ValueError, match="device 1, and device 0 is current"):
+        calls(world.ops, OnGpu1)[name]()
+    assert not world.allocated and not world.lib.calls
+
+
+def test_workspace_and_table_on_another_device_are_refused(world):
+    far = put(torch.zeros(1 << 12, dtype=torch.uint8), OnGpu1)
+    for name in ("qk_norm_rope_grad", "linear_cross_entropy", "linear_cross_entropy_grad"):
+        with pytest.raises(ValueError, match="workspace"):
+            calls(world.ops)[name](workspace=far)
+        calls(world.ops)[name](workspace=put(torch.zeros(1 << 12, dtype=torch.uint8)))
+    assert len(world.lib.calls) == 3
+    with pytest.raises(ValueError, match="out is on CUDA device 1"):
+        world.ops.rope_table(10, 64, out=put(torch.zeros(10, 64), OnGpu1))
+    world.ops.rope_table(10, 64, out=put(torch.zeros(10, 64)))
+    assert len(world.lib.calls) == 4
