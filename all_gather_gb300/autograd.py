@@ -5,12 +5,37 @@ forward pass keeps what the gradient reads and nothing else: the inputs of the
 head norm (its statistics are computed again), the hidden states, weight and
 log-sums of the cross entropy (the logits are computed again), and the 8-bit
 codes of a SwiGLU's gate and up (the inputs themselves are not kept).
+
+They can be differentiated once: a gradient taken with ``create_graph`` raises
+an error when it is differentiated itself.
 """
 from __future__ import annotations
 
 import torch
 
 from . import ops
+
+
+class _Once(torch.autograd.Function):
+    """Gradients of a backward pass that is recorded itself: they depend on `links`, and going through them again is an
+    error.  (once_differentiable lets it pass where the incoming gradients are constants.)"""
+
+    @staticmethod
+    def forward(ctx, n, *grads_and_links):
+        return grads_and_links[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("all_gather_gb300.autograd: the operators have no second derivatives")
+
+
+def _once(grads, *links):
+    """What a backward pass returns, None among it; links: tensors that the gradients depend on."""
+    if not torch.is_grad_enabled():  # not recorded
+        return grads
+    some = [g for g in grads if g is not None]
+    passed = iter(_Once.apply(len(some), *some, *[t for t in links if t is not None]))
+    return tuple(None if g is None else next(passed) for g in grads)
 
 
 class _QkNormRope(torch.autograd.Function):
@@ -22,10 +47,11 @@ class _QkNormRope(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dq, dk):
+        given = dq, dk
         q, k, table, positions, q_weight, k_weight = ctx.saved_tensors
         dq, dk, dqw, dkw = ops.qk_norm_rope_grad(_rows(dq), _rows(dk), q, k, table, positions, q_weight, k_weight,
                                                  *ctx.how)
-        return dq, dk, None, None, dqw, dkw, None, None
+        return _once((dq, dk, None, None, dqw, dkw, None, None), *given, q, k, q_weight, k_weight)
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
@@ -40,20 +66,22 @@ class _LinearCrossEntropy(torch.autograd.Function):
     def backward(ctx, dloss):
         x, weight, targets, lse = ctx.saved_tensors
         dx, dw = ops.linear_cross_entropy_grad(x, weight, targets, lse, dloss.contiguous(), ctx.ignore_index)
-        return dx, dw, None, None
+        return _once((dx, dw, None, None), dloss, x, weight)
 
 
 class _SwigluCkpt8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, gate, up):
         h, ckpt = ops.swiglu_ckpt8(gate, up)
-        ctx.save_for_backward(*ckpt)
-        return h
+        link = h.new_empty(0)  # an output, so that it leads to gate and up, which are not kept
+        ctx.save_for_backward(*ckpt, link)
+        return h, link
 
     @staticmethod
-    def backward(ctx, dh):
-        dgate, dup, _ = ops.swiglu_ckpt8_grad(ops.Ckpt8(*ctx.saved_tensors), _rows(dh), need_h=False)
-        return dgate, dup
+    def backward(ctx, dh, _):
+        *ckpt, link = ctx.saved_tensors
+        dgate, dup, _ = ops.swiglu_ckpt8_grad(ops.Ckpt8(*ckpt), _rows(dh), need_h=False)
+        return _once((dgate, dup), dh, link)
 
 
 def _rows(t):
@@ -75,4 +103,4 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100):
 def swiglu(gate, up):
     """silu(gate) * up, differentiable, keeping gate and up in 8 bits for the backward pass (so its gradients are those
     at the 8-bit values)."""
-    return _SwigluCkpt8.apply(gate, up)
+    return _SwigluCkpt8.apply(gate, up)[0]

@@ -60,7 +60,7 @@ def world(monkeypatch):
         def alloc(*a, **kw):
             w.allocated.append(w.current)
             kw.pop("device", None)
-            return f(*a, **kw).as_subclass(OnGpu)
+            return f(*a, **kw).zero_().as_subclass(OnGpu)
         return alloc
 
     monkeypatch.setattr(ops, "_current_device", lambda: 0)
@@ -130,3 +130,63 @@ def test_workspace_and_table_on_another_device_are_refused(world):
         world.ops.rope_table(10, 64, out=put(torch.zeros(10, 64), OnGpu1))
     world.ops.rope_table(10, 64, out=put(torch.zeros(10, 64)))
     assert len(world.lib.calls) == 4
+
+
+# ------------------------------------------------------------------------------------------ autograd
+
+@pytest.fixture
+def graphs(world, monkeypatch):
+    """The same, with every tensor on device 0 (autograd makes plain ones)."""
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    return world
+
+
+def leaves(*ts):
+    return [t.detach().requires_grad_() for t in ts]
+
+
+def differentiable(ad):
+    """Every differentiable operator: name -> (leaves, function that gives its first output)."""
+    bf = lambda *s: torch.zeros(s, dtype=BF16)  # noqa: E731
+    qk = leaves(bf(4, 2, 64), bf(4, 1, 64), bf(64), bf(64))
+    table, pos = torch.zeros(10, 64), torch.zeros(4, dtype=torch.int64)
+    ce = leaves(bf(4, 64), bf(100, 64))
+    gu = leaves(bf(4, 64), bf(4, 64))
+    return {
+        "qk_norm_rope": (qk, lambda: ad.qk_norm_rope(qk[0], qk[1], table, pos, qk[2], qk[3])[0]),
+        "linear_cross_entropy": (ce, lambda: ad.linear_cross_entropy(*ce, pos)),
+        "swiglu": (gu, lambda: ad.swiglu(*gu)),
+    }
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope", "linear_cross_entropy", "swiglu"])
+@pytest.mark.parametrize("curved", [False, True])
+def test_second_derivatives_are_refused(graphs, name, curved):
+    """A gradient with a graph of its own does not come back as a constant, whether or not the gradient that it was made
+    from was one: going through it again is an error, for all leaves and for each of them."""
+    from all_gather_gb300 import autograd as ad
+    xs, f = differentiable(ad)[name]
+
+    def loss():
+        y = f().float()
+        return (y * y if curved else y).sum()
+
+    grads = torch.autograd.grad(loss(), xs, create_graph=True)
+    assert len(grads) == len(xs) and all(g.requires_grad for g in grads)
+    for x in xs:
+        grads = torch.autograd.grad(loss(), xs, create_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivatives"):
+            torch.autograd.grad(loss() + sum(g.float().pow(2).sum() for g in grads), x)
+    grads = torch.autograd.grad(loss(), xs, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivatives"):
+        (loss() + sum(g.float().pow(2).sum() for g in grads)).backward()
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope", "linear_cross_entropy", "swiglu"])
+def test_first_derivatives_have_no_graph(graphs, name):
+    from all_gather_gb300 import autograd as ad
+    xs, f = differentiable(ad)[name]
+    f().float().sum().backward()
+    assert all(x.grad is not None and not x.grad.requires_grad for x in xs)
+    grads = torch.autograd.grad(f().float().sum(), xs, create_graph=True)
+    (f().float().sum() + sum(g.detach().float().sum() for g in grads)).backward()  # used as numbers
