@@ -41,6 +41,8 @@ def _once(grads, *links):
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, table, positions, q_weight, k_weight, eps, interleaved):
+        if ctx.needs_input_grad[2]:
+            raise ValueError("table has no gradient here, and requires one")
         ctx.save_for_backward(q, k, table, positions, q_weight, k_weight)
         ctx.how = eps, interleaved
         return ops.qk_norm_rope(q, k, table, positions, q_weight, k_weight, eps, interleaved)
@@ -56,17 +58,22 @@ class _QkNormRope(torch.autograd.Function):
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, targets, ignore_index):
-        loss, lse = ops.linear_cross_entropy(x, weight, targets, ignore_index)
+    def forward(ctx, x, weight, targets, ignore_index, workspace):
+        loss, lse = ops.linear_cross_entropy(x, weight, targets, ignore_index, workspace=workspace)
         ctx.save_for_backward(x, weight, targets, lse)
         ctx.ignore_index = ignore_index
-        return loss
+        ctx.set_materialize_grads(False)
+        return loss, lse
 
     @staticmethod
-    def backward(ctx, dloss):
+    def backward(ctx, dloss, dlse):
+        if dlse is not None:
+            raise RuntimeError("all_gather_gb300.autograd: lse has no gradient, the loss has")
+        if dloss is None:
+            return None, None, None, None, None
         x, weight, targets, lse = ctx.saved_tensors
         dx, dw = ops.linear_cross_entropy_grad(x, weight, targets, lse, dloss.contiguous(), ctx.ignore_index)
-        return _once((dx, dw, None, None), dloss, x, weight)
+        return _once((dx, dw, None, None, None), dloss, x, weight)
 
 
 class _SwigluCkpt8(torch.autograd.Function):
@@ -75,10 +82,11 @@ class _SwigluCkpt8(torch.autograd.Function):
         h, ckpt = ops.swiglu_ckpt8(gate, up)
         link = h.new_empty(0)  # an output, so that it leads to gate and up, which are not kept
         ctx.save_for_backward(*ckpt, link)
-        return h, link
+        ctx.mark_non_differentiable(*ckpt)
+        return h, link, *ckpt
 
     @staticmethod
-    def backward(ctx, dh, _):
+    def backward(ctx, dh, *_):
         *ckpt, link = ctx.saved_tensors
         dgate, dup, _ = ops.swiglu_ckpt8_grad(ops.Ckpt8(*ckpt), _rows(dh), need_h=False)
         return _once((dgate, dup), dh, link)
@@ -97,7 +105,19 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
 
 def linear_cross_entropy(x, weight, targets, ignore_index: int = -100):
     """The losses [T] of :func:`ops.linear_cross_entropy`, differentiable in x and weight."""
-    return _LinearCrossEntropy.apply(x, weight, targets, ignore_index)
+    return loss_and_lse(x, weight, targets, ignore_index)[0]
+
+
+def loss_and_lse(x, weight, targets, ignore_index: int = -100, workspace=None):
+    """(loss, lse) of :func:`ops.linear_cross_entropy`, the loss differentiable in x and weight; a gradient of lse is
+    refused."""
+    return _LinearCrossEntropy.apply(x, weight, targets, ignore_index, workspace)
+
+
+def swiglu_and_ckpt8(gate, up):
+    """(h, ckpt) of :func:`ops.swiglu_ckpt8`, h differentiable in gate and up as :func:`swiglu` is; the codes are not."""
+    h, _, *ckpt = _SwigluCkpt8.apply(gate, up)
+    return h, ops.Ckpt8(*ckpt)
 
 
 def swiglu(gate, up):

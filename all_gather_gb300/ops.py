@@ -12,7 +12,10 @@ may still be using is the caller's to order, as with any asynchronous call.
 
 Every operator has its gradient as a function of its own that takes and
 returns plain tensors; gradients of parameters have the parameter's type and
-can be written straight into a gradient arena with ``out``.
+can be written straight into a gradient arena with ``out``.  Where autograd
+records and an input requires a gradient, an operator's outputs lead back to it
+(``all_gather_gb300.autograd``), and ``out`` is refused, as torch's own
+operators do; under ``torch.no_grad`` it is allowed.
 """
 from __future__ import annotations
 
@@ -28,6 +31,7 @@ ROPE_SCALINGS = {None: 0, "linear": 1, "by_parts": 2}
 _BF16, _F32 = torch.bfloat16, torch.float32
 _raw_stream, _current_device, _empty = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch.empty
 _empty_like, _CONTIGUOUS = torch.empty_like, torch.contiguous_format
+_recording = torch.is_grad_enabled
 
 # These wrappers run once for every layer and token, in front of kernels of a
 # few microseconds: each attribute is read once, checks are plain comparisons,
@@ -96,6 +100,18 @@ def _scratch(n: int, workspace, like):
     if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _recorded(out, *inputs) -> bool:
+    """Whether autograd has to know of this call."""
+    if not _recording():
+        return False
+    for t in inputs:
+        if t is not None and t.requires_grad:
+            if out is not None:
+                raise RuntimeError("out is given and an input requires a gradient: autograd cannot record this call")
+            return True
+    return False
 
 
 # ------------------------------------------------------------------ head norm with rotation
@@ -175,6 +191,9 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     if stream is not None:
         with _current(stream):
             return qk_norm_rope(q, k, table, positions, q_weight, k_weight, eps, interleaved, out)
+    if _recorded(out, q, k, table, q_weight, k_weight):
+        from . import autograd
+        return autograd.qk_norm_rope(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     qh, kh = _heads(q, "q"), _heads(k, "k")
     desc, dev, qs, ks = _qk_desc(q, k, table, positions, q_weight, k_weight, eps, interleaved)
     if out is None:
@@ -267,10 +286,13 @@ def _rows(t, name) -> int:
 def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None, workspace=None, stream=None):
     """(loss, lse), both fp32 [T]: every token's cross entropy of the logits ``x @ weight.T`` (x [T, H], weight
     [V, H], bf16) and the log of its sum of exponentials, which :func:`linear_cross_entropy_grad` takes.  The logits
-    are not written to memory.  An ignored token's loss is 0."""
+    are not written to memory.  An ignored token's loss is 0.  lse itself has no gradient."""
     if stream is not None:
         with _current(stream):
             return linear_cross_entropy(x, weight, targets, ignore_index, out, workspace)
+    if _recorded(out, x, weight):
+        from . import autograd
+        return autograd.loss_and_lse(x, weight, targets, ignore_index, workspace)
     desc, dev, T = _ce_desc(x, weight, targets, ignore_index)
     if out is None:
         loss, lse = _empty(T, dtype=_F32, device=x.device), _empty(T, dtype=_F32, device=x.device)
@@ -341,6 +363,9 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
     if stream is not None:
         with _current(stream):
             return swiglu_ckpt8(gate, up, out)
+    if _recorded(out, gate, up):
+        from . import autograd
+        return autograd.swiglu_and_ckpt8(gate, up)
     dtype, shape = gate.dtype, gate.shape
     dt = _dtype(dtype, "gate")
     dev = _device(gate, "gate")

@@ -190,3 +190,71 @@ def test_first_derivatives_have_no_graph(graphs, name):
     assert all(x.grad is not None and not x.grad.requires_grad for x in xs)
     grads = torch.autograd.grad(f().float().sum(), xs, create_graph=True)
     (f().float().sum() + sum(g.detach().float().sum() for g in grads)).backward()  # used as numbers
+
+
+def top_level(ops):
+    """Every operator on leaves: name -> (leaves, function of further arguments that gives the outputs)."""
+    bf = lambda *s: torch.zeros(s, dtype=BF16)  # noqa: E731
+    qk = leaves(bf(4, 2, 64), bf(4, 1, 64), bf(64), bf(64))
+    table, pos = torch.zeros(10, 64), torch.zeros(4, dtype=torch.int64)
+    ce = leaves(bf(4, 64), bf(100, 64))
+    gu = leaves(bf(4, 64), bf(4, 64))
+    return {
+        "qk_norm_rope": (qk, lambda **kw: ops.qk_norm_rope(qk[0], qk[1], table, pos, qk[2], qk[3], **kw)),
+        "linear_cross_entropy": (ce, lambda **kw: ops.linear_cross_entropy(*ce, pos, **kw)),
+        "swiglu_ckpt8": (gu, lambda **kw: ops.swiglu_ckpt8(*gu, **kw)),
+    }
+
+
+def flat(out):
+    return [t for o in out for t in (o if isinstance(o, tuple) else (o,))]
+
+
+@pytest.mark.parametrize("stream", [None, 7])
+@pytest.mark.parametrize("name", ["qk_norm_rope", "linear_cross_entropy", "swiglu_ckpt8"])
+def test_operators_do_not_drop_the_graph(graphs, name, stream):
+    """Outputs of inputs that require a gradient lead back to them, each of the inputs by itself too; without them, or
+    without recording, outputs are plain."""
+    xs, f = top_level(graphs.ops)[name]
+    out = f(stream=stream)
+    assert out[0].requires_grad
+    out[0].float().sum().backward()
+    assert all(x.grad is not None for x in xs)
+    for x in xs:
+        x.requires_grad_(False)
+    assert not any(t.requires_grad for t in flat(f(stream=stream)))
+    for x in xs:
+        x.requires_grad_()
+        assert f()[0].requires_grad or (name == "qk_norm_rope" and f()[1].requires_grad)
+        x.requires_grad_(False)
+    xs[0].requires_grad_()
+    with torch.no_grad():
+        assert not any(t.requires_grad for t in flat(f(stream=stream)))
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope", "linear_cross_entropy", "swiglu_ckpt8"])
+def test_out_is_refused_where_a_gradient_is_wanted(graphs, name):
+    xs, f = top_level(graphs.ops)[name]
+    with torch.no_grad():
+        out = f()
+        f(out=out)
+    n = len(graphs.lib.calls)
+    with pytest.raises(RuntimeError, match="out is given"):
+        f(out=out)
+    assert len(graphs.lib.calls) == n
+
+
+def test_lse_and_table_have_no_gradient(graphs):
+    """What has no gradient here is refused instead of left out."""
+    xs, f = top_level(graphs.ops)["linear_cross_entropy"]
+    loss, lse = f()
+    with pytest.raises(RuntimeError, match="lse has no gradient"):
+        (loss.sum() + lse.square().sum()).backward()
+    ckpt = top_level(graphs.ops)["swiglu_ckpt8"][1]()[1]
+    assert not any(t.requires_grad for t in ckpt)
+    q = torch.zeros(4, 2, 64, dtype=BF16)
+    table, pos = torch.zeros(10, 64, requires_grad=True), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="table has no gradient"):
+        graphs.ops.qk_norm_rope(q, q, table, pos)
+    with torch.no_grad():
+        graphs.ops.qk_norm_rope(q, q, table, pos)
