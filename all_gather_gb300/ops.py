@@ -114,6 +114,13 @@ def _recorded(out, *inputs) -> bool:
     return False
 
 
+def _written(*tensors):
+    """Autograd's versions of tensors that the caller passed and the library has written."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 # ------------------------------------------------------------------ head norm with rotation
 
 def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -206,6 +213,8 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
                                             _stream())
     if status:
         _b._check(status, "tide_qk_norm_rope")
+    if out is not None:
+        _written(q_out, k_out)
     return q_out, k_out
 
 
@@ -245,6 +254,8 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, table=None, positions=None, q_weight
                                    _stream())
     if status:
         _b._check(status, "tide_qk_norm_rope_grad")
+    if out is not None:
+        _written(dq, dk, dqw, dkw)
     return dq, dk, dqw, dkw
 
 
@@ -302,6 +313,8 @@ def linear_cross_entropy(x, weight, targets, ignore_index: int = -100, out=None,
         _per_token(lse, dev, T, "lse")
     _keep, ws, n = _scratch(_b.tide_ce_loss_workspace(desc), workspace, x)
     _b.tide_ce_loss(desc, loss.data_ptr(), lse.data_ptr(), ws, n, _stream())
+    if out is not None:
+        _written(loss, lse)
     return loss, lse
 
 
@@ -324,6 +337,8 @@ def linear_cross_entropy_grad(x, weight, targets, lse, dloss, ignore_index: int 
     _keep, ws, n = _scratch(_b.tide_ce_grad_workspace(desc), workspace, x)
     _b.tide_ce_grad(desc, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), _rows(dx, "dx"), dw.data_ptr(),
                     _rows(dw, "dweight"), ws, n, _stream())
+    if out is not None:
+        _written(dx, dw)
     return dx, dw
 
 
@@ -384,6 +399,8 @@ def swiglu_ckpt8(gate, up, out=None, stream=None):
                                             desc, _stream())
     if status:
         _b._check(status, "tide_swiglu_ckpt8")
+    if out is not None:
+        _written(h, *ckpt)
     return h, ckpt
 
 
@@ -413,6 +430,8 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
                                                  _stream())
     if status:
         _b._check(status, "tide_swiglu_ckpt8_grad")
+    if out is not None:
+        _written(dgate, dup, h)
     return dgate, dup, h
 
 

@@ -258,3 +258,24 @@ def test_lse_and_table_have_no_gradient(graphs):
         graphs.ops.qk_norm_rope(q, q, table, pos)
     with torch.no_grad():
         graphs.ops.qk_norm_rope(q, q, table, pos)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_written_outputs_are_known_to_autograd(graphs, name):
+    """A tensor that a call wrote through `out` counts as changed, so that a graph that kept it refuses to go on."""
+    f = calls(graphs.ops)[name]
+    out = f()
+    before = [t._version for t in flat(out) if t is not None]
+    f(out=out)
+    assert [t._version for t in flat(out) if t is not None] == [v + 1 for v in before]
+    with torch.inference_mode():
+        f(out=f())
+
+
+def test_rotation_in_place_of_a_kept_tensor_is_noticed(graphs):
+    q, k = (torch.zeros(4, 2, 64, dtype=BF16) for _ in range(2))
+    w = torch.ones(64, requires_grad=True)
+    y = (q.float() * w).sum() + (q * q.detach().requires_grad_()).sum()  # keeps q
+    graphs.ops.qk_norm_rope(q, k, out=(q, k))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
