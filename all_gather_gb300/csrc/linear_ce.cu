@@ -5,11 +5,15 @@
 //   dz = (exp(z - lse) - [v = target]) dloss,  dx = dz W,  dW = dz^T x
 //
 // The loss takes tiles of the logits as they are made: each tile leaves, for
-// each of its tokens, its maximum m and sum s of exp(z - m), and a second kernel
-// joins a token's pairs in a fixed order.  That kernel also takes the target's
-// logit, as a dot product of its own: the tensor cores cut the last bits of
-// their sums towards zero, which averages out in lse but not in a single logit
-// (8192 x 131072 x 4096: the loss is 9e-7 off, 1.4e-6 with the tensor cores').
+// each of its tokens, its maximum m and sum s of exp(z - m), the target's logit
+// left out, and a second kernel joins a token's pairs in a fixed order.  That
+// kernel also takes the target's logit, as a dot product of its own: the tensor
+// cores cut the last bits of their sums towards zero, which averages out in lse
+// but not in a single logit (8192 x 131072 x 4096: the loss is 9e-7 off, 1.4e-6
+// with the tensor cores').  With z_t in one form only, the loss is
+//   log(1 + sum over v != t of exp(z_v - z_t)),
+// which no rounding makes negative and which keeps its digits where the target
+// dominates and lse - z_t would cancel (4096 columns, z_t = 30: 2e-4 off).
 //
 // The gradient makes the logits again, a piece of the vocabulary at a time, and
 // keeps only that piece's dz, rounded to bf16: the products take operands of
@@ -351,14 +355,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
             const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
             const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
-            // kDz: the lane's token of each 32 columns, before the wait: target (as a row of the warp's), lse, factor.
+            // Before the wait, the lane's token of each 32 columns: kStats and kDz: target (as a row of the warp's);
+            // kDz: lse, factor.
             int64_t hit[4];
             float lse[4], scale[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t t = n0 + k * 32 + lane;
                 int64_t y = -1;
-                if (E == kDz && k * 32 < width && t < g.N)
+                if ((E == kStats || E == kDz) && k * 32 < width && t < g.N)
                     y = g.y.get(t);
                 hit[k] = y - g.v0 - m0;
                 lse[k] = INFINITY, scale[k] = 0.f;  // an ignored token: exp(z - lse) = 0
@@ -400,6 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 }
                 if (E == kStats) {
                     turn_over(out, lane, v);  // v[r]: vocabulary row m0 + r of the lane's token
+                    const int64_t at = hit[c / 32];
+                    if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {  // its target: joined later
+#pragma unroll
+                        for (int r = 0; r < 32; ++r)
+                            if (at == r)
+                                v[r] = __float_as_uint(-INFINITY);
+                    }
                     stats[c / 32] = stats_of(v, rows);
                 } else if (E == kAdd) {
                     if (lane == 0)
@@ -628,10 +640,28 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
     float z = dots[row];
     for (int k = 1; k < parts; ++k)  // rows < 8: parts of a token are `rows` warps apart
         z += dots[row + k * rows];
-    const float l = logf(s.y) + (isinf(s.x) ? 0.f : s.x);
+    // s has every logit but the target's, if there is one.
     const int64_t v = y.get(t);
+    float l, e = 0.f;
+    if (v < 0 || !isfinite(z)) {
+        l = logf(s.y) + (isinf(s.x) ? 0.f : s.x);
+        if (v >= 0) {
+            if (!(z < 0.f) && !isnan(l))
+                l = z;
+            e = l - z;
+        } else if (v == -2) {
+            e = __int_as_float(0x7fffffff);
+        }
+    } else if (s.x <= z) {
+        e = log1pf(s.y * expf(s.x - z));
+        l = z + e;
+    } else {
+        e = logf(s.y + expf(z - s.x));
+        l = s.x + e;
+        e += s.x - z;
+    }
     lse[t] = l;
-    loss[t] = v == -1 ? 0.f : v == -2 ? __int_as_float(0x7fffffff) : l - z;
+    loss[t] = e;
 }
 
 // What dz is kept relative to: the largest finite |dloss| of the tokens that

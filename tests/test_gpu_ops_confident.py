@@ -1,0 +1,59 @@
+"""Cross entropy of tokens that are predicted well: losses near 0, where lse and the target's logit nearly cancel."""
+import pytest
+import torch
+
+import ops_reference as ref
+from test_gpu_ops import BF16, F32, close, gen, randn, tide  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def confident(seed, T, V, H, top=30.0, rivals=False):
+    """Hidden states along their target's row, with target logits up to `top`; rivals: and as much along another row."""
+    g = gen(seed)
+    w = randn(g, (V, H), BF16, H ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    a = torch.linspace(1, top, T, device="cuda")[:, None]
+    x = a * w[y].float()
+    if rivals:
+        x += a * w[(y + 1) % V].float() * torch.rand((T, 1), generator=g, device="cuda")
+    return x.to(BF16), w, y
+
+
+def exact(x, w, y):
+    """(loss, lse, 1 - p of the target, target's logit), 64 bits, the loss without a cancellation."""
+    z = x.double() @ w.double().t()
+    at = torch.arange(len(y), device="cuda")
+    zt = z[at, y].clone()
+    lse = torch.logsumexp(z, 1)
+    z[at, y] = -float("inf")
+    loss = torch.nn.functional.softplus(torch.logsumexp(z, 1) - zt, threshold=1e9)
+    return loss, lse, -torch.expm1(-loss), zt
+
+
+def logit_errors(x, w, y):
+    """Largest |error| of the other logits (every sum of the tensor cores cut once) and of the target's (an fp32 chain
+    of H / 32 + 16)."""
+    terms = x.double().abs() @ w.double().abs().t()
+    H = x.shape[1]
+    return (H + 8) * 2 * ref.U32 * terms.amax(1), (H / 32 + 16) * ref.U32 * (x.double() * w[y].double()).abs().sum(1)
+
+
+CASES = [(64, 4096, 64, 30, False), (64, 4096, 4096, 30, False), (300, 1000, 1024, 40, False), (1, 5000, 2048, 30, False),
+         (200, 3000, 4096, 40, True), (7, 32768, 2048, 25, True), (2100, 700, 256, 30, False), (40, 1, 64, 30, False),
+         (40, 2, 64, 60, True)]
+
+
+@pytest.mark.parametrize("T, V, H, top, rivals", CASES)
+def test_losses_of_well_predicted_tokens(tide, T, V, H, top, rivals):
+    """The loss's error is that of the logits, (1 - p) of it as d loss = sum of p_v (dz_v - dz_t) over the others, and
+    roundings of its own; it is never negative."""
+    x, w, y = confident(T + V + H, T, V, H, top, rivals)
+    loss, lse = tide.linear_cross_entropy(x, w, y)
+    assert (loss >= 0).all()
+    want, wl, q, zt = exact(x, w, y)
+    ev, et = logit_errors(x, w, y)
+    own = 32 * ref.U32 * (1 + zt.abs() + wl.abs())  # the exponentials' arguments and results, the logarithm
+    close(loss, want, 1.1 * q * (ev + et + own) + 8 * ref.U32 * want, "loss")
+    close(lse, wl, et + q * ev + own, "lse")
+    assert rivals or T == 1 or (want < 1e-4).any()
