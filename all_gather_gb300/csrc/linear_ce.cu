@@ -20,7 +20,10 @@
 // one type, and its error is that of rounding x or W once more.  dz is kept
 // relative to the largest |dloss|, which the results are multiplied by at their
 // end: the usual dloss, the same for all tokens, would else put its own
-// rounding on every term, where it does not average out.
+// rounding on every term, where it does not average out.  The target's own dz,
+// p - 1, is expm1(z_t - lse) of the same dot product: from the tensor cores'
+// logit it would be off by their cut, 2e-4 at z_t = 30, which is more than a
+// well-predicted token's whole gradient.
 //
 // All products run in one persistent kernel, a pair of blocks (two SMs) on tiles
 // of 256 rows and up to 256 columns: in each block a thread fetches 64 columns
@@ -101,7 +104,7 @@ struct Gemm {
     int64_t v0;          // first vocabulary row of this piece
     Targets y;
     float2 *part;        // kStats: [128-row tiles][N]
-    const float *lse, *dloss, *unit;  // unit: what dz is relative to
+    const float *lse, *dloss, *unit, *miss;  // unit: what dz is relative to; miss: p - 1 of each token's target
     bf16 *out;           // kStore
     int64_t out_stride;
     int out_tiles;       // its rows are on 16-byte boundaries: stored as tiles
@@ -356,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
             const int rows = int(max(int64_t(0), min(int64_t(32), g.M - m0)));  // of the warp's
             // Before the wait, the lane's token of each 32 columns: kStats and kDz: target (as a row of the warp's);
-            // kDz: lse, factor.
+            // kDz: lse, factor, the target's dz.
             int64_t hit[4];
-            float lse[4], scale[4];
+            float lse[4], scale[4], dz_hit[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int64_t t = n0 + k * 32 + lane;
@@ -366,10 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 if ((E == kStats || E == kDz) && k * 32 < width && t < g.N)
                     y = g.y.get(t);
                 hit[k] = y - g.v0 - m0;
-                lse[k] = INFINITY, scale[k] = 0.f;  // an ignored token: exp(z - lse) = 0
+                lse[k] = INFINITY, scale[k] = 0.f, dz_hit[k] = 0.f;  // an ignored token: exp(z - lse) = 0
                 if (E == kDz && y != -1) {
                     lse[k] = g.lse[t];
                     scale[k] = y == -2 ? __int_as_float(0x7fffffff) : __fdiv_rn(g.dloss[t], unit);
+                    dz_hit[k] = g.miss[t] * scale[k];
                 }
             }
             bool ready = um::mbar_wait<false, 100>(acc_full + 8 * buf, buf_phase, &gave_up, g.wait_ns);
@@ -459,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                             for (int j = 0; j < 32; ++j)
                                 if (hits >> j & 1) {
                                     const int r = __shfl_sync(0xffffffffu, int(at), j);
-                                    const float f = __shfl_sync(0xffffffffu, scale[c / 32], j);
+                                    const float f = __shfl_sync(0xffffffffu, dz_hit[c / 32], j);
                                     if (lane == r)
-                                        v[j] = __float_as_uint(__uint_as_float(v[j]) - f);
+                                        v[j] = __float_as_uint(f);
                                 }
                         }
                         // A row of the tile is a token: two bytes of it a lane.
@@ -577,6 +581,25 @@ __global__ void __launch_bounds__(256) unalign_kernel(const bf16 *in, int64_t pi
     }
 }
 
+// A lane's share of the dot product of two rows on 16-byte boundaries, of which
+// its warp takes part `part` of `parts`.
+__device__ __forceinline__ float dot_share(const bf16 *a, const bf16 *b, int H, int lane, int part, int parts)
+{
+    float z = 0.f;
+    const int whole = H / 8;
+    for (int i = part * 32 + lane; i < whole; i += 32 * parts) {
+        float p[8], q[8];
+        tide::load8(a + 8 * i, p);
+        tide::load8(b + 8 * i, q);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            z = __fmaf_rn(p[k], q[k], z);
+    }
+    if (part == 0 && whole * 8 + lane < H)
+        z = __fmaf_rn(tide::to_f32(a[whole * 8 + lane]), tide::to_f32(b[whole * 8 + lane]), z);
+    return z;
+}
+
 // Joins the pairs (maximum, sum) of `rows` neighbouring tokens a block, 256 /
 // rows slices of the vocabulary tiles each, and takes their targets' logits, a
 // warp a token or, where there are fewer than eight, a part of one.
@@ -592,20 +615,8 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
     for (int r = rows < 8 ? warp % rows : warp; r < rows; r += 8) {
         const int64_t v = t0 + r < T ? y.get(t0 + r) : -1;
         float z = 0.f;
-        if (v >= 0) {
-            const bf16 *a = x + (t0 + r) * x_stride, *b = w + v * w_stride;
-            const int mine = rows < 8 ? warp / rows : 0, whole = H / 8;
-            for (int i = mine * 32 + lane; i < whole; i += 32 * parts) {
-                float p[8], q[8];
-                tide::load8(a + 8 * i, p);
-                tide::load8(b + 8 * i, q);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    z = __fmaf_rn(p[k], q[k], z);
-            }
-            if (mine == 0 && whole * 8 + lane < H)
-                z = __fmaf_rn(tide::to_f32(a[whole * 8 + lane]), tide::to_f32(b[whole * 8 + lane]), z);
-        }
+        if (v >= 0)
+            z = dot_share(x + (t0 + r) * x_stride, w + v * w_stride, H, lane, rows < 8 ? warp / rows : 0, parts);
 #pragma unroll
         for (int o = 16; o > 0; o /= 2)
             z += __shfl_xor_sync(0xffffffffu, z, o);
@@ -664,10 +675,27 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
     loss[t] = e;
 }
 
-// What dz is kept relative to: the largest finite |dloss| of the tokens that
-// count, 1 if that is 0.
-__global__ void __launch_bounds__(1024) unit_kernel(const float *dloss, Targets y, int64_t T, float *unit)
+// Block 0: what dz is kept relative to: the largest finite |dloss| of the tokens
+// that count, 1 if that is 0.  The others: p - 1 of the tokens' targets, a warp
+// a token (0 where there is none).
+__global__ void __launch_bounds__(1024) unit_kernel(const float *dloss, Targets y, int64_t T, float *unit,
+                                                    const bf16 *x, int64_t x_stride, const bf16 *w, int64_t w_stride,
+                                                    int H, const float *lse, float *miss)
 {
+    if (blockIdx.x) {
+        const int lane = threadIdx.x % 32;
+        const int64_t t = (int64_t(blockIdx.x) - 1) * 32 + threadIdx.x / 32;
+        if (t >= T)
+            return;
+        const int64_t v = y.get(t);
+        float z = v < 0 ? 0.f : dot_share(x + t * x_stride, w + v * w_stride, H, lane, 0, 1);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0)
+            miss[t] = v < 0 ? 0.f : expm1f(z - lse[t]);
+        return;
+    }
     __shared__ float tops[32];
     float top = 0.f;
 #pragma unroll 4
@@ -924,7 +952,7 @@ tide_status_t launch(Gemm &g, const Mat &a, const Mat &b, const char *what, cuda
 struct Layout {
     int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
     int64_t part = 0;                   // loss
-    int64_t dz = 0, acc = 0, unit = 0, piece = 0, acc_pitch = 0;  // gradient
+    int64_t dz = 0, acc = 0, unit = 0, miss = 0, piece = 0, acc_pitch = 0;  // gradient
     int splits = 1, tile_n = kN;        // of dx
     int64_t bytes = 0;
     int64_t take(int64_t n)
@@ -952,6 +980,7 @@ Layout layout_of(const tide_ce_t *ce, bool grad)
         l.dz = l.take(ce->tokens * l.piece * 2);
         l.acc = l.take(sum * l.splits);
         l.unit = l.take(4);
+        l.miss = l.take(ce->tokens * 4);
     } else {
         l.part = l.take((ce->vocab + 2 * kM - 1) / (2 * kM) * 2 * ce->tokens * 8);
     }
@@ -1065,16 +1094,18 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
         s = align_rows(w, ws, l.w, l.pitch, st);
     bf16 *dz = reinterpret_cast<bf16 *>(ws + l.dz);
     float *acc = reinterpret_cast<float *>(ws + l.acc), *unit = reinterpret_cast<float *>(ws + l.unit);
+    float *miss = reinterpret_cast<float *>(ws + l.miss);
     if (s)
         return s;
-    unit_kernel<<<1, 1024, 0, st>>>(dloss, base(ce).y, T, unit);
+    unit_kernel<<<unsigned(1 + (T + 31) / 32), 1024, 0, st>>>(dloss, base(ce).y, T, unit, x.p, x.stride, w.p, w.stride,
+                                                              int(H), lse, miss);
     s = tide::op_launched("ce_grad: unit");
     for (int64_t v0 = 0; !s && v0 < V; v0 += l.piece) {
         const int64_t n = std::min(l.piece, V - v0);
         const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece, l.piece};
         Gemm g = base(ce);
         g.v0 = v0;
-        g.lse = lse, g.dloss = dloss, g.unit = unit;
+        g.lse = lse, g.dloss = dloss, g.unit = unit, g.miss = miss;
         s = make_map(&g.c, dzp, 32, 32);
         if (!s)
             s = launch<kDz>(g, wp, x, "ce_grad: dz", st);

@@ -57,3 +57,28 @@ def test_losses_of_well_predicted_tokens(tide, T, V, H, top, rivals):
     close(loss, want, 1.1 * q * (ev + et + own) + 8 * ref.U32 * want, "loss")
     close(lse, wl, et + q * ev + own, "lse")
     assert rivals or T == 1 or (want < 1e-4).any()
+
+
+@pytest.mark.parametrize("T, V, H, top, rivals", [c for c in CASES if c[1] > 1])
+def test_gradients_of_well_predicted_tokens(tide, T, V, H, top, rivals):
+    """dz of a target is p - 1, however near 0, to the error of the target's logit: H / 32 roundings in each lane, each
+    below U32 of the lane's share of the sum, taken as independent (six deviations), and the lanes' sum of 5 to 8."""
+    x, w, y = confident(T + V + H + 1, T, V, H, top, rivals)
+    _, wl, q, zt = exact(x, w, y)
+    lse = wl.float()
+    dloss = torch.rand(T, generator=gen(T), device="cuda") / T + 1e-3
+    dx, dw = tide.linear_cross_entropy_grad(x, w, y, lse, dloss)
+    ev, _ = logit_errors(x, w, y)
+    x, w, s = x.double(), w.double(), dloss.double()[:, None]
+    et = (6 * H ** 0.5 / 32 + 10) * ref.U32 * (x * w[y]).abs().sum(1) + 4 * ref.U32 * (zt - lse.double()).abs()
+    at = torch.arange(T, device="cuda")
+    d = torch.exp(x @ w.t() - lse.double()[:, None])
+    err = d * (ev + 64 * ref.U32 * (1 + lse.double().abs()))[:, None]
+    err[at, y] = d[at, y] * et
+    d[at, y] = torch.expm1(zt - lse.double())
+    d, err = d * s, (err + ref.U16 * d.abs()) * s
+    n = max(T, V) + 64
+    for got, want, e, terms, what in (
+            (dx, d @ w, err @ w.abs(), d.abs() @ w.abs(), "dx"),
+            (dw, d.t() @ x, err.t() @ x.abs(), d.abs().t() @ x.abs(), "dweight")):
+        close(got, want, e + n * 2 * ref.U32 * terms + ref.U16 * want.abs() + 1e-30, what)
