@@ -676,47 +676,75 @@ __global__ void __launch_bounds__(256) join_kernel(const float2 *part, int tiles
 }
 
 // Block 0: what dz is kept relative to: the largest finite |dloss| of the tokens
-// that count, 1 if that is 0.  The others: p - 1 of the tokens' targets, a warp
-// a token (0 where there is none).
-__global__ void __launch_bounds__(1024) unit_kernel(const float *dloss, Targets y, int64_t T, float *unit,
-                                                    const bf16 *x, int64_t x_stride, const bf16 *w, int64_t w_stride,
-                                                    int H, const float *lse, float *miss)
+// that count, 1 if that is 0.  The others, a token each: its hidden state into
+// the workspace, rows `pitch` (a multiple of 8) apart on 16-byte boundaries, and
+// p - 1 of its target (0 where there is none).  An ignored token's row becomes
+// zeroes, for its dz is 0, and 0 times what it holds need not be.
+// ALIGNED: x and weight have their rows on 16-byte boundaries, and H % 8 = 0.
+// Bound by loads that wait for one another: 513 x 2048 takes 4.4 us, with a
+// warp a token 7.5 us.
+template <bool ALIGNED>
+__global__ void __launch_bounds__(256) prepare_kernel(const float *dloss, Targets y, int64_t T, float *unit,
+                                                      const bf16 *x, int64_t x_stride, const bf16 *w, int64_t w_stride,
+                                                      int H, const float *lse, float *miss, bf16 *out, int64_t pitch)
 {
+    __shared__ float shares[8];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (blockIdx.x) {
-        const int lane = threadIdx.x % 32;
-        const int64_t t = (int64_t(blockIdx.x) - 1) * 32 + threadIdx.x / 32;
-        if (t >= T)
-            return;
-        const int64_t v = y.get(t);
-        float z = v < 0 ? 0.f : dot_share(x + t * x_stride, w + v * w_stride, H, lane, 0, 1);
+        const int64_t t = int64_t(blockIdx.x) - 1, v = y.get(t);
+        const float l = lse[t];
+        const bf16 *a = x + t * x_stride, *b = w + max(v, int64_t(0)) * w_stride;
+        float z = 0.f;
+        for (int c = 8 * threadIdx.x; c < H; c += 8 * 256) {
+            uint32_t p[4], q[4];
+            if constexpr (ALIGNED) {
+                const uint4 i = *reinterpret_cast<const uint4 *>(a + c), j = *reinterpret_cast<const uint4 *>(b + c);
+                p[0] = i.x, p[1] = i.y, p[2] = i.z, p[3] = i.w;
+                q[0] = j.x, q[1] = j.y, q[2] = j.z, q[3] = j.w;
+            } else {
+                tide::load16_any(a + c, a + H, p);
+                tide::load16_any(b + c, b + H, q);
+            }
+            const uint32_t kept = v == -1 ? 0 : ~0u;
+            *reinterpret_cast<uint4 *>(out + t * pitch + c) =
+                make_uint4(p[0] & kept, p[1] & kept, p[2] & kept, p[3] & kept);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t high = k % 2 ? 0xffff0000u : 0xffffu, up = k % 2 ? 0 : 16;
+                if (ALIGNED || c + k < H)
+                    z = __fmaf_rn(__uint_as_float((p[k / 2] & high) << up), __uint_as_float((q[k / 2] & high) << up), z);
+            }
+        }
 #pragma unroll
         for (int o = 16; o > 0; o /= 2)
             z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0)
-            miss[t] = v < 0 ? 0.f : expm1f(z - lse[t]);
+            shares[warp] = z;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int k = 1; k < 8; ++k)
+                z += shares[k];
+            miss[t] = v < 0 ? 0.f : expm1f(z - l);
+        }
         return;
     }
-    __shared__ float tops[32];
     float top = 0.f;
-#pragma unroll 4
-    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+#pragma unroll 8
+    for (int64_t t = threadIdx.x; t < T; t += 256) {
         const float d = fabsf(dloss[t]);
-        if (d > top && d < INFINITY && y.get(t) != -1)
+        if (y.get(t) != -1 && d > top && d < INFINITY)
             top = d;
     }
 #pragma unroll
     for (int o = 16; o > 0; o /= 2)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (threadIdx.x % 32 == 0)
-        tops[threadIdx.x / 32] = top;
+    if (lane == 0)
+        shares[warp] = top;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        top = tops[threadIdx.x];
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (threadIdx.x == 0)
-            *unit = top > 0.f ? top : 1.f;
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < 8; ++k)
+            top = fmaxf(top, shares[k]);
+        *unit = top > 0.f ? top : 1.f;
     }
 }
 
@@ -950,7 +978,7 @@ tide_status_t launch(Gemm &g, const Mat &a, const Mat &b, const char *what, cuda
 
 // Where a call's scratch data lies in its workspace, in bytes.
 struct Layout {
-    int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x and weight, where they are needed
+    int64_t x = -1, w = -1, pitch = 0;  // aligned copies of x (always for the gradient) and weight, where needed
     int64_t part = 0;                   // loss
     int64_t dz = 0, acc = 0, unit = 0, miss = 0, piece = 0, acc_pitch = 0;  // gradient
     int splits = 1, tile_n = kN;        // of dx
@@ -967,7 +995,7 @@ Layout layout_of(const tide_ce_t *ce, bool grad)
 {
     Layout l;
     l.pitch = round_up(ce->hidden, 8);
-    if (!rows_aligned(ce->x, ce->x_stride, ce->tokens))
+    if (grad || !rows_aligned(ce->x, ce->x_stride, ce->tokens))
         l.x = l.take(ce->tokens * l.pitch * 2);
     if (!rows_aligned(ce->weight, ce->weight_stride, ce->vocab))
         l.w = l.take(ce->vocab * l.pitch * 2);
@@ -1089,17 +1117,17 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
     }
     Mat x = {static_cast<const bf16 *>(ce->x), T, H, ce->x_stride};
     Mat w = {static_cast<const bf16 *>(ce->weight), V, H, ce->weight_stride};
-    s = align_rows(x, ws, l.x, l.pitch, st);
-    if (!s)
-        s = align_rows(w, ws, l.w, l.pitch, st);
-    bf16 *dz = reinterpret_cast<bf16 *>(ws + l.dz);
+    bf16 *dz = reinterpret_cast<bf16 *>(ws + l.dz), *rows = reinterpret_cast<bf16 *>(ws + l.x);
     float *acc = reinterpret_cast<float *>(ws + l.acc), *unit = reinterpret_cast<float *>(ws + l.unit);
     float *miss = reinterpret_cast<float *>(ws + l.miss);
+    s = align_rows(w, ws, l.w, l.pitch, st);
     if (s)
         return s;
-    unit_kernel<<<unsigned(1 + (T + 31) / 32), 1024, 0, st>>>(dloss, base(ce).y, T, unit, x.p, x.stride, w.p, w.stride,
-                                                              int(H), lse, miss);
-    s = tide::op_launched("ce_grad: unit");
+    const bool aligned = H % 8 == 0 && rows_aligned(x.p, x.stride, T);  // w is, here
+    (aligned ? prepare_kernel<true> : prepare_kernel<false>)<<<unsigned(1 + T), 256, 0, st>>>(
+        dloss, base(ce).y, T, unit, x.p, x.stride, w.p, w.stride, int(H), lse, miss, rows, l.pitch);
+    s = tide::op_launched("ce_grad: rows");
+    x.p = rows, x.stride = l.pitch;
     for (int64_t v0 = 0; !s && v0 < V; v0 += l.piece) {
         const int64_t n = std::min(l.piece, V - v0);
         const Mat wp = {w.p + v0 * w.stride, n, H, w.stride}, dzp = {dz, T, n, l.piece, l.piece};

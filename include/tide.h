@@ -493,8 +493,9 @@ TIDE_API int64_t tide_ce_loss_workspace(const tide_ce_t *ce);
  * The logits are computed again, one piece of the vocabulary at a time; dz is
  * rounded to bf16 for the two products.  dx (bf16 [T, H], row stride
  * dx_stride) and dweight (bf16 [V, H], dweight_stride) are overwritten.  An
- * ignored token gives nothing, whatever its dloss; a target outside [0, V)
- * that is not ignore_index makes the token's dz NaN.
+ * ignored token gives nothing, whatever its dloss, lse and hidden state (they
+ * may be infinite or NaN); a target outside [0, V) that is not ignore_index
+ * makes the token's dz NaN.
  */
 TIDE_API tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *dloss, void *dx,
                                     int64_t dx_stride, void *dweight, int64_t dweight_stride, void *workspace,

@@ -82,3 +82,27 @@ def test_gradients_of_well_predicted_tokens(tide, T, V, H, top, rivals):
             (dx, d @ w, err @ w.abs(), d.abs() @ w.abs(), "dx"),
             (dw, d.t() @ x, err.t() @ x.abs(), d.abs().t() @ x.abs(), "dweight")):
         close(got, want, e + n * 2 * ref.U32 * terms + ref.U16 * want.abs() + 1e-30, what)
+
+
+@pytest.mark.parametrize("T, V, H, pad", [(9, 300, 64, 0), (150, 1000, 72, 8), (70, 515, 63, 0), (513, 400, 256, 0),
+                                          (33, 2000, 7, 1)])
+def test_ignored_tokens_that_are_not_finite(tide, T, V, H, pad):
+    """An ignored token's hidden state, lse and dloss give nothing, whatever they hold: the bits of a call in which they
+    are zero."""
+    g = gen(T)
+    x, w = randn(g, (T, H + pad), BF16)[:, :H], randn(g, (V, H), BF16, H ** -0.5)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    off = torch.arange(T, device="cuda") % 4 == 1
+    y[off] = -100
+    d = torch.rand(T, generator=g, device="cuda")
+    clean = torch.where(off[:, None], torch.zeros_like(x), x)
+    loss, lse = tide.linear_cross_entropy(clean, w, y)
+    want = tide.linear_cross_entropy_grad(clean, w, y, lse, d)
+    assert (want[0][off] == 0).all()
+    for value in (float("nan"), float("inf"), -float("inf"), 3e38):
+        odd = torch.where(off[:, None], torch.full_like(x, value), x)
+        got = tide.linear_cross_entropy(odd, w, y)[0]
+        assert torch.equal(got, loss)
+        fill = torch.full_like(d, value)
+        got = tide.linear_cross_entropy_grad(odd, w, y, torch.where(off, fill, lse), torch.where(off, fill, d))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
