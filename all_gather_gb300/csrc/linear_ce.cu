@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         const uint32_t acc_done = um::cluster_addr(acc_empty, 0);
         const float unit = E == kStore || E == kDz ? *g.unit : 1.f;
         int buf = 0, buf_phase = 0, out_at = 0;
-        for (int64_t i = first; i < works; i += step) {
+        int64_t i = first;
+        for (; i < works; i += step) {
             const Work w = work_of(g, i);
             const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32, m = m0 + lane;
             const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
@@ -534,6 +535,45 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         if (lane == 0)
             um::stores_read<0>();
         __syncwarp();
+        if (i < works) {  // a wait has run out: this tile and the later ones become NaN (0x7fff7fff: so is either half)
+            for (int j = 0; j < kOutTile / 512; ++j)
+                um::store_shared16(out + j * 512 + lane * 16, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            um::fence_copies();
+            __syncwarp();
+            for (; i < works; i += step) {
+                const Work w = work_of(g, i);
+                const int64_t m0 = (int64_t(w.m) * 2 + rank) * kM + quarter * 32;
+                const int64_t n0 = int64_t(w.n) * g.tile_n + half * half_n;
+                if (E == kStats) {
+                    const int64_t t = n0 + quarter * 32 + lane;
+                    if (quarter * 32 < width && t < g.N)
+                        g.part[(int64_t(w.m) * 2 + rank) * g.N + t] = make_float2(-INFINITY, __int_as_float(0x7fffffff));
+                    continue;
+                }
+                for (int c = 0; c < width; c += 32) {
+                    const int64_t n = n0 + c;
+                    if (n >= g.N || m0 >= g.M)
+                        continue;
+                    if (E == kStore && !g.out_tiles) {
+                        for (int64_t j = n; j < min(n + 32, g.N); ++j)
+                            if (m0 + lane < g.M)
+                                reinterpret_cast<uint16_t *>(g.out)[(m0 + lane) * g.out_stride + j] = 0x7fff;
+                    } else if (lane == 0) {
+                        if (E == kAdd && g.first)
+                            um::tma_store_3d(&g.c, out, int(n), int(m0), w.split);
+                        else if (E == kAdd)
+                            um::tma_add_3d(&g.c, out, int(n), int(m0), w.split);
+                        else
+                            um::tma_store_2d(&g.c, out, int(E == kDz ? m0 : n), int(E == kDz ? n : m0));
+                    }
+                }
+            }
+            if (lane == 0) {
+                um::stores_end();
+                um::stores_read<0>();
+            }
+            __syncwarp();
+        }
     }
     um::fence_before();
     __syncthreads();

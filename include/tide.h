@@ -470,7 +470,7 @@ typedef struct {
     int64_t ignore_index;    /* tokens with this target count for nothing */
     uint32_t debug;          /* 0, or TIDE_DEBUG_SHORT_WAIT (device-side waits of at most 50 ms instead of 4 s)
                                 and TIDE_DEBUG_SKIP_FILL (the first tile of every product waits for a fill that
-                                never comes: exercises the TIMEOUT status, the outputs are incomplete) */
+                                never comes: exercises the TIMEOUT status, what depends on it is NaN) */
 } tide_ce_t;
 
 /*
@@ -542,9 +542,9 @@ TIDE_API tide_status_t tide_swiglu_ckpt8_grad(int64_t rows, int64_t cols, int32_
 /*
  * Read and clear the operators' status word of the current device
  * (synchronises `stream`): TIDE_ERR_TIMEOUT if a bounded device-side wait of
- * tide_ce_loss or tide_ce_grad expired there since the last such read (the
- * outputs of that call are then incomplete), else TIDE_OK.  Not to be called
- * during a capture.
+ * tide_ce_loss or tide_ce_grad expired there since the last such read, else
+ * TIDE_OK.  What the wait kept from being computed is NaN in that call's
+ * outputs.  Not to be called during a capture.
  */
 TIDE_API tide_status_t tide_ops_device_status(void *stream);
 
