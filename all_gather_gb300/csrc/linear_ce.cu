@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     __shared__ uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
+    __shared__ int pair_gave_up, fills;  // told at the end: a block of the pair gave up; stages that this one filled
     const uint32_t full = um::smem_addr(bars), empty = full + 8 * kMaxStages;
     const uint32_t acc_full = empty + 8 * kMaxStages, acc_empty = acc_full + 16, drained = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         }
         um::mbar_init(drained, 1);
         um::fence_barrier_init();
-        gave_up = 0;
+        gave_up = pair_gave_up = 0;
         um::prefetch_map(&g.a);
         um::prefetch_map(&g.b);
     }
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     const uint32_t tmem = tmem_slot;
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    int stage = 0, turns = 0;  // of the fetch warp: ring position, and how often the ring went round
 
     // The two loops below set the pace of every step of the sum, a few hundred cycles: operand layouts are known at
     // compile time, addresses run along, and whether MN-major blocks come in one copy is settled outside.
@@ -233,8 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
         const bool leader = um::elected();
         const uint32_t full0 = um::cluster_addr(full, 0);  // both blocks' copies count at block 0's barriers
         const uint32_t tx = uint32_t(stage_bytes) * 2;
-        int stage = 0, turns = 0;                          // ring position, and how often the ring went round
-        bool ok = true;
         auto fetch = [&](auto copies) {
             constexpr bool one_copy = decltype(copies)::value;
             uint32_t at = ring, bar = 0;  // the stage's memory, and its barrier's offset
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
                 const Work w = work_of(g, i);
                 const int m = (w.m * 2 + rank) * kM, n = w.n * g.tile_n + rank * cols_b;
                 for (int k = w.s0 * kK; k < w.s1 * kK; k += kK) {
-                    if (!(ok = um::mbar_wait(empty + bar, (turns & 1) ^ 1, &gave_up, g.wait_ns)))
+                    if (!um::mbar_wait(empty + bar, (turns & 1) ^ 1, &gave_up, g.wait_ns))
                         return;
                     if (leader) {
                         if (rank == 0)
@@ -274,15 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
             fetch(std::true_type{});
         else
             fetch(std::false_type{});
-        __syncwarp();
-        if (!ok && rank == 0 && leader) {  // wait for the copies in flight before the pair's memory goes
-            for (int k = 0; k < g.stages; ++k) {
-                const int times = turns + (k < stage);
-                const uint64_t t0 = um::now_ns();
-                while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) && um::now_ns() - t0 < g.wait_ns) {
-                }
-            }
-        }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -577,7 +568,27 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) gemm_ke
     }
     um::fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && gave_up) {
+        for (int r = 0; r < 2; ++r)
+            um::store_cluster(um::cluster_addr(um::smem_addr(&pair_gave_up), r), 1);
+    }
+    if (threadIdx.x == 0)
+        fills = turns * g.stages + stage;
     um::cluster_sync();
+    if (pair_gave_up) {  // the pair's copies in flight land, for as long as another wait, before its memory goes
+        if (threadIdx.x == 0 && rank == 0) {
+            const int mine = fills, theirs = um::load_cluster(um::cluster_addr(um::smem_addr(&fills), 1));
+            const uint64_t t0 = um::now_ns();
+            for (int k = 0; k < g.stages; ++k) {
+                const int times = (max(mine, theirs) - k + g.stages - 1) / g.stages;  // fills of this stage
+                if ((mine - k + g.stages - 1) / g.stages < times)  // the other block was ahead: its bytes alone
+                    um::mbar_expect(full + 8 * k, uint32_t(stage_bytes));
+                while (times > 0 && !um::mbar_try(full + 8 * k, (times - 1) & 1) && um::now_ns() - t0 < g.wait_ns) {
+                }
+            }
+        }
+        um::cluster_sync();
+    }
     um::fence_after();
     if (warp == 1)
         um::tmem_free(tmem, kTmemCols);

@@ -67,6 +67,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, int x)
+{
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ int load_cluster(uint32_t addr)
+{
+    int x;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
