@@ -828,6 +828,12 @@ __global__ void __launch_bounds__(256) round_kernel(const float *acc, int splits
 
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// Rows apart, and less than the 2^40 bytes that a tensor map takes.
+bool stride_ok(int64_t rows, int64_t stride, int64_t cols)
+{
+    return tide::op_extent_ok(rows, stride) && (rows < 2 || (stride >= cols && stride < int64_t(1) << 39));
+}
+
 tide_status_t check_desc(const tide_ce_t *ce)
 {
     if (!ce)
@@ -840,8 +846,7 @@ tide_status_t check_desc(const tide_ce_t *ce)
         return op_fail(TIDE_ERR_INVALID_ARG, "unknown debug bits 0x%x", ce->debug);
     if (ce->target_bytes != 4 && ce->target_bytes != 8)
         return op_fail(TIDE_ERR_INVALID_ARG, "target_bytes %d: need 4 or 8", ce->target_bytes);
-    if (!tide::op_extent_ok(ce->tokens, ce->x_stride) || !tide::op_extent_ok(ce->vocab, ce->weight_stride) ||
-        (ce->tokens > 1 && ce->x_stride < ce->hidden) || (ce->vocab > 1 && ce->weight_stride < ce->hidden))
+    if (!stride_ok(ce->tokens, ce->x_stride, ce->hidden) || !stride_ok(ce->vocab, ce->weight_stride, ce->hidden))
         return op_fail(TIDE_ERR_INVALID_ARG, "x_stride %lld, weight_stride %lld for hidden %lld",
                        (long long)ce->x_stride, (long long)ce->weight_stride, (long long)ce->hidden);
     return TIDE_OK;
@@ -907,11 +912,8 @@ bool rows_aligned(const void *p, int64_t stride, int64_t rows)
 tide_status_t encode(CUtensorMap *map, CUtensorMapDataType type, int rank, void *p, const cuuint64_t *dims,
                      const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle)
 {
-    const EncodeTiled enc = encode_tiled();
-    if (!enc)
-        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint32_t step[3] = {1, 1, 1};
-    const CUresult r = enc(map, type, cuuint32_t(rank), p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUresult r = encode_tiled()(map, type, cuuint32_t(rank), p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
@@ -1018,13 +1020,22 @@ tide_status_t launch(Gemm &g, const Mat &a, const Mat &b, const char *what, cuda
         s = make_map(&g.c, {g.out, g.M, g.N, g.out_stride}, 32, 32);
     if (s)
         return s;
-    const cudaError_t e = tide::op_allow_smem<gemm_kernel<E>>(kSmemBytes);
-    if (e != cudaSuccess)
-        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     const int64_t works = int64_t(g.tiles_m) * g.tiles_n * g.splits;
     const unsigned grid = unsigned(std::min<int64_t>(works, std::max(tide::op_sm_count() / 2, 1))) * 2;
     gemm_kernel<E><<<grid, kThreads, kSmemBytes, st>>>(g);
     return tide::op_launched(what);
+}
+
+// What the products need besides good arguments, asked for before a call
+// enqueues anything.
+template <int... E>
+tide_status_t get_ready()
+{
+    if (!encode_tiled())
+        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    cudaError_t e = cudaSuccess;
+    ((e = e == cudaSuccess ? tide::op_allow_smem<gemm_kernel<E>>(kSmemBytes) : e), ...);
+    return e == cudaSuccess ? TIDE_OK : op_fail(TIDE_ERR_CUDA, "ce: %s", cudaGetErrorString(e));
 }
 
 // Where a call's scratch data lies in its workspace, in bytes.
@@ -1103,6 +1114,8 @@ tide_status_t tide_ce_loss(const tide_ce_t *ce, float *loss, float *lse, void *w
         return op_fail(TIDE_ERR_ALIGNMENT, "loss or lse is not aligned to its element size");
     const Layout l = layout_of(ce, false);
     s = check_workspace(workspace, workspace_bytes, l.bytes);
+    if (!s)
+        s = get_ready<kStats>();
     if (s)
         return s;
     const tide::NvtxRange range("tide_ce_loss");
@@ -1149,12 +1162,13 @@ tide_status_t tide_ce_grad(const tide_ce_t *ce, const float *lse, const float *d
         return op_fail(TIDE_ERR_INVALID_ARG, "lse, dloss, dx or dweight is NULL");
     if (!op_aligned(lse, 4) || !op_aligned(dloss, 4) || !op_aligned(dx, 2) || !op_aligned(dweight, 2))
         return op_fail(TIDE_ERR_ALIGNMENT, "lse, dloss, dx or dweight is not aligned to its element size");
-    if (!tide::op_extent_ok(ce->tokens, dx_stride) || !tide::op_extent_ok(ce->vocab, dweight_stride) ||
-        (ce->tokens > 1 && dx_stride < ce->hidden) || (ce->vocab > 1 && dweight_stride < ce->hidden))
+    if (!stride_ok(ce->tokens, dx_stride, ce->hidden) || !stride_ok(ce->vocab, dweight_stride, ce->hidden))
         return op_fail(TIDE_ERR_INVALID_ARG, "dx_stride %lld, dweight_stride %lld for hidden %lld",
                        (long long)dx_stride, (long long)dweight_stride, (long long)ce->hidden);
     const Layout l = layout_of(ce, true);
     s = check_workspace(workspace, workspace_bytes, l.bytes);
+    if (!s)
+        s = get_ready<kDz, kAdd, kStore>();
     if (s)
         return s;
     const tide::NvtxRange range("tide_ce_grad");

@@ -462,7 +462,7 @@ typedef struct {
     int64_t vocab;           /* V in [1, 2^31 - 512] */
     int64_t hidden;          /* H in [1, 2^20] */
     const void *x;           /* device bf16 [T, H] */
-    int64_t x_stride;        /* elements between rows, >= H */
+    int64_t x_stride;        /* elements between rows, >= H and below 2^39 (here and for the outputs) */
     const void *weight;      /* device bf16 [V, H] */
     int64_t weight_stride;
     const void *targets;     /* device integers [T] */

@@ -279,3 +279,27 @@ def test_rotation_in_place_of_a_kept_tensor_is_noticed(graphs):
     graphs.ops.qk_norm_rope(q, k, out=(q, k))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+# ------------------------------------------------------------------------------------------ the C calls
+
+def test_strides_that_no_tensor_map_takes_are_refused_at_once():
+    """Such a call used to fail half way, with kernels already under way."""
+    from all_gather_gb300 import _binding as b, build
+    build.build()
+    a, far = 0x7F0000000000, 1 << 39  # an address that is never read
+
+    def desc(x_stride=64, weight_stride=64):
+        return b.CeDesc(4, 100, 64, a, x_stride, a, weight_stride, a, 8, -100)
+
+    def refused(match, f, *args):
+        before = b.tide_launch_count()
+        with pytest.raises(b.TideError, match=match) as e:
+            f(*args)
+        assert e.value.status == b.TIDE_ERR_INVALID_ARG and b.tide_launch_count() == before
+
+    for d in (desc(x_stride=far), desc(weight_stride=far)):
+        refused("x_stride", b.tide_ce_loss, d, a, a, a, 1 << 50)
+        refused("x_stride", b.tide_ce_grad, d, a, a, a, 64, a, 64, a, 1 << 50)
+    refused("dx_stride", b.tide_ce_grad, desc(), a, a, a, far, a, 64, a, 1 << 50)
+    refused("dweight_stride", b.tide_ce_grad, desc(), a, a, a, 64, a, far, a, 1 << 50)
