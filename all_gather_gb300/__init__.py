@@ -38,7 +38,7 @@ from ._binding import (  # noqa: F401  (re-exported C-ABI names)
     tide_ops_device_status)
 
 _OPS = ("rope_table", "qk_norm_rope", "qk_norm_rope_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
-        "Ckpt8", "new_ckpt8", "swiglu_ckpt8", "swiglu_ckpt8_grad")
+        "Ckpt8", "new_ckpt8", "swiglu_ckpt8", "swiglu_ckpt8_grad", "device_status")
 
 
 def __getattr__(name):

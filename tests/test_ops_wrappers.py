@@ -303,3 +303,8 @@ def test_strides_that_no_tensor_map_takes_are_refused_at_once():
         refused("x_stride", b.tide_ce_grad, d, a, a, a, 64, a, 64, a, 1 << 50)
     refused("dx_stride", b.tide_ce_grad, desc(), a, a, a, far, a, 64, a, 1 << 50)
     refused("dweight_stride", b.tide_ce_grad, desc(), a, a, a, 64, a, far, a, 1 << 50)
+
+
+def test_the_status_is_read_next_to_the_operators(graphs):
+    import all_gather_gb300 as tide
+    assert tide.device_status is graphs.ops.device_status
