@@ -40,9 +40,9 @@
 // Bound by the tensor cores for many tokens and by the weight's bytes for few.
 // Measured: loss 8192 x 131072 x 4096 4.93 ms, 1,785 TFLOP/s (the clock held at
 // 1.7 GHz by the power limit; 128 x 256 tiles of single blocks 5.69 ms); 64 x
-// 131072 x 4096 162 us, 6.6 TB/s; 7 x 32768 x 2048 28 us, 4.8 TB/s.  Gradient
-// 4096 x 131072 x 4096 7.66 ms, 1,723 TFLOP/s (single blocks 9.5 ms); 513 x
-// 50001 x 2048 234 us, 1,346 TFLOP/s.
+// 131072 x 4096 162 us, 6.6 TB/s; 7 x 32768 x 2048 29 us, 4.6 TB/s.  Gradient
+// 4096 x 131072 x 4096 7.68 ms, 1,718 TFLOP/s (single blocks 9.5 ms); 513 x
+// 50001 x 2048 238 us, 1,324 TFLOP/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -48,7 +48,8 @@
  *     order 0, 1, ..., W-1 starting from rank 0's value; then y = alpha * sum;
  *     then out = old + y in accumulate mode.  No FMA contraction, no
  *     flush-to-zero.  Results are bitwise independent of CTA budget, chunk
- *     size, stage shape and scheduling.
+ *     size, stage shape and scheduling.  (The training-step operators below
+ *     have numerics of their own.)
  */
 #ifndef TIDE_H
 #define TIDE_H
@@ -376,6 +377,8 @@ TIDE_API tide_status_t tide_rs_fold_noalloc(int32_t world, int32_t num_params, c
  * types are TIDE_DTYPE_BF16 and TIDE_DTYPE_F32; strides are in elements and
  * innermost dimensions are contiguous; sums, statistics and intermediate
  * values are fp32 and rounded once, to nearest even, when they are stored.
+ * Products and sums are contracted (FMA), the tensor cores' sums are cut
+ * towards zero, and the cross entropy's exponentials below 2^-126 are 0.
  * Tensors are aligned to their element size; rows on 16-byte boundaries take
  * the vector paths.  Outputs must not overlap inputs or each other, except
  * that tide_qk_norm_rope and its gradient may write an output over the input
@@ -476,7 +479,7 @@ typedef struct {
 /*
  * Softmax cross entropy of every token, with the logits taken in pieces of
  * the vocabulary and kept nowhere:
- *   lse[t] = log sum_v exp(z_tv);  loss[t] = lse[t] - z_t,target.
+ *   lse[t] = log sum_v exp(z_tv);  loss[t] = lse[t] - z_t,target  (>= 0).
  * loss and lse are device fp32 [T].  An ignored token's loss is 0; a target
  * outside [0, V) that is not ignore_index makes the token's loss NaN.
  * bf16 only.  Rows that are not on 16-byte boundaries are copied into the
