@@ -12,9 +12,10 @@ functions mirror the C entry points one to one, and :class:`Plan` is a thin
 convenience wrapper that takes torch tensors and passes their pointers.
 torch is used for device memory and streams only.
 
-The operators of the training step around the collectives (norm of queries
-and keys with the position rotation, vocabulary cross entropy, SwiGLU with
-8-bit checkpoints, each with its gradient) are in :mod:`all_gather_gb300.ops`
+The operators of the training step around the collectives (layer norm, norm
+of queries and keys with the position rotation, attention over packed
+sequences, SwiGLU with 8-bit checkpoints, vocabulary cross entropy, each with
+its gradient) are in :mod:`all_gather_gb300.ops`
 and re-exported here.
 """
 from __future__ import annotations
@@ -35,10 +36,12 @@ from ._binding import (  # noqa: F401  (re-exported C-ABI names)
     tide_bruck_schedule, tide_sm_probe, tide_sm_probe_max_clusters, tide_corun_cta_budget, pointer_array,
     tide_rope_table, tide_qk_norm_rope, tide_qk_norm_rope_grad, tide_qk_norm_rope_grad_workspace, tide_ce_loss,
     tide_ce_loss_workspace, tide_ce_grad, tide_ce_grad_workspace, tide_swiglu_ckpt8, tide_swiglu_ckpt8_grad,
-    tide_ops_device_status)
+    tide_attention, tide_attention_grad, tide_attention_grad_workspace, tide_layer_norm, tide_layer_norm_grad,
+    tide_layer_norm_grad_workspace, tide_ops_device_status)
 
 _OPS = ("rope_table", "qk_norm_rope", "qk_norm_rope_grad", "linear_cross_entropy", "linear_cross_entropy_grad",
-        "Ckpt8", "new_ckpt8", "swiglu_ckpt8", "swiglu_ckpt8_grad", "device_status")
+        "Ckpt8", "new_ckpt8", "swiglu_ckpt8", "swiglu_ckpt8_grad", "attention", "attention_grad", "layer_norm",
+        "layer_norm_grad", "device_status")
 
 
 def __getattr__(name):

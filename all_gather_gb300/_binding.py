@@ -40,7 +40,9 @@ EXPORTED = ("tide_plan_build", "tide_plan_rebind", "tide_rs_fold", "tide_ag_plac
             "tide_rs_wave_zero_mask", "tide_bruck_schedule", "tide_sm_probe", "tide_sm_probe_max_clusters",
             "tide_corun_cta_budget", "tide_rope_table", "tide_qk_norm_rope", "tide_qk_norm_rope_grad",
             "tide_qk_norm_rope_grad_workspace", "tide_ce_loss", "tide_ce_loss_workspace", "tide_ce_grad",
-            "tide_ce_grad_workspace", "tide_swiglu_ckpt8", "tide_swiglu_ckpt8_grad", "tide_ops_device_status")
+            "tide_ce_grad_workspace", "tide_swiglu_ckpt8", "tide_swiglu_ckpt8_grad", "tide_attention", "tide_attention_grad",
+            "tide_attention_grad_workspace", "tide_layer_norm", "tide_layer_norm_grad",
+            "tide_layer_norm_grad_workspace", "tide_ops_device_status")
 
 
 class WavePlan(ctypes.Structure):
@@ -94,6 +96,19 @@ class CeDesc(ctypes.Structure):
 class Ckpt8Desc(ctypes.Structure):
     _fields_ = [("gate_codes", ctypes.c_void_p), ("gate_exps", ctypes.c_void_p), ("up_codes", ctypes.c_void_p),
                 ("up_exps", ctypes.c_void_p)]
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("offset_bytes", ctypes.c_int32), ("sequences", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("debug", ctypes.c_uint32)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("center", ctypes.c_int32), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -175,6 +190,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.tide_swiglu_ckpt8.restype = st
     lib.tide_swiglu_ckpt8_grad.argtypes = [i64, i64, i32, P(Ckpt8Desc), vp, i64, vp, i64, vp, i64, vp, i64, vp]
     lib.tide_swiglu_ckpt8_grad.restype = st
+    lib.tide_attention.argtypes = [P(AttentionDesc)] + [P(Heads)] * 4 + [vp, vp]
+    lib.tide_attention.restype = st
+    lib.tide_attention_grad.argtypes = [P(AttentionDesc)] + [P(Heads)] * 5 + [vp] + [P(Heads)] * 3 + [vp, i64, vp]
+    lib.tide_attention_grad.restype = st
+    lib.tide_attention_grad_workspace.argtypes = [P(AttentionDesc)]
+    lib.tide_attention_grad_workspace.restype = i64
+    lib.tide_layer_norm.argtypes = [P(NormDesc), vp, i64, vp, i64, vp]
+    lib.tide_layer_norm.restype = st
+    lib.tide_layer_norm_grad.argtypes = [P(NormDesc), vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]
+    lib.tide_layer_norm_grad.restype = st
+    lib.tide_layer_norm_grad_workspace.argtypes = [P(NormDesc)]
+    lib.tide_layer_norm_grad_workspace.restype = i64
     lib.tide_ops_device_status.argtypes = [vp]
     lib.tide_ops_device_status.restype = st
     _lib = lib
@@ -385,11 +412,14 @@ def tide_qk_norm_rope_grad(qk: QkDesc, dq_out: Heads, dk_out: Heads, q: Optional
 
 class PackedCalls:
     """The operators that run for every token, with their structures as packed bytes: a third of the time of filling
-    ctypes structures.  Layouts are those of tide_qk_t, tide_heads_t and tide_ckpt8_t.  Calls return the status."""
+    ctypes structures.  Layouts are those of tide_qk_t, tide_heads_t,
+    tide_ckpt8_t, tide_attention_t and tide_norm_t.  Calls return the status."""
 
     qk = struct.Struct("qiiiiqPPiiifPP").pack
     heads = struct.Struct("Pqq").pack
     ckpt8 = struct.Struct("PPPP").pack
+    attention = struct.Struct("qiiiifiqPI4x").pack
+    norm = struct.Struct("qqiiPPf4x").pack
 
     def __init__(self):
         lib = load_library()
@@ -407,6 +437,14 @@ class PackedCalls:
         self.swiglu_ckpt8 = function("tide_swiglu_ckpt8", i64, i64, i32, vp, i64, vp, i64, vp, i64, raw, vp)
         self.swiglu_ckpt8_grad = function("tide_swiglu_ckpt8_grad", i64, i64, i32, raw, vp, i64, vp, i64, vp, i64, vp,
                                           i64, vp)
+        self.attention_forward = function("tide_attention", *[raw] * 5, vp, vp)
+        self.attention_grad = function("tide_attention_grad", *[raw] * 6, vp, *[raw] * 3, vp, i64, vp)
+        self.attention_grad_workspace = function("tide_attention_grad_workspace", raw)
+        self.attention_grad_workspace.restype = i64
+        self.layer_norm = function("tide_layer_norm", raw, vp, i64, vp, i64, vp)
+        self.layer_norm_grad = function("tide_layer_norm_grad", raw, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp)
+        self.layer_norm_grad_workspace = function("tide_layer_norm_grad_workspace", raw)
+        self.layer_norm_grad_workspace.restype = i64
 
 
 _packed: Optional[PackedCalls] = None
@@ -458,6 +496,36 @@ def tide_swiglu_ckpt8_grad(rows: int, cols: int, dtype: int, ckpt: Ckpt8Desc, dh
     _check(load_library().tide_swiglu_ckpt8_grad(rows, cols, dtype, ckpt, dh or None, dh_stride, dgate or None,
                                                  dgate_stride, dup or None, dup_stride, h or None, h_stride,
                                                  stream or None), "tide_swiglu_ckpt8_grad")
+
+
+def tide_attention(at: AttentionDesc, q: Heads, k: Heads, v: Heads, o: Heads, lse: int, stream: int = 0) -> None:
+    _check(load_library().tide_attention(at, q, k, v, o, lse or None, stream or None), "tide_attention")
+
+
+def tide_attention_grad_workspace(at: AttentionDesc) -> int:
+    return _size(load_library().tide_attention_grad_workspace(at), "tide_attention_grad_workspace")
+
+
+def tide_attention_grad(at: AttentionDesc, dout: Heads, q: Heads, k: Heads, v: Heads, o: Heads, lse: int, dq: Heads,
+                        dk: Heads, dv: Heads, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().tide_attention_grad(at, dout, q, k, v, o, lse or None, dq, dk, dv, workspace or None,
+                                              workspace_bytes, stream or None), "tide_attention_grad")
+
+
+def tide_layer_norm(norm: NormDesc, x: int, x_stride: int, y: int, y_stride: int, stream: int = 0) -> None:
+    _check(load_library().tide_layer_norm(norm, x or None, x_stride, y or None, y_stride, stream or None),
+           "tide_layer_norm")
+
+
+def tide_layer_norm_grad_workspace(norm: NormDesc) -> int:
+    return _size(load_library().tide_layer_norm_grad_workspace(norm), "tide_layer_norm_grad_workspace")
+
+
+def tide_layer_norm_grad(norm: NormDesc, dy: int, dy_stride: int, x: int, x_stride: int, dx: int, dx_stride: int,
+                         dweight: int, dbias: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load_library().tide_layer_norm_grad(norm, dy or None, dy_stride, x or None, x_stride, dx or None, dx_stride,
+                                               dweight or None, dbias or None, workspace or None, workspace_bytes,
+                                               stream or None), "tide_layer_norm_grad")
 
 
 def tide_ops_device_status(stream: int = 0) -> int:

@@ -3,8 +3,10 @@
 Each pairs an operator of :mod:`all_gather_gb300.ops` with its gradient; the
 forward pass keeps what the gradient reads and nothing else: the inputs of the
 head norm (its statistics are computed again), the hidden states, weight and
-log-sums of the cross entropy (the logits are computed again), and the 8-bit
-codes of a SwiGLU's gate and up (the inputs themselves are not kept).
+log-sums of the cross entropy (the logits are computed again), the 8-bit codes
+of a SwiGLU's gate and up (the inputs themselves are not kept), the heads,
+output and log-sums of the attention (the scores are computed again), and the
+rows and parameters of the layer norm (its statistics are computed again).
 
 They can be differentiated once: a gradient taken with ``create_graph`` raises
 an error when it is differentiated itself.
@@ -92,6 +94,48 @@ class _SwigluCkpt8(torch.autograd.Function):
         return _once((dgate, dup), dh, link)
 
 
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, offsets, causal, scale):
+        o, lse = ops.attention(q, k, v, offsets, causal, scale)
+        ctx.save_for_backward(q, k, v, offsets, o, lse)
+        ctx.how = causal, scale
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    def backward(ctx, do, dlse):
+        if dlse is not None:
+            raise RuntimeError("all_gather_gb300.autograd: lse has no gradient, the attention's output has")
+        if do is None:
+            return None, None, None, None, None, None
+        q, k, v, offsets, o, lse = ctx.saved_tensors
+        grads = ops.attention_grad(_head_rows(do), q, k, v, o, lse, offsets, *ctx.how)
+        return _once((*grads, None, None, None), do, q, k, v)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, center):
+        ctx.save_for_backward(x, weight, bias)
+        ctx.how = eps, center
+        return ops.layer_norm(x, weight, bias, eps, center)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias = ctx.saved_tensors
+        grads = ops.layer_norm_grad(_rows(dy), x, weight, bias, *ctx.how)
+        return _once((*grads, None, None), dy, x, weight, bias)
+
+
+def _head_rows(t):
+    """An incoming gradient of heads with rows on 16-byte boundaries."""
+    st = t.stride()
+    if st[2] == 1 and st[0] > 0 and st[1] > 0 and not (st[0] % 8 or st[1] % 8 or t.data_ptr() % 16):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _rows(t):
     """An incoming gradient with contiguous rows (autograd hands out expanded ones)."""
     return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
@@ -124,3 +168,18 @@ def swiglu(gate, up):
     """silu(gate) * up, differentiable, keeping gate and up in 8 bits for the backward pass (so its gradients are those
     at the 8-bit values)."""
     return _SwigluCkpt8.apply(gate, up)[0]
+
+
+def attention(q, k, v, offsets=None, causal: bool = True, scale=None):
+    """The output of :func:`ops.attention`, differentiable in q, k and v."""
+    return attention_and_lse(q, k, v, offsets, causal, scale)[0]
+
+
+def attention_and_lse(q, k, v, offsets=None, causal: bool = True, scale=None):
+    """(o, lse) of :func:`ops.attention`, o differentiable in q, k and v; a gradient of lse is refused."""
+    return _Attention.apply(q, k, v, offsets, causal, scale)
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True):
+    """:func:`ops.layer_norm`, differentiable in x, weight and bias."""
+    return _LayerNorm.apply(x, weight, bias, eps, center)

@@ -146,6 +146,7 @@ def rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, scalin
 
 
 _packed_qk, _packed_heads, _packed_ckpt8 = _b.PackedCalls.qk, _b.PackedCalls.heads, _b.PackedCalls.ckpt8
+_packed_attention, _packed_norm = _b.PackedCalls.attention, _b.PackedCalls.norm
 
 
 def _heads(t, name):
@@ -433,6 +434,180 @@ def swiglu_ckpt8_grad(ckpt: Ckpt8, dh, out=None, need_h: bool = True, stream=Non
     if out is not None:
         _written(dgate, dup, h)
     return dgate, dup, h
+
+
+# ------------------------------------------------------------------ attention over packed sequences
+
+def _attention_desc(q, k, v, offsets, causal, scale):
+    """(descriptor, device, q's shape)."""
+    dtype, dev, qs, ks = q.dtype, q.get_device(), q.shape, k.shape
+    if dtype is not _BF16:
+        raise TypeError(f"q is {dtype}: need bfloat16")
+    if len(qs) != 3 or len(ks) != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    T, Hq, D = qs
+    if (k.dtype is not dtype or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev or ks[0] != T
+            or ks[2] != D or v.shape != ks):
+        raise ValueError("q, k and v must agree in type, device, tokens and head_dim, k and v in heads")
+    _device(q, "q")
+    n = op = 0
+    nbytes = 8
+    if offsets is not None:
+        nbytes = _INT_BYTES.get(offsets.dtype)
+        if (nbytes is None or offsets.get_device() != dev or offsets.dim() != 1 or not offsets.is_contiguous()
+                or not offsets.shape[0]):
+            raise ValueError("offsets must be a contiguous int32 or int64 tensor [sequences + 1] on q's device")
+        n, op = offsets.shape[0] - 1, offsets.data_ptr()
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    return _packed_attention(T, Hq, ks[1], D, 1 if causal else 0, scale, nbytes, n, op, 0), dev, qs
+
+
+def _lse(t, dev, qs):
+    if t.dtype is not _F32 or t.get_device() != dev or t.shape != (qs[1], qs[0]) or not t.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor [{qs[1]}, {qs[0]}] on q's device")
+
+
+def attention(q, k, v, offsets=None, causal: bool = True, scale: Optional[float] = None, out=None, stream=None):
+    """(o, lse): softmax attention of q [T, Hq, D] over k and v [T, Hk, D] (bf16; query head h reads key head
+    h * Hk // Hq), and the log of every row's sum of exponentials, fp32 [Hq, T], which :func:`attention_grad` takes.
+    ``offsets`` (int32 or int64 [n + 1], on the device): sequence i is the tokens offsets[i] to offsets[i + 1] - 1, and
+    sees itself only; without them all tokens are one sequence.  ``causal``: a token sees no later one.  ``scale`` of
+    the scores: default 1 / sqrt(D).  A token of no sequence gets 0 (lse: -inf).  lse itself has no gradient."""
+    if stream is not None:
+        with _current(stream):
+            return attention(q, k, v, offsets, causal, scale, out)
+    if _recorded(out, q, k, v):
+        from . import autograd
+        return autograd.attention_and_lse(q, k, v, offsets, causal, scale)
+    desc, dev, qs = _attention_desc(q, k, v, offsets, causal, scale)
+    if out is None:
+        o, lse = _new(q), _empty((qs[1], qs[0]), dtype=_F32, device=q.device)
+    else:
+        o, lse = out
+        _like(o, _BF16, dev, qs, "o")
+        _lse(lse, dev, qs)
+    status = _b.packed_calls().attention_forward(desc, _heads(q, "q"), _heads(k, "k"), _heads(v, "v"), _heads(o, "o"),
+                                                 lse.data_ptr(), _stream())
+    if status:
+        _b._check(status, "tide_attention")
+    if out is not None:
+        _written(o, lse)
+    return o, lse
+
+
+def attention_grad(do, q, k, v, o, lse, offsets=None, causal: bool = True, scale: Optional[float] = None, out=None,
+                   workspace=None, stream=None):
+    """(dq, dk, dv) of :func:`attention` from the gradient ``do`` of its o, its inputs, and its outputs o and lse."""
+    if stream is not None:
+        with _current(stream):
+            return attention_grad(do, q, k, v, o, lse, offsets, causal, scale, out, workspace)
+    desc, dev, qs = _attention_desc(q, k, v, offsets, causal, scale)
+    _like(do, _BF16, dev, qs, "do")
+    _like(o, _BF16, dev, qs, "o")
+    _lse(lse, dev, qs)
+    if out is None:
+        dq, dk, dv = _new(q), _new(k), _new(v)
+    else:
+        dq, dk, dv = out
+        _like(dq, _BF16, dev, qs, "dq")
+        _like(dk, _BF16, dev, k.shape, "dk")
+        _like(dv, _BF16, dev, k.shape, "dv")
+    lib = _b.packed_calls()
+    need = _b._size(lib.attention_grad_workspace(desc), "tide_attention_grad_workspace")
+    _keep, ws, n = _scratch(need, workspace, q)
+    status = lib.attention_grad(desc, _heads(do, "do"), _heads(q, "q"), _heads(k, "k"), _heads(v, "v"), _heads(o, "o"),
+                                lse.data_ptr(), _heads(dq, "dq"), _heads(dk, "dk"), _heads(dv, "dv"), ws, n, _stream())
+    if status:
+        _b._check(status, "tide_attention_grad")
+    if out is not None:
+        _written(dq, dk, dv)
+    return dq, dk, dv
+
+
+# ------------------------------------------------------------------ layer norm
+
+def _norm_desc(x, weight, bias, eps, center):
+    """(descriptor, device, x's shape)."""
+    dtype, shape = x.dtype, x.shape
+    dt = _dtype(dtype, "x")
+    dev = _device(x, "x")
+    if len(shape) != 2:
+        raise ValueError("x must be [rows, cols]")
+    wp = bp = 0
+    if weight is not None:
+        _like(weight, dtype, dev, shape[1:], "weight")
+        wp = _vector(weight, "weight")
+    if bias is not None:
+        _like(bias, dtype, dev, shape[1:], "bias")
+        bp = _vector(bias, "bias")
+    return _packed_norm(shape[0], shape[1], dt, 1 if center else 0, wp, bp, eps), dev, shape
+
+
+def _vector(t, name) -> int:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, out=None, stream=None):
+    """Every row of x [rows, cols] (bf16 or fp32) less its mean, over the root of its variance plus ``eps``, times
+    ``weight`` plus ``bias`` [cols] (where given).  ``center=False``: the mean is not taken off, which is the
+    root-mean-square norm.  ``out`` may be x itself."""
+    if stream is not None:
+        with _current(stream):
+            return layer_norm(x, weight, bias, eps, center, out)
+    if _recorded(out, x, weight, bias):
+        from . import autograd
+        return autograd.layer_norm(x, weight, bias, eps, center)
+    desc, dev, shape = _norm_desc(x, weight, bias, eps, center)
+    if out is None:
+        y = _new(x)
+    else:
+        y = out
+        _like(y, x.dtype, dev, shape, "out")
+    status = _b.packed_calls().layer_norm(desc, x.data_ptr(), _rows(x, "x"), y.data_ptr(), _rows(y, "out"), _stream())
+    if status:
+        _b._check(status, "tide_layer_norm")
+    if out is not None:
+        _written(y)
+    return y
+
+
+def layer_norm_grad(dy, x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, out=None, workspace=None,
+                    stream=None):
+    """(dx, dweight, dbias) of :func:`layer_norm` from its output's gradient and its inputs; a weight or bias that is
+    None has no gradient (None).  ``out = (dx, dweight, dbias)``, of which dx may be dy or x."""
+    if stream is not None:
+        with _current(stream):
+            return layer_norm_grad(dy, x, weight, bias, eps, center, out, workspace)
+    desc, dev, shape = _norm_desc(x, weight, bias, eps, center)
+    dtype = x.dtype
+    _like(dy, dtype, dev, shape, "dy")
+    if out is None:
+        dx = _new(x)
+        dw = None if weight is None else _new(weight)
+        db = None if bias is None else _new(bias)
+    else:
+        dx, dw, db = out
+        _like(dx, dtype, dev, shape, "dx")
+        for w, d, name in ((weight, dw, "dweight"), (bias, db, "dbias")):
+            if (w is None) != (d is None):
+                raise ValueError(f"{name} goes with its parameter: both or neither")
+            if w is not None:
+                _like(d, dtype, dev, shape[1:], name)
+    lib, ws, n = _b.packed_calls(), 0, 0
+    if weight is not None or bias is not None:
+        need = _b._size(lib.layer_norm_grad_workspace(desc), "tide_layer_norm_grad_workspace")
+        _keep, ws, n = _scratch(need, workspace, x)
+    status = lib.layer_norm_grad(desc, dy.data_ptr(), _rows(dy, "dy"), x.data_ptr(), _rows(x, "x"), dx.data_ptr(),
+                                 _rows(dx, "dx"), 0 if dw is None else _vector(dw, "dweight"),
+                                 0 if db is None else _vector(db, "dbias"), ws, n, _stream())
+    if status:
+        _b._check(status, "tide_layer_norm_grad")
+    if out is not None:
+        _written(dx, dw, db)
+    return dx, dw, db
 
 
 def device_status(stream=None) -> int:

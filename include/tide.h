@@ -542,6 +542,86 @@ TIDE_API tide_status_t tide_swiglu_ckpt8_grad(int64_t rows, int64_t cols, int32_
                                               void *dup, int64_t dup_stride, void *h, int64_t h_stride,
                                               void *stream);
 
+/* Attention of whole prompts: what it needs besides the heads. */
+typedef struct {
+    int64_t tokens;          /* T in [0, 2^31 - 512], T * q_heads at most 2^34 */
+    int32_t q_heads;         /* Hq in [1, 65535], a multiple of k_heads */
+    int32_t k_heads;         /* Hk >= 1: query head h reads key head h / (Hq / Hk) */
+    int32_t head_dim;        /* D, a multiple of 8 in [8, 128] */
+    int32_t causal;          /* 0: a token sees its whole sequence; else: itself and what is before it */
+    float scale;             /* > 0, of the scores */
+    int32_t offset_bytes;    /* 4 or 8 */
+    int64_t sequences;       /* n in [0, 2^31 - 2] */
+    const void *offsets;     /* device integers [n + 1], not decreasing: sequence i is tokens offsets[i] to
+                                offsets[i + 1] - 1; empty ones are allowed.  NULL: one sequence of all tokens */
+    uint32_t debug;          /* 0, or TIDE_DEBUG_SHORT_WAIT and TIDE_DEBUG_SKIP_FILL, as for tide_ce_t */
+} tide_attention_t;
+
+/*
+ * Softmax attention over packed sequences, for each query head:
+ *   s_rc = scale q_r . k_c for the keys c that token r sees,
+ *   lse_r = log sum_c exp(s_rc);  o_r = sum_c exp(s_rc - lse_r) v_c.
+ * q, o: device [T, Hq, D]; k, v: [T, Hk, D]; lse: device fp32 [Hq, T].  bf16
+ * only; rows on 16-byte boundaries; strides of dimensions longer than 1 are
+ * positive multiples of 8.  exp(s - a), a the largest score or one less than
+ * 8 log2 below it, is rounded to bf16 for its product with v; sums are fp32.
+ * A token of no sequence (before offsets[0], behind the last one, or past T)
+ * sees nothing: o = 0, lse = -inf.  What a token does not see does not reach
+ * its row, whether finite or not.  Offsets are not checked on the host;
+ * decreasing ones, or ones outside [0, T], give rows that mean nothing, but
+ * nothing outside the tensors is read or written.
+ */
+TIDE_API tide_status_t tide_attention(const tide_attention_t *at, const tide_heads_t *q, const tide_heads_t *k,
+                                      const tide_heads_t *v, const tide_heads_t *o, float *lse, void *stream);
+
+/*
+ * Gradient of tide_attention from its outputs' (do of o), its inputs and its
+ * outputs o and lse:
+ *   p = exp(s - lse);  ds_rc = p_rc (do_r . v_c - do_r . o_r);
+ *   dv_c = sum_r p_rc do_r;  dq_r = scale sum_c ds_rc k_c;  dk_c = scale sum_r ds_rc q_r,
+ * the sums of dk and dv over the query heads of a key head too.  The scores
+ * are computed again; p and ds are rounded to bf16 for their products.  lse
+ * itself has no gradient here.  A token of no sequence has gradients of 0.
+ * Sums are taken in a fixed order.
+ */
+TIDE_API tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t *dout,
+                                           const tide_heads_t *q, const tide_heads_t *k, const tide_heads_t *v,
+                                           const tide_heads_t *o, const float *lse, const tide_heads_t *dq,
+                                           const tide_heads_t *dk, const tide_heads_t *dv, void *workspace,
+                                           int64_t workspace_bytes, void *stream);
+TIDE_API int64_t tide_attention_grad_workspace(const tide_attention_t *at);
+
+/* What a layer norm needs besides its rows. */
+typedef struct {
+    int64_t rows;            /* >= 0 */
+    int64_t cols;            /* in [1, 2^24] */
+    int32_t dtype;           /* of rows, weight, bias and their gradients */
+    int32_t center;          /* 0: the mean is not taken off (root-mean-square norm) */
+    const void *weight;      /* device [cols], or NULL */
+    const void *bias;        /* device [cols], or NULL */
+    float eps;               /* >= 0, added to the mean square */
+} tide_norm_t;
+
+/*
+ * y = (x - m) / sqrt(mean((x - m)^2) + eps) * weight + bias for each row, m its
+ * mean (0 without the centre).  x, y: device [rows, cols] with row strides;
+ * y may be x (same pointer and stride).
+ */
+TIDE_API tide_status_t tide_layer_norm(const tide_norm_t *norm, const void *x, int64_t x_stride, void *y,
+                                       int64_t y_stride, void *stream);
+
+/*
+ * Gradient of tide_layer_norm from dy and x: dx (may be dy or x, same pointer
+ * and stride), and dweight and dbias (device [cols] of `dtype`, overwritten;
+ * NULL where the weight or bias is, which is not read itself if it is the
+ * bias).  Sums over rows are taken in a fixed order.
+ */
+TIDE_API tide_status_t tide_layer_norm_grad(const tide_norm_t *norm, const void *dy, int64_t dy_stride,
+                                            const void *x, int64_t x_stride, void *dx, int64_t dx_stride,
+                                            void *dweight, void *dbias, void *workspace, int64_t workspace_bytes,
+                                            void *stream);
+TIDE_API int64_t tide_layer_norm_grad_workspace(const tide_norm_t *norm);
+
 /*
  * Read and clear the operators' status word of the current device
  * (synchronises `stream`): TIDE_ERR_TIMEOUT if a bounded device-side wait of
