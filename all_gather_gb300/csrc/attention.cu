@@ -1,131 +1,72 @@
-// Softmax attention of whole prompts over packed sequences, and its gradient.
+// Softmax attention of whole prompts over packed sequences.
 //
 //   s_rc = scale q_r k_c  for the keys c that row r sees,
 //   lse_r = log sum_c exp(s_rc),  o_r = sum_c exp(s_rc - lse_r) v_c
-//   p = exp(s - lse),  delta_r = do_r o_r,  dp_rc = do_r v_c,  ds = p (dp - delta),
-//   dq_r = scale sum_c ds_rc k_c,  dk_c = scale sum_r ds_rc q_r,  dv_c = sum_r p_rc do_r
-#include <cuda_runtime.h>
-
-#include <algorithm>
-
-#include "ops_internal.h"
+//
+// Tiles are 128 tokens of the whole batch, wherever sequences begin and end: a
+// row sees an interval of keys, [begin of its sequence, itself] or the whole
+// sequence, so a mask is two comparisons, full tiles need none, and short
+// sequences share a tile.
+//
+// A block takes 256 rows of a query head, two tiles, and goes over the key
+// tiles that their rows see, one pass with the running maximum and sum.  A warp
+// fetches q, k and v (TMA, a ring of key and value tiles); a warp issues the
+// tensor-core products; and for each of the two row tiles four warps, a row a
+// thread, make the scores S = q k^T (fp32 in tensor memory) into the
+// probabilities P, bf16, written over S and taken from there as an operand of
+// O += P v.  While one tile's P is made, the tensor cores work for the other.
+// The maximum that P is relative to moves only when it has grown by more than
+// 2^8, which keeps O, in tensor memory too, from being multiplied at every tile;
+// P and its sum then hold values up to 2^8, which neither type minds.
+//
+// What a row does not see does not reach it: its P is 0 there.  A v that is
+// not finite would still leave 0 * v = NaN; rows whose result is not finite
+// are computed once more, by themselves, over what they see.
+//
+// Blocks ask the hardware for the next block of the grid that has not started
+// and do its work too, so what follows of a row tile's end (O out of tensor
+// memory, to memory) runs beside the next one's beginning.  The grid goes from
+// the last rows to the first, which are the shortest of a causal sequence.
+#include "attention.h"
 
 namespace {
 
+using namespace tide::attn;
 using tide::op_aligned;
 using tide::op_fail;
-using bf16 = __nv_bfloat16;
+namespace um = tide::umma;
 
-constexpr int kMaxHeadDim = 128;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 320;          // two groups of four warps for the rows, a warp that fetches, one that multiplies
+constexpr int kRingBytes = 160 * 1024;
+constexpr int kClaims = 8;             // of a block's last items, kept for a wait that runs out
+constexpr float kLazy = 8.f;           // log2 of how far P may grow before its maximum moves
 
-// A tensor of heads: rows of D contiguous elements on 16-byte boundaries.
-struct Heads {
-    bf16 *p;
-    int64_t ts, hs;
-    __host__ __device__ bf16 *row(int64_t t, int64_t h) const { return p + t * ts + h * hs; }
+// Set when a bounded wait runs out.
+__device__ int g_timed_out;
+
+struct Forward {
+    CUtensorMap q, k, v;
+    Problem pr;
+    Heads hq, hk, hv, o;
+    float *lse;
+    int items;  // pairs of row tiles times query heads
+    uint64_t wait_ns;
+    int skip_fill;  // TIDE_DEBUG_SKIP_FILL
 };
 
-// [a, b): what a row sees, or which rows see a key; empty: a >= b.
-struct Span {
-    int a, b;
+struct Item {
+    int number;  // -1: no more
+    Tiles keys[2];
 };
-
-struct Problem {
-    const void *offsets;  // NULL: one sequence
-    int offset_bytes, n;  // n sequences
-    int T, Hq, Hk, D, causal;
-    float scale;
-
-    __device__ int64_t offset(int i) const
-    {
-        return offset_bytes == 8 ? static_cast<const int64_t *>(offsets)[i]
-                                 : int64_t(static_cast<const int32_t *>(offsets)[i]);
-    }
-    // The sequence of token t, cut to [0, T); empty if it belongs to none.  Whatever the offsets hold, nothing
-    // outside them is read and what comes out lies in [0, T).
-    __device__ Span sequence(int t) const
-    {
-        if (t < 0 || t >= T)
-            return {0, 0};
-        if (!offsets)
-            return {0, T};
-        int lo = -1, hi = n;  // offset(lo) <= t < offset(hi)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (offset(mid) <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        if (lo < 0)
-            return {0, 0};
-        const int64_t a = max(int64_t(0), offset(lo)), b = min(int64_t(T), offset(lo + 1));
-        return a <= t && t < b ? Span{int(a), int(b)} : Span{0, 0};
-    }
-    __device__ Span keys_of(int r) const
-    {
-        const Span s = sequence(r);
-        return {s.a, causal ? min(s.b, r + 1) : s.b};
-    }
-    __device__ Span rows_of(int c) const
-    {
-        const Span s = sequence(c);
-        return {causal ? max(s.a, c) : s.a, s.b};
-    }
-};
-
-__device__ __forceinline__ float exp2_fast(float x)
+__device__ __forceinline__ void place_of(const Forward &f, int item, int &head, int &r0)
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    head = item % f.pr.Hq;
+    r0 = (f.items / f.pr.Hq - 1 - item / f.pr.Hq) * 2 * kTile;
 }
 
-// ---------------------------------------------------------------- rows by themselves
-//
-// One row (or key) a lane, by the formulas, over what it sees and nothing else.
-
-__device__ float dot_row(const bf16 *a, const bf16 *b, int D)
-{
-    float s = 0.f;
-    for (int d = 0; d < D; d += 8) {
-        float x[8], y[8];
-        tide::load8(a + d, x);
-        tide::load8(b + d, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = fmaf(x[i], y[i], s);
-    }
-    return s;
-}
-
-// The union of a warp's spans.
-__device__ Span warp_span(Span s)
-{
-    const bool some = s.a < s.b;
-    return {__reduce_min_sync(kAll, some ? s.a : 0x7fffffff), __reduce_max_sync(kAll, some ? s.b : 0)};
-}
-
-// log2 of the sum of 2^(c s) over the span, -inf if it is empty.
-__device__ float row_lse2(const bf16 *q, const Heads &k, int hk, Span see, int D, float c)
-{
-    const Span all = warp_span(see);
-    float top = -INFINITY, sum = 0.f;
-    for (int j = all.a; j < all.b; ++j) {
-        if (j < see.a || j >= see.b)
-            continue;
-        const float s = dot_row(q, k.row(j, hk), D) * c;
-        const float m = fmaxf(top, s), at = isinf(m) ? 0.f : m;
-        sum = sum * exp2_fast(top - at) + exp2_fast(s - at);
-        top = m;
-    }
-    return see.a < see.b ? (isinf(top) ? 0.f : top) + log2f(sum) : -INFINITY;
-}
-
-__device__ void row_forward(const bf16 *q, const Heads &k, const Heads &v, int hk, Span see, int D, float c, float lse2,
-                            bf16 *o)
+// Rows of a warp whose result was not finite, over what they see only.
+__device__ __noinline__ void row_forward(const bf16 *q, const Heads &k, const Heads &v, int hk, Span see, int D, float c,
+                                         float lse2, bf16 *o)
 {
     const Span all = warp_span(see);
     for (int d0 = 0; d0 < D; d0 += 8) {
@@ -133,213 +74,480 @@ __device__ void row_forward(const bf16 *q, const Heads &k, const Heads &v, int h
         for (int j = all.a; j < all.b; ++j) {
             if (j < see.a || j >= see.b)
                 continue;
-            const float p = exp2_fast(dot_row(q, k.row(j, hk), D) * c - lse2);
+            const float p = exp2_fast(fmaf(dot_row(q, k.row(j, hk), D), c, -lse2));
             float x[8];
             tide::load8(v.row(j, hk) + d0, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 acc[i] = fmaf(p, x[i], acc[i]);
         }
-        if (o)
+        if (see.a < see.b)
             tide::store8(o + d0, acc);
     }
 }
 
-__global__ void __launch_bounds__(128) forward_simple(Problem pr, Heads q, Heads k, Heads v, Heads o, float *lse)
+template <int W>  // columns of a head in shared and tensor memory: 64 or 128
+__global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_constant__ Forward f)
 {
-    const int r = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y, hk = h / (pr.Hq / pr.Hk);
-    const Span see = r < pr.T ? pr.keys_of(r) : Span{0, 0};
-    const bool mine = r < pr.T;
-    const bf16 *qr = q.row(mine ? r : 0, h);
-    const float c = pr.scale * kLog2e, lse2 = row_lse2(qr, k, hk, see, pr.D, c);
-    row_forward(qr, k, v, hk, see, pr.D, c, lse2, mine ? o.row(r, h) : nullptr);
-    if (mine)
-        lse[int64_t(h) * pr.T + r] = lse2 * kLn2;
-}
+    constexpr int kHalves = W / 64, kTileBytes = kHalves * kHalf, kStages = kRingBytes / kTileBytes;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t q_at = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024, ring = q_at + 2 * kTileBytes;
+    __shared__ uint64_t bars[2 * kStages + 19];
+    __shared__ alignas(16) uint4 answer;
+    __shared__ Item items[2];
+    __shared__ int claims[kClaims], claimed, done[8];  // done: items of each of the rows' warps
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int gave_up;
+    const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages, rest = empty + 8 * kStages;
+    const uint32_t q_full = rest, q_empty = rest + 16, s_full = rest + 32, p_ready = rest + 48, pv_done = rest + 64,
+                   o_free = rest + 80, item_full = rest + 96, item_empty = rest + 112, asked = rest + 128,
+                   drained = rest + 136, never = rest + 144;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Problem &pr = f.pr;
+    const int group = pr.Hq / pr.Hk;
 
-// delta [Hq][T] = sum over d of do * o.
-__global__ void __launch_bounds__(256) delta_kernel(Problem pr, Heads dout, Heads o, float *delta)
-{
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 16;  // 16 lanes a row
-    const int at = threadIdx.x % 16 * 8;
-    const int64_t t = i / pr.Hq;
-    const int h = int(i % pr.Hq);
-    float s = 0.f;
-    if (t < pr.T && at < pr.D) {
-        float x[8], y[8];
-        tide::load8(dout.row(t, h) + at, x);
-        tide::load8(o.row(t, h) + at, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            s = fmaf(x[j], y[j], s);
-    }
-#pragma unroll
-    for (int w = 8; w > 0; w /= 2)
-        s += __shfl_xor_sync(kAll, s, w);
-    if (t < pr.T && at == 0)
-        delta[int64_t(h) * pr.T + t] = s;
-}
-
-__device__ void row_dq(const bf16 *q, const bf16 *dout, const Heads &k, const Heads &v, int hk, Span see, int D, float c,
-                       float scale, float lse2, float delta, bf16 *dq)
-{
-    const Span all = warp_span(see);
-    for (int d0 = 0; d0 < D; d0 += 8) {
-        float acc[8] = {};
-        for (int j = all.a; j < all.b; ++j) {
-            if (j < see.a || j >= see.b)
-                continue;
-            const float p = exp2_fast(dot_row(q, k.row(j, hk), D) * c - lse2);
-            const float ds = p * (dot_row(dout, v.row(j, hk), D) - delta);
-            float x[8];
-            tide::load8(k.row(j, hk) + d0, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[i] = fmaf(ds, x[i], acc[i]);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            um::mbar_init(full + 8 * i, 1);
+            um::mbar_init(empty + 8 * i, 1);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            acc[i] *= scale;
-        if (dq)
-            tide::store8(dq + d0, acc);
+        for (int i = 0; i < 2; ++i) {
+            um::mbar_init(q_full + 8 * i, 1);
+            um::mbar_init(q_empty + 8 * i, 1);
+            um::mbar_init(s_full + 8 * i, 1);
+            um::mbar_init(p_ready + 8 * i, 4);
+            um::mbar_init(pv_done + 8 * i, 1);
+            um::mbar_init(o_free + 8 * i, 4);
+            um::mbar_init(item_full + 8 * i, 1);
+            um::mbar_init(item_empty + 8 * i, 9);
+        }
+        um::mbar_init(asked, 1);
+        um::mbar_init(drained, 1);
+        um::mbar_init(never, 1);
+        um::fence_barrier_init();
+        gave_up = 0, claimed = 0, answer = make_uint4(0, 0, 0, 0);
+        um::fence_copies();
+        um::prefetch_map(&f.q);
+        um::prefetch_map(&f.k);
+        um::prefetch_map(&f.v);
     }
-}
+    if (threadIdx.x < 8)
+        done[threadIdx.x] = 0;
+    if (warp == 9)
+        um::tmem_alloc_own(um::smem_addr(&tmem_slot), 512);
+    um::fence_before();
+    __syncthreads();
+    um::fence_after();
+    const uint32_t tmem = tmem_slot;  // S of both tiles, 128 columns each, then their O
+    auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait(bar, parity, &gave_up, f.wait_ns); };
 
-__device__ void row_dkv(const Problem &pr, const bf16 *k, const bf16 *v, const Heads &q, const Heads &dout, int hk, Span see,
-                        float c, const float *lse, const float *delta, bf16 *dk, bf16 *dv)
-{
-    const Span all = warp_span(see);
-    const int group = pr.Hq / pr.Hk, D = pr.D;
-    for (int d0 = 0; d0 < D; d0 += 8) {
-        float ak[8] = {}, av[8] = {};
-        for (int h = hk * group; h < (hk + 1) * group; ++h)
-            for (int r = all.a; r < all.b; ++r) {
-                if (r < see.a || r >= see.b)
-                    continue;
-                const int64_t i = int64_t(h) * pr.T + r;
-                const float p = exp2_fast(dot_row(q.row(r, h), k, D) * c - lse[i] * kLog2e);
-                const float ds = p * (dot_row(dout.row(r, h), v, D) - delta[i]);
-                float x[8], y[8];
-                tide::load8(q.row(r, h) + d0, x);
-                tide::load8(dout.row(r, h) + d0, y);
+    if (warp == 8) {
+        const bool leader = um::elected();
+        int number = blockIdx.x, slot = 0, turn = 0, stage = 0, phase = 0, taken = 0;
+        int fills = 0, q_fills[2] = {0, 0};  // copies under way at most: the last of each place
+        uint32_t q_phase[2] = {0, 0};
+        bool ok = true;
+        while (ok) {
+            if (lane == 0) {
+                claims[taken % kClaims] = number;
+                claimed = taken + 1;
+            }
+            ++taken;
+            if (leader)
+                um::ask_next_block(um::smem_addr(&answer), asked);
+            // which key tiles the rows see: four rows a lane
+            int head, r0;
+            place_of(f, number, head, r0);
+            Tiles keys[2];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    ak[j] = fmaf(ds, x[j], ak[j]);
-                    av[j] = fmaf(p, y[j], av[j]);
+            for (int t = 0; t < 2; ++t) {
+                Span see = {0x7fffffff, 0};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Span s = pr.keys_of(r0 + t * kTile + i * 32 + lane);
+                    if (s.a < s.b)
+                        see = {min(see.a, s.a), max(see.b, s.b)};
+                }
+                keys[t] = tiles_of(warp_span(see));
+            }
+            if (!(ok = wait(item_empty + 8 * slot, turn ^ 1)))
+                break;
+            if (lane == 0) {
+                items[slot] = {number, {keys[0], keys[1]}};
+                um::mbar_arrive(item_full + 8 * slot);
+            }
+            if (++slot == 2)
+                slot = 0, turn ^= 1;
+            const bool both = keys[0].a < keys[0].b && keys[1].a < keys[1].b;
+            const Tiles all = both ? Tiles{min(keys[0].a, keys[1].a), max(keys[0].b, keys[1].b)}
+                                   : keys[0].a < keys[0].b ? keys[0] : keys[1];
+            bool skip = f.skip_fill && number == 0;  // this item's first key tile never comes
+            for (int j = all.a; ok && j < all.b; ++j) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j != all.a || keys[t].a >= keys[t].b)
+                        continue;
+                    if (!(ok = wait(q_empty + 8 * t, q_phase[t] ^ 1)))
+                        break;
+                    q_phase[t] ^= 1;
+                    if (leader) {
+                        um::mbar_expect(q_full + 8 * t, kTileBytes);
+                        load_tile(q_at + t * kTileBytes, &f.q, kHalves, head, r0 + t * kTile, q_full + 8 * t);
+                    }
+                    ++q_fills[t];
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!ok || !(ok = wait(empty + 8 * stage, phase ^ 1)))
+                        break;
+                    if (skip) {
+                        ok = wait(never, 0);  // nothing arrives there
+                        skip = false;
+                        break;
+                    }
+                    if (leader) {
+                        um::mbar_expect(full + 8 * stage, kTileBytes);
+                        load_tile(ring + stage * kTileBytes, kv ? &f.v : &f.k, kHalves, head / group, j * kTile,
+                                  full + 8 * stage);
+                    }
+                    ++fills;
+                    if (++stage == kStages)
+                        stage = 0, phase ^= 1;
                 }
             }
+            if (!ok || !(ok = wait(asked, (taken - 1) & 1)))
+                break;
+            number = um::next_block(um::smem_addr(&answer));
+            um::fence_copies();
+            __syncwarp();
+            if (number < 0)
+                break;
+        }
+        if (ok && (ok = wait(item_empty + 8 * slot, turn ^ 1))) {
+            if (lane == 0) {
+                items[slot].number = -1;
+                um::mbar_arrive(item_full + 8 * slot);
+            }
+        }
+        if (!ok) {
+            // The answer that is under way, and the copies: neither may find the block gone.
+            auto land = [&](uint32_t bar, uint32_t parity) {
+                const uint64_t t0 = um::now_ns();
+                while (!um::mbar_try(bar, parity) && um::now_ns() - t0 < f.wait_ns) {
+                }
+            };
+            land(asked, (taken - 1) & 1);
+            const int more = um::next_block(um::smem_addr(&answer));
+            if (lane == 0 && more >= 0 && more != number) {
+                claims[taken % kClaims] = more;
+                claimed = taken + 1;
+            }
+            for (int i = max(0, fills - kStages); i < fills; ++i)
+                land(full + 8 * (i % kStages), (i / kStages) & 1);
+            for (int t = 0; t < 2; ++t)
+                if (q_fills[t])
+                    land(q_full + 8 * t, (q_fills[t] - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        const bool leader = um::elected();
+        const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
+        const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
+        const uint32_t idesc_o = um::instr_desc(kTile, dn, false, true);
+        int slot = 0, turn = 0, stage = 0, phase = 0;
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+        bool ok = true;
+        // S of row tile t from the key tile in a stage
+        auto scores = [&](int t, int at) {
+            um::fence_after();
+            if (leader) {
+                const uint64_t a = um::operand_desc(q_at + t * kTileBytes, false, 0);
+                const uint64_t b = um::operand_desc(ring + at * kTileBytes, false, 0);
+                for (int i = 0; i < ksteps; ++i) {
+                    const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
+                    um::mma_own(tmem + t * kTile, a + off, b + off, idesc_s, i > 0);
+                }
+                um::mma_commit_own(s_full + 8 * t);
+            }
+        };
+        while (ok) {
+            if (!(ok = wait(item_full + 8 * slot, turn)))
+                break;
+            const Item it = items[slot];
+            __syncwarp();
+            if (lane == 0)
+                um::mbar_arrive(item_empty + 8 * slot);
+            if (++slot == 2)
+                slot = 0, turn ^= 1;
+            if (it.number < 0)
+                break;
+            const Tiles &k0 = it.keys[0], &k1 = it.keys[1];
+            const bool both = k0.a < k0.b && k1.a < k1.b;
+            const Tiles all = both ? Tiles{min(k0.a, k1.a), max(k0.b, k1.b)} : k0.a < k0.b ? k0 : k1;
+            for (int j = all.a - 1; ok && j < all.b; ++j) {  // P v of key tile j, scores of key tile j + 1
+                const int v_at = stage;
+                bool v_here = j < all.a;
+                int k_at = stage;
+                uint32_t k_phase = phase;
+                if (j >= all.a && ++k_at == kStages)
+                    k_at = 0, k_phase ^= 1;
+                bool k_here = j + 1 >= all.b;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ak[i] *= pr.scale;
-        if (dk) {
-            tide::store8(dk + d0, ak);
-            tide::store8(dv + d0, av);
+                for (int t = 0; t < 2; ++t) {
+                    const Tiles &mine = t ? k1 : k0;
+                    if (j >= mine.a && j < mine.b) {
+                        if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
+                            break;
+                        v_here = true;
+                        if (j == mine.a) {
+                            if (!(ok = wait(o_free + 8 * t, o_phase[t] ^ 1)))
+                                break;
+                            o_phase[t] ^= 1;
+                        }
+                        if (!(ok = wait(p_ready + 8 * t, p_phase[t])))
+                            break;
+                        p_phase[t] ^= 1;
+                        um::fence_after();
+                        if (leader) {
+                            const uint64_t b = um::operand_desc(ring + v_at * kTileBytes, true, kHalf);
+#pragma unroll
+                            for (int i = 0; i < kTile / 16; ++i)
+                                um::mma_own_tmem(tmem + 2 * kTile + t * kTile, tmem + t * kTile + i * 8, b + i * (2048 >> 4),
+                                                 idesc_o, j > mine.a || i > 0);
+                            um::mma_commit_own(pv_done + 8 * t);
+                        }
+                    }
+                    if (j + 1 >= mine.a && j + 1 < mine.b) {
+                        if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
+                            break;
+                        k_here = true;
+                        if (j + 1 == mine.a) {
+                            if (!(ok = wait(q_full + 8 * t, q_phase[t])))
+                                break;
+                            q_phase[t] ^= 1;
+                        }
+                        scores(t, k_at);
+                        if (j + 2 == mine.b && leader)
+                            um::mma_commit_own(q_empty + 8 * t);
+                    }
+                }
+                if (!ok)
+                    break;
+                // a tile that neither row tile needed has to have come all the same, before its place is given back
+                if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
+                    break;
+                if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
+                    break;
+                if (leader) {
+                    if (j >= all.a)
+                        um::mma_commit_own(empty + 8 * v_at);
+                    if (j + 1 < all.b)
+                        um::mma_commit_own(empty + 8 * k_at);
+                }
+                // stages: k of all.a, then v of j and k of j + 1 in the order of their loads
+                const int used = (j >= all.a) + (j + 1 < all.b);
+                for (int i = 0; i < used; ++i)
+                    if (++stage == kStages)
+                        stage = 0, phase ^= 1;
+            }
+        }
+        __syncwarp();
+        if (leader) {  // nothing may be under way when the accumulators go
+            um::mma_commit_own(drained);
+            const uint64_t t0 = um::now_ns();
+            while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < f.wait_ns) {
+            }
+        }
+        __syncwarp();
+    } else {
+        const int t = warp / 4, quarter = warp % 4;
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t s_at = tmem + lanes + t * kTile, o_at = s_at + 2 * kTile;
+        const float c = pr.scale * kLog2e;
+        int slot = 0, turn = 0;
+        uint32_t s_phase = 0, pv_phase = 0;
+        bool ok = true;
+        for (;;) {
+            if (!wait(item_full + 8 * slot, turn))
+                break;
+            const int number = items[slot].number;
+            const Tiles keys = items[slot].keys[t];
+            __syncwarp();
+            if (lane == 0)
+                um::mbar_arrive(item_empty + 8 * slot);
+            if (++slot == 2)
+                slot = 0, turn ^= 1;
+            if (number < 0)
+                break;
+            int head, r0;
+            place_of(f, number, head, r0);
+            const int r = r0 + t * kTile + quarter * 32 + lane;
+            const Span see = pr.keys_of(r);
+            float top = -INFINITY, sum = 0.f;
+            for (int j = keys.a; j < keys.b; ++j) {
+                if (!(ok = wait(s_full + 8 * t, s_phase)))
+                    break;
+                s_phase ^= 1;
+                um::fence_after();
+                uint32_t v[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    um::tmem_load32(s_at + 32 * i, v[i]);
+                um::tmem_wait_load();
+                const int a = see.a - j * kTile, b = see.b - j * kTile;
+                if (__any_sync(kAll, a > 0 || b < kTile)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (32 * i + x < a || 32 * i + x >= b)
+                                v[i][x] = __float_as_uint(-INFINITY);
+                }
+                float m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    m[i] = fmaxf(__uint_as_float(v[i][0]), __uint_as_float(v[i][1]));
+#pragma unroll
+                    for (int x = 2; x < 32; x += 2)
+                        m[i] = um::max3(m[i], __uint_as_float(v[i][x]), __uint_as_float(v[i][x + 1]));
+                }
+                const float now = um::max3(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]), top);
+                if (j == keys.a) {
+                    top = now;
+                } else if (__any_sync(kAll, (now - top) * c > kLazy || (top == -INFINITY && now > top))) {
+                    // O so far goes over to the new maximum
+                    const float by = now == top ? 1.f : exp2_fast((top - now) * c);
+                    top = now;
+                    sum *= by;
+                    if (!(ok = wait(pv_done + 8 * t, pv_phase ^ 1)))
+                        break;
+                    um::fence_after();
+#pragma unroll
+                    for (int i = 0; i < W; i += 32) {
+                        uint32_t o[32];
+                        um::tmem_load32(o_at + i, o);
+                        um::tmem_wait_load();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+                        um::tmem_store32(o_at + i, o);
+                    }
+                }
+                // exp2(c s - c top); an infinite maximum stands for itself
+                const float at = isinf(top) ? 0.f : top * c;
+                const float2 cc = make_float2(c, c), aa = make_float2(-at, -at);
+                float2 part[2] = {};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const int i = 2 * h + x / 16, y = x % 16 * 2;
+                        float2 e = um::fma2(make_float2(__uint_as_float(v[i][y]), __uint_as_float(v[i][y + 1])), cc, aa);
+                        e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
+                        part[x % 2] = um::add2(part[x % 2], e);
+                        p[x] = tide::pack_bf16(e.x, e.y);
+                    }
+                    um::tmem_store32(s_at + 32 * h, p);
+                }
+                um::tmem_wait_store();
+                um::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    um::mbar_arrive(p_ready + 8 * t);
+                part[0] = um::add2(part[0], part[1]);
+                sum += part[0].x + part[0].y;
+                pv_phase ^= 1;
+            }
+            if (!ok)
+                break;
+            const bool some = see.a < see.b;
+            const float lse2 = some ? (isinf(top) ? 0.f : top * c) + log2f(sum) : -INFINITY;
+            bf16 *out = f.o.row(min(r, pr.T - 1), head);
+            bool odd = false;  // not finite
+            if (keys.a < keys.b) {
+                if (!(ok = wait(pv_done + 8 * t, pv_phase ^ 1)))
+                    break;
+                um::fence_after();
+                uint32_t o[W / 32][32];
+#pragma unroll
+                for (int i = 0; i < W / 32; ++i)
+                    um::tmem_load32(o_at + 32 * i, o[i]);
+                um::tmem_wait_load();
+                um::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    um::mbar_arrive(o_free + 8 * t);
+                const float by = some ? 1.f / sum : 0.f;
+#pragma unroll
+                for (int d = 0; d < W; d += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = __uint_as_float(o[d / 32][d % 32 + i]);
+                        odd = odd || !(fabsf(x[i]) < INFINITY);
+                        x[i] = some ? x[i] * by : 0.f;
+                    }
+                    if (d < pr.D && r < pr.T)
+                        tide::store8(out + d, x);
+                }
+            } else if (r < pr.T) {
+                const float x[8] = {};
+                for (int d = 0; d < pr.D; d += 8)
+                    tide::store8(out + d, x);
+            }
+            odd = odd && some && fabsf(lse2) < INFINITY;
+            if (__any_sync(kAll, odd))
+                row_forward(f.hq.row(odd ? r : 0, head), f.hk, f.hv, head / group, odd ? see : Span{0, 0}, pr.D, c, lse2,
+                            out);
+            if (r < pr.T)
+                f.lse[int64_t(head) * pr.T + r] = lse2 * kLn2;
+            if (lane == 0)
+                ++done[warp];
         }
     }
-}
-
-__global__ void __launch_bounds__(128) dq_simple(Problem pr, Heads q, Heads k, Heads v, Heads dout, const float *lse,
-                                                 const float *delta, Heads dq)
-{
-    const int r = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y, hk = h / (pr.Hq / pr.Hk);
-    const bool mine = r < pr.T;
-    const Span see = mine ? pr.keys_of(r) : Span{0, 0};
-    const int64_t t = mine ? r : 0, i = int64_t(h) * pr.T + t;
-    row_dq(q.row(t, h), dout.row(t, h), k, v, hk, see, pr.D, pr.scale * kLog2e, pr.scale, lse[i] * kLog2e, delta[i],
-           mine ? dq.row(r, h) : nullptr);
-}
-
-__global__ void __launch_bounds__(128) dkv_simple(Problem pr, Heads q, Heads k, Heads v, Heads dout, const float *lse,
-                                                  const float *delta, Heads dk, Heads dv)
-{
-    const int c = blockIdx.x * 128 + threadIdx.x, h = blockIdx.y;
-    const bool mine = c < pr.T;
-    const Span see = mine ? pr.rows_of(c) : Span{0, 0};
-    const int64_t t = mine ? c : 0;
-    row_dkv(pr, k.row(t, h), v.row(t, h), q, dout, h, see, pr.scale * kLog2e, lse, delta, mine ? dk.row(c, h) : nullptr,
-            mine ? dv.row(c, h) : nullptr);
-}
-
-// ---------------------------------------------------------------- host
-
-tide_status_t check_desc(const tide_attention_t *at)
-{
-    if (!at)
-        return op_fail(TIDE_ERR_INVALID_ARG, "at is NULL");
-    if (at->tokens < 0 || at->tokens > 0x7fffffff - 512)
-        return op_fail(TIDE_ERR_INVALID_ARG, "tokens %lld", (long long)at->tokens);
-    if (at->k_heads < 1 || at->q_heads < 1 || at->q_heads > 65535 || at->q_heads % at->k_heads)
-        return op_fail(TIDE_ERR_INVALID_ARG, "q_heads %d, k_heads %d: need a multiple, at most 65535", at->q_heads,
-                       at->k_heads);
-    if (at->tokens * at->q_heads > int64_t(1) << 34)
-        return op_fail(TIDE_ERR_INVALID_ARG, "tokens %lld times q_heads %d is above 2^34", (long long)at->tokens,
-                       at->q_heads);
-    if (at->head_dim < 8 || at->head_dim % 8)
-        return op_fail(TIDE_ERR_INVALID_ARG, "head_dim %d: need a multiple of 8", at->head_dim);
-    if (at->head_dim > kMaxHeadDim)
-        return op_fail(TIDE_ERR_UNSUPPORTED, "head_dim %d: at most %d", at->head_dim, kMaxHeadDim);
-    if (!(at->scale > 0.f) || at->scale > 3.0e38f)
-        return op_fail(TIDE_ERR_INVALID_ARG, "scale %g: need a positive number", double(at->scale));
-    if (at->offsets) {
-        if (at->sequences < 0 || at->sequences > 0x7ffffffe)
-            return op_fail(TIDE_ERR_INVALID_ARG, "sequences %lld", (long long)at->sequences);
-        if (at->offset_bytes != 4 && at->offset_bytes != 8)
-            return op_fail(TIDE_ERR_INVALID_ARG, "offset_bytes %d: need 4 or 8", at->offset_bytes);
-        if (!op_aligned(at->offsets, size_t(at->offset_bytes)))
-            return op_fail(TIDE_ERR_ALIGNMENT, "offsets are not aligned to their size");
+    um::fence_before();
+    __syncthreads();
+    um::fence_after();
+    if (gave_up) {  // what was claimed and not finished is NaN
+        if (threadIdx.x == 0)
+            g_timed_out = 1;
+        if (warp < 8)
+            for (int i = done[warp]; i < claimed; ++i) {
+                int head, r0;
+                place_of(f, claims[i % kClaims], head, r0);
+                const int r = r0 + threadIdx.x;
+                if (r >= pr.T)
+                    continue;
+                for (int d = 0; d < pr.D; ++d)
+                    f.o.row(r, head)[d] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+                f.lse[int64_t(head) * pr.T + r] = __int_as_float(0x7fffffff);
+            }
     }
-    return TIDE_OK;
+    if (warp == 9)
+        um::tmem_free_own(tmem, 512);
 }
 
-tide_status_t check_heads(const tide_attention_t *at, const tide_heads_t *x, int heads, bool output, const char *name)
+template <int W>
+tide_status_t launch(const Forward &f, cudaStream_t st)
 {
-    if (at->tokens == 0)
-        return TIDE_OK;
-    if (!x || !x->data)
-        return op_fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
-    const bool many_t = at->tokens > 1, many_h = heads > 1;
-    const int64_t limit = int64_t(1) << 38;  // a tensor map's strides are below 2^40 bytes
-    if ((many_t && (x->token_stride < 1 || x->token_stride > limit)) ||
-        (many_h && (x->head_stride < 1 || x->head_stride > limit)))
-        return op_fail(TIDE_ERR_INVALID_ARG, "%s has bad strides", name);
-    if (!op_aligned(x->data, 16) || (many_t && x->token_stride % 8) || (many_h && x->head_stride % 8))
-        return op_fail(TIDE_ERR_ALIGNMENT, "rows of %s are not on 16-byte boundaries", name);
-    if (output) {
-        const int64_t d = at->head_dim;
-        bool apart = (!many_t || x->token_stride >= d) && (!many_h || x->head_stride >= d);
-        if (apart && many_t && many_h)
-            apart = x->token_stride >= x->head_stride ? x->token_stride >= (heads - 1) * x->head_stride + d
-                                                      : x->head_stride >= (at->tokens - 1) * x->token_stride + d;
-        if (!apart)
-            return op_fail(TIDE_ERR_INVALID_ARG, "rows of %s overlap", name);
-    }
-    return TIDE_OK;
-}
-
-tide_status_t check_floats(const tide_attention_t *at, const float *p, const char *name)
-{
-    if (at->tokens && !p)
-        return op_fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
-    return op_aligned(p, 4) ? TIDE_OK : op_fail(TIDE_ERR_ALIGNMENT, "%s is not aligned to its element size", name);
-}
-
-Problem problem_of(const tide_attention_t *at)
-{
-    Problem p = {};
-    p.offsets = at->offsets, p.offset_bytes = at->offset_bytes, p.n = int(at->sequences);
-    p.T = int(at->tokens), p.Hq = at->q_heads, p.Hk = at->k_heads, p.D = at->head_dim;
-    p.causal = at->causal != 0, p.scale = at->scale;
-    return p;
-}
-
-// Strides of dimensions of one element are not looked at: any will do.
-Heads heads_of(const tide_attention_t *at, const tide_heads_t *x, int heads)
-{
-    return {static_cast<bf16 *>(x->data), at->tokens > 1 ? x->token_stride : int64_t(at->head_dim),
-            heads > 1 ? x->head_stride : int64_t(at->head_dim)};
+    constexpr int smem = 2 * (W / 64) * kHalf + kRingBytes + 1024;  // 1024: alignment
+    const cudaError_t e = tide::op_allow_smem<forward_kernel<W>>(smem);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "attention: %s", cudaGetErrorString(e));
+    forward_kernel<W><<<unsigned(f.items), kThreads, smem, st>>>(f);
+    return tide::op_launched("attention");
 }
 
 }  // namespace
+
+namespace tide {
+namespace attn {
+
+cudaError_t forward_timed_out(int *seen, cudaStream_t st) { return take_flag(g_timed_out, seen, st); }
+
+}  // namespace attn
+}  // namespace tide
 
 extern "C" {
 
@@ -360,66 +568,26 @@ tide_status_t tide_attention(const tide_attention_t *at, const tide_heads_t *q, 
         s = check_floats(at, lse, "lse");
     if (s || at->tokens == 0)
         return s;
+    if (!tide::encode_tiled())
+        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const tide::NvtxRange range("tide_attention");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Problem p = problem_of(at);
-    forward_simple<<<dim3(unsigned((p.T + 127) / 128), unsigned(p.Hq)), 128, 0, st>>>(
-        p, heads_of(at, q, p.Hq), heads_of(at, k, p.Hk), heads_of(at, v, p.Hk), heads_of(at, o, p.Hq), lse);
-    return tide::op_launched("attention");
-}
-
-int64_t tide_attention_grad_workspace(const tide_attention_t *at)
-{
-    tide::record_error("");
-    if (check_desc(at))
-        return -1;
-    return std::max<int64_t>(256, at->tokens * at->q_heads * 4);
-}
-
-tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t *dout, const tide_heads_t *q,
-                                  const tide_heads_t *k, const tide_heads_t *v, const tide_heads_t *o,
-                                  const float *lse, const tide_heads_t *dq, const tide_heads_t *dk,
-                                  const tide_heads_t *dv, void *workspace, int64_t workspace_bytes, void *stream)
-{
-    tide::record_error("");
-    tide_status_t s = check_desc(at);
-    const struct {
-        const tide_heads_t *x;
-        bool q, output;
-        const char *name;
-    } all[] = {{dout, true, false, "do"}, {q, true, false, "q"},  {k, false, false, "k"},  {v, false, false, "v"},
-               {o, true, false, "o"},     {dq, true, true, "dq"}, {dk, false, true, "dk"}, {dv, false, true, "dv"}};
-    for (const auto &a : all)
-        if (!s)
-            s = check_heads(at, a.x, a.q ? at->q_heads : at->k_heads, a.output, a.name);
+    Forward f = {};
+    f.pr = problem_of(at);
+    const Problem &p = f.pr;
+    f.hq = heads_of(at, q, p.Hq), f.hk = heads_of(at, k, p.Hk), f.hv = heads_of(at, v, p.Hk), f.o = heads_of(at, o, p.Hq);
+    f.lse = lse;
+    f.items = (p.T + 2 * kTile - 1) / (2 * kTile) * p.Hq;
+    f.wait_ns = wait_of(at);
+    f.skip_fill = (at->debug & TIDE_DEBUG_SKIP_FILL) != 0;
+    s = heads_map(&f.q, f.hq, p.T, p.Hq, p.D);
     if (!s)
-        s = check_floats(at, lse, "lse");
-    if (s || at->tokens == 0)
-        return s;
-    const int64_t need = tide_attention_grad_workspace(at);
-    if (!workspace || workspace_bytes < need)
-        return op_fail(TIDE_ERR_INVALID_ARG, "workspace of %lld bytes: need %lld", (long long)workspace_bytes,
-                       (long long)need);
-    if (!op_aligned(workspace, 256))
-        return op_fail(TIDE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-    const tide::NvtxRange range("tide_attention_grad");
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Problem p = problem_of(at);
-    float *delta = static_cast<float *>(workspace);
-    const Heads hq = heads_of(at, q, p.Hq), hk = heads_of(at, k, p.Hk), hv = heads_of(at, v, p.Hk);
-    const Heads hd = heads_of(at, dout, p.Hq);
-    delta_kernel<<<unsigned((int64_t(p.T) * p.Hq + 15) / 16), 256, 0, st>>>(p, hd, heads_of(at, o, p.Hq), delta);
-    s = tide::op_launched("attention_grad: delta");
+        s = heads_map(&f.k, f.hk, p.T, p.Hk, p.D);
+    if (!s)
+        s = heads_map(&f.v, f.hv, p.T, p.Hk, p.D);
     if (s)
         return s;
-    const unsigned tiles = unsigned((p.T + 127) / 128);
-    dkv_simple<<<dim3(tiles, unsigned(p.Hk)), 128, 0, st>>>(p, hq, hk, hv, hd, lse, delta, heads_of(at, dk, p.Hk),
-                                                           heads_of(at, dv, p.Hk));
-    s = tide::op_launched("attention_grad: dk, dv");
-    if (s)
-        return s;
-    dq_simple<<<dim3(tiles, unsigned(p.Hq)), 128, 0, st>>>(p, hq, hk, hv, hd, lse, delta, heads_of(at, dq, p.Hq));
-    return tide::op_launched("attention_grad: dq");
+    return p.D <= 64 ? launch<64>(f, st) : launch<128>(f, st);
 }
 
 }  // extern "C"

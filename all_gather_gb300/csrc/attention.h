@@ -1,0 +1,244 @@
+// What attention and its gradient share: the problem, which tokens see which,
+// rows computed by themselves, argument checks.  Not part of the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "ops_internal.h"
+#include "tensor_map.h"
+#include "umma.h"
+
+namespace tide {
+namespace attn {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kMaxHeadDim = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr unsigned kAll = 0xffffffffu;
+
+// A tensor of heads: rows of D contiguous elements on 16-byte boundaries.
+struct Heads {
+    bf16 *p;
+    int64_t ts, hs;
+    __host__ __device__ bf16 *row(int64_t t, int64_t h) const { return p + t * ts + h * hs; }
+};
+
+// [a, b): which keys a row sees, or which rows see a key; empty: a >= b.
+struct Span {
+    int a, b;
+};
+
+struct Problem {
+    const void *offsets;  // NULL: one sequence
+    int offset_bytes, n;  // n sequences
+    int T, Hq, Hk, D, causal;
+    float scale;
+
+    __device__ int64_t offset(int i) const
+    {
+        return offset_bytes == 8 ? static_cast<const int64_t *>(offsets)[i]
+                                 : int64_t(static_cast<const int32_t *>(offsets)[i]);
+    }
+    // The sequence of token t, cut to [0, T); empty if it belongs to none.  Whatever the offsets hold, nothing
+    // outside them is read and what comes out lies in [0, T).
+    __device__ Span sequence(int t) const
+    {
+        if (t < 0 || t >= T)
+            return {0, 0};
+        if (!offsets)
+            return {0, T};
+        int lo = -1, hi = n;  // offset(lo) <= t < offset(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (offset(mid) <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        if (lo < 0)
+            return {0, 0};
+        const int64_t a = max(int64_t(0), offset(lo)), b = min(int64_t(T), offset(lo + 1));
+        return a <= t && t < b ? Span{int(a), int(b)} : Span{0, 0};
+    }
+    __device__ Span keys_of(int r) const
+    {
+        const Span s = sequence(r);
+        return {s.a, causal ? min(s.b, r + 1) : s.b};
+    }
+    __device__ Span rows_of(int c) const
+    {
+        const Span s = sequence(c);
+        return {causal ? max(s.a, c) : s.a, s.b};
+    }
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- rows by themselves
+//
+// One row (or key) a lane, by the formulas, over what it sees and nothing else.
+
+static __device__ float dot_row(const bf16 *a, const bf16 *b, int D)
+{
+    float s = 0.f;
+    for (int d = 0; d < D; d += 8) {
+        float x[8], y[8];
+        tide::load8(a + d, x);
+        tide::load8(b + d, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s = fmaf(x[i], y[i], s);
+    }
+    return s;
+}
+
+// The union of a warp's spans.
+static __device__ Span warp_span(Span s)
+{
+    const bool some = s.a < s.b;
+    return {__reduce_min_sync(kAll, some ? s.a : 0x7fffffff), __reduce_max_sync(kAll, some ? s.b : 0)};
+}
+
+// ---------------------------------------------------------------- what the kernels share
+
+constexpr int kTile = 128;        // rows and keys of a tile
+constexpr int kHalf = kTile * 128;  // bytes of a tile's 64 columns in shared memory
+
+// Tensor map whose copies are 64 columns of one head of `kTile` tokens; what lies outside reads as 0.
+inline tide_status_t heads_map(CUtensorMap *map, const Heads &x, int T, int H, int D)
+{
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(H), cuuint64_t(T)};
+    const cuuint64_t strides[2] = {cuuint64_t(x.hs) * 2, cuuint64_t(x.ts) * 2};
+    const cuuint32_t box[3] = {64, 1, kTile};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, x.p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// A tile of `halves` times 64 columns into shared memory, by one thread.
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int halves, int head, int t0, uint32_t bar)
+{
+    for (int i = 0; i < halves; ++i)
+        umma::tma_load_3d_own(dst + i * kHalf, map, 64 * i, head, t0, bar);
+}
+
+// Tiles of 128 that hold the tokens of a span.
+struct Tiles {
+    int a, b;
+};
+__device__ __forceinline__ Tiles tiles_of(Span s) { return s.a < s.b ? Tiles{s.a / kTile, (s.b + kTile - 1) / kTile} : Tiles{0, 0}; }
+
+// ---------------------------------------------------------------- host
+
+inline tide_status_t check_desc(const tide_attention_t *at)
+{
+    if (!at)
+        return op_fail(TIDE_ERR_INVALID_ARG, "at is NULL");
+    if (at->tokens < 0 || at->tokens > 0x7fffffff - 512)
+        return op_fail(TIDE_ERR_INVALID_ARG, "tokens %lld", (long long)at->tokens);
+    if (at->k_heads < 1 || at->q_heads < 1 || at->q_heads > 65535 || at->q_heads % at->k_heads)
+        return op_fail(TIDE_ERR_INVALID_ARG, "q_heads %d, k_heads %d: need a multiple, at most 65535", at->q_heads,
+                       at->k_heads);
+    if (at->tokens * at->q_heads > int64_t(1) << 34)
+        return op_fail(TIDE_ERR_INVALID_ARG, "tokens %lld times q_heads %d is above 2^34", (long long)at->tokens,
+                       at->q_heads);
+    if (at->head_dim < 8 || at->head_dim % 8)
+        return op_fail(TIDE_ERR_INVALID_ARG, "head_dim %d: need a multiple of 8", at->head_dim);
+    if (at->head_dim > kMaxHeadDim)
+        return op_fail(TIDE_ERR_UNSUPPORTED, "head_dim %d: at most %d", at->head_dim, kMaxHeadDim);
+    if (!(at->scale > 0.f) || at->scale > 3.0e38f)
+        return op_fail(TIDE_ERR_INVALID_ARG, "scale %g: need a positive number", double(at->scale));
+    if (at->debug & ~(TIDE_DEBUG_SHORT_WAIT | TIDE_DEBUG_SKIP_FILL))
+        return op_fail(TIDE_ERR_INVALID_ARG, "unknown debug bits 0x%x", at->debug);
+    if (at->offsets) {
+        if (at->sequences < 0 || at->sequences > 0x7ffffffe)
+            return op_fail(TIDE_ERR_INVALID_ARG, "sequences %lld", (long long)at->sequences);
+        if (at->offset_bytes != 4 && at->offset_bytes != 8)
+            return op_fail(TIDE_ERR_INVALID_ARG, "offset_bytes %d: need 4 or 8", at->offset_bytes);
+        if (!op_aligned(at->offsets, size_t(at->offset_bytes)))
+            return op_fail(TIDE_ERR_ALIGNMENT, "offsets are not aligned to their size");
+    }
+    return TIDE_OK;
+}
+
+inline tide_status_t check_heads(const tide_attention_t *at, const tide_heads_t *x, int heads, bool output, const char *name)
+{
+    if (at->tokens == 0)
+        return TIDE_OK;
+    if (!x || !x->data)
+        return op_fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
+    const bool many_t = at->tokens > 1, many_h = heads > 1;
+    const int64_t limit = int64_t(1) << 38;  // a tensor map's strides are below 2^40 bytes
+    if ((many_t && (x->token_stride < 1 || x->token_stride > limit)) ||
+        (many_h && (x->head_stride < 1 || x->head_stride > limit)))
+        return op_fail(TIDE_ERR_INVALID_ARG, "%s has bad strides", name);
+    if (!op_aligned(x->data, 16) || (many_t && x->token_stride % 8) || (many_h && x->head_stride % 8))
+        return op_fail(TIDE_ERR_ALIGNMENT, "rows of %s are not on 16-byte boundaries", name);
+    if (output) {
+        const int64_t d = at->head_dim;
+        bool apart = (!many_t || x->token_stride >= d) && (!many_h || x->head_stride >= d);
+        if (apart && many_t && many_h)
+            apart = x->token_stride >= x->head_stride ? x->token_stride >= (heads - 1) * x->head_stride + d
+                                                      : x->head_stride >= (at->tokens - 1) * x->token_stride + d;
+        if (!apart)
+            return op_fail(TIDE_ERR_INVALID_ARG, "rows of %s overlap", name);
+    }
+    return TIDE_OK;
+}
+
+inline tide_status_t check_floats(const tide_attention_t *at, const float *p, const char *name)
+{
+    if (at->tokens && !p)
+        return op_fail(TIDE_ERR_INVALID_ARG, "%s is NULL", name);
+    return op_aligned(p, 4) ? TIDE_OK : op_fail(TIDE_ERR_ALIGNMENT, "%s is not aligned to its element size", name);
+}
+
+inline Problem problem_of(const tide_attention_t *at)
+{
+    Problem p = {};
+    p.offsets = at->offsets, p.offset_bytes = at->offset_bytes, p.n = int(at->sequences);
+    p.T = int(at->tokens), p.Hq = at->q_heads, p.Hk = at->k_heads, p.D = at->head_dim;
+    p.causal = at->causal != 0, p.scale = at->scale;
+    return p;
+}
+
+// Strides of dimensions of one element are not looked at: any will do.
+inline Heads heads_of(const tide_attention_t *at, const tide_heads_t *x, int heads)
+{
+    return {static_cast<bf16 *>(x->data), at->tokens > 1 ? x->token_stride : int64_t(at->head_dim),
+            heads > 1 ? x->head_stride : int64_t(at->head_dim)};
+}
+
+
+inline uint64_t wait_of(const tide_attention_t *at)
+{
+    return at->debug & TIDE_DEBUG_SHORT_WAIT ? kShortWaitBudgetNs : kWaitBudgetNs;
+}
+
+// Reads and clears a device flag (synchronises the stream).
+inline cudaError_t take_flag(const int &flag, int *seen, cudaStream_t st)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(seen, flag, sizeof *seen, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *seen) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(flag, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+    }
+    return e;
+}
+
+// Reads and clears whether a bounded wait ran out (attention.cu, attention_grad.cu).
+cudaError_t forward_timed_out(int *seen, cudaStream_t st);
+cudaError_t grad_timed_out(int *seen, cudaStream_t st);
+
+}  // namespace attn
+}  // namespace tide

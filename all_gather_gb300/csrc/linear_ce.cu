@@ -48,11 +48,15 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "attention.h"
 #include "ops_internal.h"
+#include "tensor_map.h"
 #include "umma.h"
 
 namespace {
 
+using tide::encode;
+using tide::encode_tiled;
 using tide::op_aligned;
 using tide::op_fail;
 using bf16 = __nv_bfloat16;
@@ -878,24 +882,6 @@ int64_t piece_of(const tide_ce_t *ce)
 
 // ---------------------------------------------------------------- host
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // A row-major bf16 matrix.
 struct Mat {
     const bf16 *p;
@@ -907,18 +893,6 @@ struct Mat {
 bool rows_aligned(const void *p, int64_t stride, int64_t rows)
 {
     return op_aligned(p, 16) && (rows < 2 || stride % 8 == 0);
-}
-
-tide_status_t encode(CUtensorMap *map, CUtensorMapDataType type, int rank, void *p, const cuuint64_t *dims,
-                     const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle)
-{
-    const cuuint32_t step[3] = {1, 1, 1};
-    const CUresult r = encode_tiled()(map, type, cuuint32_t(rank), p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return op_fail(TIDE_ERR_CUDA, "cuTensorMapEncodeTiled: %d", int(r));
-    return TIDE_OK;
 }
 
 // Tensor map whose copies are `box_rows` rows of `box_cols` columns (64, or 32);
@@ -1238,19 +1212,15 @@ tide_status_t tide_ops_device_status(void *stream)
 {
     tide::record_error("");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int seen = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&seen, g_timed_out, sizeof seen, 0, cudaMemcpyDeviceToHost, st);
+    int seen[3] = {};
+    cudaError_t e = tide::attn::take_flag(g_timed_out, &seen[0], st);
     if (e == cudaSuccess)
-        e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && seen) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_timed_out, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess)
-            e = cudaStreamSynchronize(st);
-    }
+        e = tide::attn::forward_timed_out(&seen[1], st);
+    if (e == cudaSuccess)
+        e = tide::attn::grad_timed_out(&seen[2], st);
     if (e != cudaSuccess)
         return op_fail(TIDE_ERR_CUDA, "operators' status: %s", cudaGetErrorString(e));
-    return seen ? op_fail(TIDE_ERR_TIMEOUT, "a bounded device-side wait expired") : TIDE_OK;
+    return seen[0] || seen[1] || seen[2] ? op_fail(TIDE_ERR_TIMEOUT, "a bounded device-side wait expired") : TIDE_OK;
 }
 
 }  // extern "C"
