@@ -36,7 +36,8 @@ using tide::op_aligned;
 using tide::op_fail;
 namespace um = tide::umma;
 
-constexpr int kThreads = 320;          // two groups of four warps for the rows, a warp that fetches, one that multiplies
+constexpr int kThreads = 384;          // two groups of four warps for the rows; a warp that fetches, one that multiplies, two idle
+constexpr int kRowRegs = 224, kOtherRegs = 56;  // registers a thread, of 168 at the launch: (2 * 224 + 56) * 128 = 168 * 384
 constexpr int kRingBytes = 160 * 1024;
 constexpr int kClaims = 8;             // of a block's last items, kept for a wait that runs out
 constexpr float kLazy = 8.f;           // log2 of how far P may grow before its maximum moves
@@ -64,8 +65,21 @@ __device__ __forceinline__ void place_of(const Forward &f, int item, int &head, 
     r0 = (f.items / f.pr.Hq - 1 - item / f.pr.Hq) * 2 * kTile;
 }
 
+// Key tiles that the rows r0 to r0 + 127 see, by a warp: four rows a lane.
+__device__ __forceinline__ Tiles seen_by_tile(const Problem &pr, int r0, int lane)
+{
+    Span see = {0x7fffffff, 0};
+#pragma unroll 1
+    for (int r = r0 + lane; r < r0 + kTile; r += 32) {
+        const Span s = pr.keys_of(r);
+        if (s.a < s.b)
+            see = {min(see.a, s.a), max(see.b, s.b)};
+    }
+    return tiles_of(warp_span(see));
+}
+
 // Rows of a warp whose result was not finite, over what they see only.
-__device__ __noinline__ void row_forward(const bf16 *q, const Heads &k, const Heads &v, int hk, Span see, int D, float c,
+__device__ __forceinline__ void row_forward(const bf16 *q, const Heads &k, const Heads &v, int hk, Span see, int D, float c,
                                          float lse2, bf16 *o)
 {
     const Span all = warp_span(see);
@@ -141,225 +155,218 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     const uint32_t tmem = tmem_slot;  // S of both tiles, 128 columns each, then their O
     auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait(bar, parity, &gave_up, f.wait_ns); };
 
-    if (warp == 8) {
-        const bool leader = um::elected();
-        int number = blockIdx.x, slot = 0, turn = 0, stage = 0, phase = 0, taken = 0;
-        int fills = 0, q_fills[2] = {0, 0};  // copies under way at most: the last of each place
-        uint32_t q_phase[2] = {0, 0};
-        bool ok = true;
-        while (ok) {
-            if (lane == 0) {
-                claims[taken % kClaims] = number;
-                claimed = taken + 1;
-            }
-            ++taken;
-            if (leader)
-                um::ask_next_block(um::smem_addr(&answer), asked);
-            // which key tiles the rows see: four rows a lane
-            int head, r0;
-            place_of(f, number, head, r0);
-            Tiles keys[2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                Span see = {0x7fffffff, 0};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const Span s = pr.keys_of(r0 + t * kTile + i * 32 + lane);
-                    if (s.a < s.b)
-                        see = {min(see.a, s.a), max(see.b, s.b)};
+    if (warp >= 8) {
+        um::fewer_registers<kOtherRegs>();
+        if (warp == 8) {
+            const bool leader = um::elected();
+            int number = blockIdx.x, slot = 0, turn = 0, stage = 0, phase = 0, taken = 0;
+            int fills = 0, q_fills[2] = {0, 0};  // copies under way at most: the last of each place
+            uint32_t q_phase[2] = {0, 0};
+            bool ok = true;
+            while (ok) {
+                if (lane == 0) {
+                    claims[taken % kClaims] = number;
+                    claimed = taken + 1;
                 }
-                keys[t] = tiles_of(warp_span(see));
-            }
-            if (!(ok = wait(item_empty + 8 * slot, turn ^ 1)))
-                break;
-            if (lane == 0) {
-                items[slot] = {number, {keys[0], keys[1]}};
-                um::mbar_arrive(item_full + 8 * slot);
-            }
-            if (++slot == 2)
-                slot = 0, turn ^= 1;
-            const bool both = keys[0].a < keys[0].b && keys[1].a < keys[1].b;
-            const Tiles all = both ? Tiles{min(keys[0].a, keys[1].a), max(keys[0].b, keys[1].b)}
-                                   : keys[0].a < keys[0].b ? keys[0] : keys[1];
-            bool skip = f.skip_fill && number == 0;  // this item's first key tile never comes
-            for (int j = all.a; ok && j < all.b; ++j) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (j != all.a || keys[t].a >= keys[t].b)
-                        continue;
-                    if (!(ok = wait(q_empty + 8 * t, q_phase[t] ^ 1)))
-                        break;
-                    q_phase[t] ^= 1;
-                    if (leader) {
-                        um::mbar_expect(q_full + 8 * t, kTileBytes);
-                        load_tile(q_at + t * kTileBytes, &f.q, kHalves, head, r0 + t * kTile, q_full + 8 * t);
-                    }
-                    ++q_fills[t];
+                ++taken;
+                if (leader)
+                    um::ask_next_block(um::smem_addr(&answer), asked);
+                // which key tiles the rows see: four rows a lane
+                int head, r0;
+                place_of(f, number, head, r0);
+                const Tiles keys[2] = {seen_by_tile(pr, r0, lane), seen_by_tile(pr, r0 + kTile, lane)};
+                if (!(ok = wait(item_empty + 8 * slot, turn ^ 1)))
+                    break;
+                if (lane == 0) {
+                    items[slot] = {number, {keys[0], keys[1]}};
+                    um::mbar_arrive(item_full + 8 * slot);
                 }
+                if (++slot == 2)
+                    slot = 0, turn ^= 1;
+                const bool both = keys[0].a < keys[0].b && keys[1].a < keys[1].b;
+                const Tiles all = both ? Tiles{min(keys[0].a, keys[1].a), max(keys[0].b, keys[1].b)}
+                                       : keys[0].a < keys[0].b ? keys[0] : keys[1];
+                bool skip = f.skip_fill && number == 0;  // this item's first key tile never comes
+                for (int j = all.a; ok && j < all.b; ++j) {
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!ok || !(ok = wait(empty + 8 * stage, phase ^ 1)))
-                        break;
-                    if (skip) {
-                        ok = wait(never, 0);  // nothing arrives there
-                        skip = false;
-                        break;
+                    for (int t = 0; t < 2; ++t) {
+                        if (j != all.a || keys[t].a >= keys[t].b)
+                            continue;
+                        if (!(ok = wait(q_empty + 8 * t, q_phase[t] ^ 1)))
+                            break;
+                        q_phase[t] ^= 1;
+                        if (leader) {
+                            um::mbar_expect(q_full + 8 * t, kTileBytes);
+                            load_tile(q_at + t * kTileBytes, &f.q, kHalves, head, r0 + t * kTile, q_full + 8 * t);
+                        }
+                        ++q_fills[t];
                     }
-                    if (leader) {
-                        um::mbar_expect(full + 8 * stage, kTileBytes);
-                        load_tile(ring + stage * kTileBytes, kv ? &f.v : &f.k, kHalves, head / group, j * kTile,
-                                  full + 8 * stage);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (!ok || !(ok = wait(empty + 8 * stage, phase ^ 1)))
+                            break;
+                        if (skip) {
+                            ok = wait(never, 0);  // nothing arrives there
+                            skip = false;
+                            break;
+                        }
+                        if (leader) {
+                            um::mbar_expect(full + 8 * stage, kTileBytes);
+                            load_tile(ring + stage * kTileBytes, kv ? &f.v : &f.k, kHalves, head / group, j * kTile,
+                                      full + 8 * stage);
+                        }
+                        ++fills;
+                        if (++stage == kStages)
+                            stage = 0, phase ^= 1;
                     }
-                    ++fills;
-                    if (++stage == kStages)
-                        stage = 0, phase ^= 1;
+                }
+                if (!ok || !(ok = wait(asked, (taken - 1) & 1)))
+                    break;
+                number = um::next_block(um::smem_addr(&answer));
+                um::fence_copies();
+                __syncwarp();
+                if (number < 0)
+                    break;
+            }
+            if (ok && (ok = wait(item_empty + 8 * slot, turn ^ 1))) {
+                if (lane == 0) {
+                    items[slot].number = -1;
+                    um::mbar_arrive(item_full + 8 * slot);
                 }
             }
-            if (!ok || !(ok = wait(asked, (taken - 1) & 1)))
-                break;
-            number = um::next_block(um::smem_addr(&answer));
-            um::fence_copies();
+            if (!ok) {
+                // The answer that is under way, and the copies: neither may find the block gone.
+                auto land = [&](uint32_t bar, uint32_t parity) {
+                    const uint64_t t0 = um::now_ns();
+                    while (!um::mbar_try(bar, parity) && um::now_ns() - t0 < f.wait_ns) {
+                    }
+                };
+                land(asked, (taken - 1) & 1);
+                const int more = um::next_block(um::smem_addr(&answer));
+                if (lane == 0 && more >= 0 && more != number) {
+                    claims[taken % kClaims] = more;
+                    claimed = taken + 1;
+                }
+                for (int i = max(0, fills - kStages); i < fills; ++i)
+                    land(full + 8 * (i % kStages), (i / kStages) & 1);
+                for (int t = 0; t < 2; ++t)
+                    if (q_fills[t])
+                        land(q_full + 8 * t, (q_fills[t] - 1) & 1);
+            }
             __syncwarp();
-            if (number < 0)
-                break;
-        }
-        if (ok && (ok = wait(item_empty + 8 * slot, turn ^ 1))) {
-            if (lane == 0) {
-                items[slot].number = -1;
-                um::mbar_arrive(item_full + 8 * slot);
-            }
-        }
-        if (!ok) {
-            // The answer that is under way, and the copies: neither may find the block gone.
-            auto land = [&](uint32_t bar, uint32_t parity) {
-                const uint64_t t0 = um::now_ns();
-                while (!um::mbar_try(bar, parity) && um::now_ns() - t0 < f.wait_ns) {
+        } else if (warp == 9) {
+            const bool leader = um::elected();
+            const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
+            const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
+            const uint32_t idesc_o = um::instr_desc(kTile, dn, false, true);
+            int slot = 0, turn = 0, stage = 0, phase = 0;
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+            bool ok = true;
+            // S of row tile t from the key tile in a stage
+            auto scores = [&](int t, int at) {
+                um::fence_after();
+                if (leader) {
+                    const uint64_t a = um::operand_desc(q_at + t * kTileBytes, false, 0);
+                    const uint64_t b = um::operand_desc(ring + at * kTileBytes, false, 0);
+                    for (int i = 0; i < ksteps; ++i) {
+                        const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
+                        um::mma_own(tmem + t * kTile, a + off, b + off, idesc_s, i > 0);
+                    }
+                    um::mma_commit_own(s_full + 8 * t);
                 }
             };
-            land(asked, (taken - 1) & 1);
-            const int more = um::next_block(um::smem_addr(&answer));
-            if (lane == 0 && more >= 0 && more != number) {
-                claims[taken % kClaims] = more;
-                claimed = taken + 1;
-            }
-            for (int i = max(0, fills - kStages); i < fills; ++i)
-                land(full + 8 * (i % kStages), (i / kStages) & 1);
-            for (int t = 0; t < 2; ++t)
-                if (q_fills[t])
-                    land(q_full + 8 * t, (q_fills[t] - 1) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 9) {
-        const bool leader = um::elected();
-        const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
-        const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
-        const uint32_t idesc_o = um::instr_desc(kTile, dn, false, true);
-        int slot = 0, turn = 0, stage = 0, phase = 0;
-        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
-        bool ok = true;
-        // S of row tile t from the key tile in a stage
-        auto scores = [&](int t, int at) {
-            um::fence_after();
-            if (leader) {
-                const uint64_t a = um::operand_desc(q_at + t * kTileBytes, false, 0);
-                const uint64_t b = um::operand_desc(ring + at * kTileBytes, false, 0);
-                for (int i = 0; i < ksteps; ++i) {
-                    const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
-                    um::mma_own(tmem + t * kTile, a + off, b + off, idesc_s, i > 0);
+            while (ok) {
+                if (!(ok = wait(item_full + 8 * slot, turn)))
+                    break;
+                const Item it = items[slot];
+                __syncwarp();
+                if (lane == 0)
+                    um::mbar_arrive(item_empty + 8 * slot);
+                if (++slot == 2)
+                    slot = 0, turn ^= 1;
+                if (it.number < 0)
+                    break;
+                const Tiles &k0 = it.keys[0], &k1 = it.keys[1];
+                const bool both = k0.a < k0.b && k1.a < k1.b;
+                const Tiles all = both ? Tiles{min(k0.a, k1.a), max(k0.b, k1.b)} : k0.a < k0.b ? k0 : k1;
+                for (int j = all.a - 1; ok && j < all.b; ++j) {  // P v of key tile j, scores of key tile j + 1
+                    const int v_at = stage;
+                    bool v_here = j < all.a;
+                    int k_at = stage;
+                    uint32_t k_phase = phase;
+                    if (j >= all.a && ++k_at == kStages)
+                        k_at = 0, k_phase ^= 1;
+                    bool k_here = j + 1 >= all.b;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const Tiles &mine = t ? k1 : k0;
+                        if (j >= mine.a && j < mine.b) {
+                            if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
+                                break;
+                            v_here = true;
+                            if (j == mine.a) {
+                                if (!(ok = wait(o_free + 8 * t, o_phase[t] ^ 1)))
+                                    break;
+                                o_phase[t] ^= 1;
+                            }
+                            if (!(ok = wait(p_ready + 8 * t, p_phase[t])))
+                                break;
+                            p_phase[t] ^= 1;
+                            um::fence_after();
+                            if (leader) {
+                                const uint64_t b = um::operand_desc(ring + v_at * kTileBytes, true, kHalf);
+#pragma unroll
+                                for (int i = 0; i < kTile / 16; ++i)
+                                    um::mma_own_tmem(tmem + 2 * kTile + t * kTile, tmem + t * kTile + i * 8, b + i * (2048 >> 4),
+                                                     idesc_o, j > mine.a || i > 0);
+                                um::mma_commit_own(pv_done + 8 * t);
+                            }
+                        }
+                        if (j + 1 >= mine.a && j + 1 < mine.b) {
+                            if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
+                                break;
+                            k_here = true;
+                            if (j + 1 == mine.a) {
+                                if (!(ok = wait(q_full + 8 * t, q_phase[t])))
+                                    break;
+                                q_phase[t] ^= 1;
+                            }
+                            scores(t, k_at);
+                            if (j + 2 == mine.b && leader)
+                                um::mma_commit_own(q_empty + 8 * t);
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    // a tile that neither row tile needed has to have come all the same, before its place is given back
+                    if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
+                        break;
+                    if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
+                        break;
+                    if (leader) {
+                        if (j >= all.a)
+                            um::mma_commit_own(empty + 8 * v_at);
+                        if (j + 1 < all.b)
+                            um::mma_commit_own(empty + 8 * k_at);
+                    }
+                    // stages: k of all.a, then v of j and k of j + 1 in the order of their loads
+                    const int used = (j >= all.a) + (j + 1 < all.b);
+                    for (int i = 0; i < used; ++i)
+                        if (++stage == kStages)
+                            stage = 0, phase ^= 1;
                 }
-                um::mma_commit_own(s_full + 8 * t);
             }
-        };
-        while (ok) {
-            if (!(ok = wait(item_full + 8 * slot, turn)))
-                break;
-            const Item it = items[slot];
             __syncwarp();
-            if (lane == 0)
-                um::mbar_arrive(item_empty + 8 * slot);
-            if (++slot == 2)
-                slot = 0, turn ^= 1;
-            if (it.number < 0)
-                break;
-            const Tiles &k0 = it.keys[0], &k1 = it.keys[1];
-            const bool both = k0.a < k0.b && k1.a < k1.b;
-            const Tiles all = both ? Tiles{min(k0.a, k1.a), max(k0.b, k1.b)} : k0.a < k0.b ? k0 : k1;
-            for (int j = all.a - 1; ok && j < all.b; ++j) {  // P v of key tile j, scores of key tile j + 1
-                const int v_at = stage;
-                bool v_here = j < all.a;
-                int k_at = stage;
-                uint32_t k_phase = phase;
-                if (j >= all.a && ++k_at == kStages)
-                    k_at = 0, k_phase ^= 1;
-                bool k_here = j + 1 >= all.b;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const Tiles &mine = t ? k1 : k0;
-                    if (j >= mine.a && j < mine.b) {
-                        if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
-                            break;
-                        v_here = true;
-                        if (j == mine.a) {
-                            if (!(ok = wait(o_free + 8 * t, o_phase[t] ^ 1)))
-                                break;
-                            o_phase[t] ^= 1;
-                        }
-                        if (!(ok = wait(p_ready + 8 * t, p_phase[t])))
-                            break;
-                        p_phase[t] ^= 1;
-                        um::fence_after();
-                        if (leader) {
-                            const uint64_t b = um::operand_desc(ring + v_at * kTileBytes, true, kHalf);
-#pragma unroll
-                            for (int i = 0; i < kTile / 16; ++i)
-                                um::mma_own_tmem(tmem + 2 * kTile + t * kTile, tmem + t * kTile + i * 8, b + i * (2048 >> 4),
-                                                 idesc_o, j > mine.a || i > 0);
-                            um::mma_commit_own(pv_done + 8 * t);
-                        }
-                    }
-                    if (j + 1 >= mine.a && j + 1 < mine.b) {
-                        if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
-                            break;
-                        k_here = true;
-                        if (j + 1 == mine.a) {
-                            if (!(ok = wait(q_full + 8 * t, q_phase[t])))
-                                break;
-                            q_phase[t] ^= 1;
-                        }
-                        scores(t, k_at);
-                        if (j + 2 == mine.b && leader)
-                            um::mma_commit_own(q_empty + 8 * t);
-                    }
+            if (leader) {  // nothing may be under way when the accumulators go
+                um::mma_commit_own(drained);
+                const uint64_t t0 = um::now_ns();
+                while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < f.wait_ns) {
                 }
-                if (!ok)
-                    break;
-                // a tile that neither row tile needed has to have come all the same, before its place is given back
-                if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
-                    break;
-                if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
-                    break;
-                if (leader) {
-                    if (j >= all.a)
-                        um::mma_commit_own(empty + 8 * v_at);
-                    if (j + 1 < all.b)
-                        um::mma_commit_own(empty + 8 * k_at);
-                }
-                // stages: k of all.a, then v of j and k of j + 1 in the order of their loads
-                const int used = (j >= all.a) + (j + 1 < all.b);
-                for (int i = 0; i < used; ++i)
-                    if (++stage == kStages)
-                        stage = 0, phase ^= 1;
             }
+            __syncwarp();
         }
-        __syncwarp();
-        if (leader) {  // nothing may be under way when the accumulators go
-            um::mma_commit_own(drained);
-            const uint64_t t0 = um::now_ns();
-            while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < f.wait_ns) {
-            }
-        }
-        __syncwarp();
     } else {
+        um::more_registers<kRowRegs>();
         const int t = warp / 4, quarter = warp % 4;
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t s_at = tmem + lanes + t * kTile, o_at = s_at + 2 * kTile;

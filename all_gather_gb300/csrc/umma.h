@@ -356,6 +356,18 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Registers of the warps of a group of four, all of which call this; the block's sum stays what it was launched with.
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Asks for the next block of the grid that has not started, to work on it here:
 // 16 bytes at `dst`, which count at the barrier.
 __device__ __forceinline__ void ask_next_block(uint32_t dst, uint32_t bar)
