@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             place_of(f, number, head, r0);
             const int r = r0 + t * kTile + quarter * 32 + lane;
             const Span see = pr.keys_of(r);
+            __syncwarp();  // the search for the sequence took lanes apart
             float top = -INFINITY, sum = 0.f;
             for (int j = keys.a; j < keys.b; ++j) {
                 if (!(ok = wait(s_full + 8 * t, s_phase)))
