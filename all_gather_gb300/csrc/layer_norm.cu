@@ -58,27 +58,99 @@ struct Raw {
     uint4 v[sizeof(T) / 2];
 };
 
-template <typename T, bool VEC, int U>
-__device__ __forceinline__ void load_row(const T *p, int cols, int t, int n, Raw<T> (&raw)[U])
+__device__ __forceinline__ void unpack(const Raw<bf16> &raw, float *f);
+__device__ __forceinline__ void unpack(const Raw<float> &raw, float *f);
+
+// Unit u of a thread, from memory.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load_unit(const T *p, int cols, int u, int t, int n)
 {
+    Raw<T> raw;
+    if (VEC) {
+        const int c = column<VEC>(u, 0, t, n);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (VEC) {
-            const int c = column<VEC>(u, 0, t, n);
+        for (int k = 0; k < int(sizeof(T) / 2); ++k)
+            raw.v[k] = c < cols ? __ldg(reinterpret_cast<const uint4 *>(p + c) + k) : make_uint4(0, 0, 0, 0);
+    } else {
+        T e[8];
 #pragma unroll
-            for (int k = 0; k < int(sizeof(T) / 2); ++k)
-                raw[u].v[k] = c < cols ? reinterpret_cast<const uint4 *>(p + c)[k] : make_uint4(0, 0, 0, 0);
-        } else {
-            T e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = column<VEC>(u, i, t, n);
-                e[i] = c < cols ? p[c] : T(0.f);
-            }
-            raw[u] = *reinterpret_cast<Raw<T> *>(e);
+        for (int i = 0; i < 8; ++i) {
+            const int c = column<VEC>(u, i, t, n);
+            e[i] = c < cols ? p[c] : T(0.f);
         }
+        raw = *reinterpret_cast<Raw<T> *>(e);
     }
+    return raw;
 }
+
+// Rows on their way to the threads that will work on them: a thread copies its
+// own units to shared memory (cp.async) two rows ahead, and waits for nobody
+// else's.  Where rows are not on 16-byte boundaries it loads them when it needs
+// them.
+constexpr int kStages = 3;
+template <typename T, bool VEC, int U, int TENSORS>
+struct Stream {
+    static constexpr int kPieces = sizeof(T) / 2;                  // of 16 bytes a unit
+    static constexpr int kStage = TENSORS * U * kPieces * 16;      // bytes a thread
+    uint32_t at;                                                   // of the thread's first piece
+    int pitch;                                                     // between pieces
+    int stage;
+
+    __device__ __forceinline__ Stream(uint32_t smem) : at(smem + threadIdx.x * 16), pitch(int(blockDim.x) * 16), stage(0) {}
+    __device__ __forceinline__ void fetch(const T *const (&rows)[TENSORS], bool some, int ahead, int cols, int t, int n)
+    {
+        if (!VEC)
+            return;
+        const uint32_t to = at + uint32_t((stage + ahead) % kStages) * TENSORS * U * kPieces * pitch;
+        if (some) {
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = column<VEC>(u, 0, t, n);
+                    if (c < cols)
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                             to + uint32_t((k * U + u) * kPieces + i) * pitch),
+                                         "l"(reinterpret_cast<const uint4 *>(rows[k] + c) + i)
+                                         : "memory");
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // The current row's units as fp32; what lies behind its end is 0.
+    __device__ __forceinline__ void take(const T *const (&rows)[TENSORS], int cols, int t, int n, float (&f)[TENSORS][U][8])
+    {
+        if (VEC)
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint32_t from = at + uint32_t(stage) * TENSORS * U * kPieces * pitch;
+#pragma unroll
+        for (int k = 0; k < TENSORS; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                Raw<T> raw;
+                if (VEC) {
+                    const bool in = column<VEC>(u, 0, t, n) < cols;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        uint4 &v = raw.v[i];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(from + uint32_t((k * U + u) * kPieces + i) * pitch)
+                                     : "memory");
+                        if (!in)
+                            v = make_uint4(0, 0, 0, 0);
+                    }
+                } else {
+                    raw = load_unit<T, VEC>(rows[k], cols, u, t, n);
+                }
+                unpack(raw, f[k][u]);
+            }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+};
+
 __device__ __forceinline__ void unpack(const Raw<bf16> &raw, float *f)
 {
     const uint32_t w[4] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w};
@@ -152,28 +224,30 @@ __device__ __forceinline__ Group group_of(int warps, float *shared)
     return {warps, index, int(threadIdx.x) % n, n, shared + index * warps * 8};
 }
 
-template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(1024) forward_kernel(Args<T> a, int warps)
+// THREADS: of a block at most, with BLOCKS of them on an SM.
+template <typename T, bool VEC, int U, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) forward_kernel(Args<T> a, int warps)
 {
+    extern __shared__ uint4 ring[];
     __shared__ float shared[kMaxWarps * 8];
     const Group g = group_of(warps, shared);
     const int64_t step = int64_t(gridDim.x) * (blockDim.x / g.n);
     const float inv = 1.f / float(a.cols);
-    Raw<T> w[U], b[U], x[U];
-    if (a.w)
-        load_row<T, VEC, U>(a.w, a.cols, g.t, g.n, w);
-    if (a.b)
-        load_row<T, VEC, U>(a.b, a.cols, g.t, g.n, b);
+    Stream<T, VEC, U, 1> in(uint32_t(__cvta_generic_to_shared(ring)));
     int64_t row = int64_t(blockIdx.x) * (blockDim.x / g.n) + g.index;
-    if (row < a.rows)
-        load_row<T, VEC, U>(a.x + row * a.xs, a.cols, g.t, g.n, x);
-    for (; row < a.rows; row += step) {
-        float f[U][8], mean[1] = {0.f}, var[1] = {0.f};
+    auto fetch = [&](int64_t r, int ahead) {
+        const T *const rows[1] = {a.x + r * a.xs};
+        in.fetch(rows, r < a.rows, ahead, a.cols, g.t, g.n);
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            unpack(x[u], f[u]);
-        if (row + step < a.rows)  // the next row is on its way
-            load_row<T, VEC, U>(a.x + (row + step) * a.xs, a.cols, g.t, g.n, x);
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(row + i * step, i);
+    for (; row < a.rows; row += step) {
+        fetch(row + (kStages - 1) * step, kStages - 1);
+        float x[1][U][8], mean[1] = {0.f}, var[1] = {0.f};
+        const T *const rows[1] = {a.x + row * a.xs};
+        in.take(rows, a.cols, g.t, g.n, x);
+        auto &f = x[0];
         if (a.center) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -188,7 +262,7 @@ __global__ void __launch_bounds__(1024) forward_kernel(Args<T> a, int warps)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 f[u][i] -= mean[0];
-                if (column<VEC>(u, i, g.t, g.n) < a.cols)
+                if (column<VEC>(u, VEC ? 0 : i, g.t, g.n) < a.cols)
                     var[0] = fmaf(f[u][i], f[u][i], var[0]);
             }
         g.sum(var, 1);
@@ -198,9 +272,9 @@ __global__ void __launch_bounds__(1024) forward_kernel(Args<T> a, int warps)
         for (int u = 0; u < U; ++u) {
             float k[8], s[8];
             if (a.w)
-                unpack(w[u], k);
+                unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
             if (a.b)
-                unpack(b[u], s);
+                unpack(load_unit<T, VEC>(a.b, a.cols, u, g.t, g.n), s);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 f[u][i] *= r;
@@ -214,34 +288,31 @@ __global__ void __launch_bounds__(1024) forward_kernel(Args<T> a, int warps)
     }
 }
 
-template <typename T, bool VEC, int U>
-__global__ void __launch_bounds__(1024) backward_kernel(Args<T> a, int warps)
+template <typename T, bool VEC, int U, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) backward_kernel(Args<T> a, int warps)
 {
+    extern __shared__ uint4 ring[];
     __shared__ float shared[kMaxWarps * 8];
     const Group g = group_of(warps, shared);
     const int groups = blockDim.x / g.n;
     const int64_t step = int64_t(gridDim.x) * groups;
     const float inv = 1.f / float(a.cols);
-    Raw<T> w[U], x[U], dy[U];
+    Stream<T, VEC, U, 2> in(uint32_t(__cvta_generic_to_shared(ring)));
     float dw[U][8] = {}, db[U][8] = {};
-    if (a.w)
-        load_row<T, VEC, U>(a.w, a.cols, g.t, g.n, w);
     const int64_t first = int64_t(blockIdx.x) * groups + g.index;
-    if (first < a.rows) {
-        load_row<T, VEC, U>(a.x + first * a.xs, a.cols, g.t, g.n, x);
-        load_row<T, VEC, U>(a.dy + first * a.dys, a.cols, g.t, g.n, dy);
-    }
-    for (int64_t row = first; row < a.rows; row += step) {
-        float f[U][8], d[U][8], mean[1] = {0.f}, s[3] = {0.f, 0.f, 0.f};
+    auto fetch = [&](int64_t r, int ahead) {
+        const T *const rows[2] = {a.x + r * a.xs, a.dy + r * a.dys};
+        in.fetch(rows, r < a.rows, ahead, a.cols, g.t, g.n);
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            unpack(x[u], f[u]);
-            unpack(dy[u], d[u]);
-        }
-        if (row + step < a.rows) {
-            load_row<T, VEC, U>(a.x + (row + step) * a.xs, a.cols, g.t, g.n, x);
-            load_row<T, VEC, U>(a.dy + (row + step) * a.dys, a.cols, g.t, g.n, dy);
-        }
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(first + i * step, i);
+    for (int64_t row = first; row < a.rows; row += step) {
+        fetch(row + (kStages - 1) * step, kStages - 1);
+        float both[2][U][8], mean[1] = {0.f}, s[3] = {0.f, 0.f, 0.f};
+        const T *const rows[2] = {a.x + row * a.xs, a.dy + row * a.dys};
+        in.take(rows, a.cols, g.t, g.n, both);
+        auto &f = both[0], &d = both[1];
         if (a.center) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -255,10 +326,10 @@ __global__ void __launch_bounds__(1024) backward_kernel(Args<T> a, int warps)
         for (int u = 0; u < U; ++u) {
             float k[8];
             if (a.w)
-                unpack(w[u], k);
+                unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (column<VEC>(u, i, g.t, g.n) >= a.cols)
+                if (column<VEC>(u, VEC ? 0 : i, g.t, g.n) >= a.cols)
                     continue;
                 f[u][i] -= mean[0];
                 const float gi = a.w ? d[u][i] * k[i] : d[u][i];
@@ -275,7 +346,7 @@ __global__ void __launch_bounds__(1024) backward_kernel(Args<T> a, int warps)
         for (int u = 0; u < U; ++u) {
             float k[8], y[8];
             if (a.w)
-                unpack(w[u], k);
+                unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float n = f[u][i] * r, gi = a.w ? d[u][i] * k[i] : d[u][i];
@@ -290,17 +361,17 @@ __global__ void __launch_bounds__(1024) backward_kernel(Args<T> a, int warps)
         return;
     float *p = a.partial + (int64_t(blockIdx.x) * groups + g.index) * 2 * a.cols;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = column<VEC>(u, i, g.t, g.n);
             if (c < a.cols) {
                 if (a.w)
                     p[c] = dw[u][i];
-                p[a.cols + c] = db[u][i];
+                if (a.b)
+                    p[a.cols + c] = db[u][i];
             }
         }
-    }
 }
 
 // ---------------------------------------------------------------- rows that do not fit
@@ -435,20 +506,21 @@ struct Shape {
     int units, warps, groups, blocks;
 };
 
+// A thread has 64 bytes of a row of one tensor, 32 of one of two.
 Shape shape_of(const tide_norm_t *n, bool grad, bool vec)
 {
     Shape s = {};
     s.vec = vec;
-    s.units = grad && n->cols <= 256 * 2 * kMaxWarps ? 2 : 4;
+    s.units = (n->dtype == TIDE_DTYPE_F32 ? 2 : 4) / (grad ? 2 : 1);
     s.warps = int((n->cols + 256 * s.units - 1) / (256 * s.units));
     s.wide = s.warps > kMaxWarps;
     if (s.wide)
         s.warps = kMaxWarps;
     s.groups = std::max(1, 8 / s.warps);
-    const int sms = std::max(tide::op_sm_count(), 1);
     const int threads = s.warps * s.groups * 32;
-    const int per_sm = std::max(1, (grad ? 768 : 1536) / threads);
-    s.blocks = int(std::max<int64_t>(1, std::min<int64_t>((n->rows + s.groups - 1) / s.groups, int64_t(sms) * per_sm)));
+    const int per_sm = threads <= 256 ? grad ? 2 : 3 : threads <= 320 ? 2 : 1;
+    s.blocks = int(std::max<int64_t>(1, std::min<int64_t>((n->rows + s.groups - 1) / s.groups,
+                                                          int64_t(std::max(tide::op_sm_count(), 1)) * per_sm)));
     return s;
 }
 
@@ -467,28 +539,51 @@ Args<T> args_of(const tide_norm_t *n, const void *x, int64_t xs, void *out, int6
     return a;
 }
 
-template <typename T, bool GRAD>
-void launch(const Args<T> &a, const Shape &s, cudaStream_t st)
+template <auto KERNEL, typename T>
+tide_status_t launch_ring(const Args<T> &a, const Shape &s, int bytes, const char *what, cudaStream_t st)
 {
-    const unsigned grid = unsigned(s.blocks), threads = unsigned(s.warps * s.groups * 32);
-    if (s.wide)
-        wide_kernel<T, GRAD><<<grid, 1024, 0, st>>>(a);
-    else if (!GRAD)
-        (s.vec ? forward_kernel<T, true, 4> : forward_kernel<T, false, 4>)<<<grid, threads, 0, st>>>(a, s.warps);
-    else if (s.units == 2)
-        (s.vec ? backward_kernel<T, true, 2> : backward_kernel<T, false, 2>)<<<grid, threads, 0, st>>>(a, s.warps);
-    else
-        (s.vec ? backward_kernel<T, true, 4> : backward_kernel<T, false, 4>)<<<grid, threads, 0, st>>>(a, s.warps);
+    const int threads = s.warps * s.groups * 32, smem = bytes * kStages * threads;
+    const cudaError_t e = tide::op_allow_smem<KERNEL>(200 * 1024);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    KERNEL<<<unsigned(s.blocks), unsigned(threads), smem, st>>>(a, s.warps);
+    return tide::op_launched(what);
+}
+
+template <typename T, bool GRAD, bool VEC>
+tide_status_t launch_shape(const Args<T> &a, const Shape &s, const char *what, cudaStream_t st)
+{
+    constexpr int U = 8 / int(sizeof(T)) / (GRAD ? 2 : 1), kBytes = VEC ? 64 : 0;
+    const int threads = s.warps * s.groups * 32;
+    if constexpr (GRAD) {
+        return threads <= 256   ? launch_ring<backward_kernel<T, VEC, U, 256, 2>>(a, s, kBytes, what, st)
+               : threads <= 320 ? launch_ring<backward_kernel<T, VEC, U, 320, 2>>(a, s, kBytes, what, st)
+               : threads <= 512 ? launch_ring<backward_kernel<T, VEC, U, 512, 1>>(a, s, kBytes, what, st)
+                                : launch_ring<backward_kernel<T, VEC, U, 1024, 1>>(a, s, kBytes, what, st);
+    } else {
+        return threads <= 256   ? launch_ring<forward_kernel<T, VEC, U, 256, 3>>(a, s, kBytes, what, st)
+               : threads <= 320 ? launch_ring<forward_kernel<T, VEC, U, 320, 2>>(a, s, kBytes, what, st)
+               : threads <= 512 ? launch_ring<forward_kernel<T, VEC, U, 512, 1>>(a, s, kBytes, what, st)
+                                : launch_ring<forward_kernel<T, VEC, U, 1024, 1>>(a, s, kBytes, what, st);
+    }
+}
+
+template <typename T, bool GRAD>
+tide_status_t launch(const Args<T> &a, const Shape &s, const char *what, cudaStream_t st)
+{
+    if (s.wide) {
+        wide_kernel<T, GRAD><<<unsigned(s.blocks), 1024, 0, st>>>(a);
+        return tide::op_launched(what);
+    }
+    return s.vec ? launch_shape<T, GRAD, true>(a, s, what, st) : launch_shape<T, GRAD, false>(a, s, what, st);
 }
 
 template <typename T>
 tide_status_t backward(const tide_norm_t *n, const Args<T> &a, const Shape &s, void *dw, void *db, cudaStream_t st)
 {
-    if (n->rows) {
-        launch<T, true>(a, s, st);
-        if (const tide_status_t e = tide::op_launched("layer_norm_grad"))
+    if (n->rows)
+        if (const tide_status_t e = launch<T, true>(a, s, "layer_norm_grad", st))
             return e;
-    }
     if (!dw && !db)
         return TIDE_OK;
     weight_grad_kernel<T><<<dim3(unsigned((n->cols + 31) / 32), 2), 1024, 0, st>>>(
@@ -518,10 +613,8 @@ tide_status_t tide_layer_norm(const tide_norm_t *norm, const void *x, int64_t x_
                      rows_aligned(y, y_stride, norm->rows, e) && op_aligned(norm->weight, 16) && op_aligned(norm->bias, 16);
     const Shape shape = shape_of(norm, false, vec);
     if (norm->dtype == TIDE_DTYPE_F32)
-        launch<float, false>(args_of<float>(norm, x, x_stride, y, y_stride), shape, st);
-    else
-        launch<bf16, false>(args_of<bf16>(norm, x, x_stride, y, y_stride), shape, st);
-    return tide::op_launched("layer_norm");
+        return launch<float, false>(args_of<float>(norm, x, x_stride, y, y_stride), shape, "layer_norm", st);
+    return launch<bf16, false>(args_of<bf16>(norm, x, x_stride, y, y_stride), shape, "layer_norm", st);
 }
 
 int64_t tide_layer_norm_grad_workspace(const tide_norm_t *norm)
