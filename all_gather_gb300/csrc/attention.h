@@ -221,21 +221,6 @@ inline uint64_t wait_of(const tide_attention_t *at)
     return at->debug & TIDE_DEBUG_SHORT_WAIT ? kShortWaitBudgetNs : kWaitBudgetNs;
 }
 
-// Reads and clears a device flag (synchronises the stream).
-inline cudaError_t take_flag(const int &flag, int *seen, cudaStream_t st)
-{
-    cudaError_t e = cudaMemcpyFromSymbolAsync(seen, flag, sizeof *seen, 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess)
-        e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && *seen) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(flag, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess)
-            e = cudaStreamSynchronize(st);
-    }
-    return e;
-}
-
 // Reads and clears whether a bounded wait ran out (attention.cu, attention_grad.cu).
 cudaError_t forward_timed_out(int *seen, cudaStream_t st);
 cudaError_t grad_timed_out(int *seen, cudaStream_t st);

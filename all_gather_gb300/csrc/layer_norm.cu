@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "ops_internal.h"
+#include "umma.h"
 
 namespace {
 
@@ -27,8 +28,15 @@ using tide::op_aligned;
 using tide::op_fail;
 using bf16 = __nv_bfloat16;
 
+using tide::umma::add2;
+using tide::umma::fma2;
+using tide::umma::mul2;
+
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxWarps = 32;  // of a row
+
+// Set when a bounded wait runs out.
+__device__ int g_timed_out;
 
 template <typename T>
 struct Args {
@@ -58,8 +66,23 @@ struct Raw {
     uint4 v[sizeof(T) / 2];
 };
 
-__device__ __forceinline__ void unpack(const Raw<bf16> &raw, float *f);
-__device__ __forceinline__ void unpack(const Raw<float> &raw, float *f);
+// As pairs of fp32, two of which an instruction takes at a time.
+__device__ __forceinline__ void unpack(const Raw<bf16> &raw, float2 *f)
+{
+    const uint32_t w[4] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<float> &raw, float2 *f)
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        f[2 * k] = make_float2(__uint_as_float(raw.v[k].x), __uint_as_float(raw.v[k].y));
+        f[2 * k + 1] = make_float2(__uint_as_float(raw.v[k].z), __uint_as_float(raw.v[k].w));
+    }
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Unit u of a thread, from memory.
 template <typename T, bool VEC>
@@ -90,87 +113,95 @@ __device__ __forceinline__ Raw<T> load_unit(const T *p, int cols, int u, int t, 
 constexpr int kStages = 3;
 template <typename T, bool VEC, int U, int TENSORS>
 struct Stream {
-    static constexpr int kPieces = sizeof(T) / 2;                  // of 16 bytes a unit
-    static constexpr int kStage = TENSORS * U * kPieces * 16;      // bytes a thread
-    uint32_t at;                                                   // of the thread's first piece
-    int pitch;                                                     // between pieces
-    int stage;
+    static constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes a unit
+    int cols, t, n;
+    const T *next[TENSORS];   // of the next row to fetch
+    int64_t advance[TENSORS];
+    int left;                 // rows to fetch
+    uint32_t at, to, end, pitch, stage;  // the thread's pieces in shared memory: next to take, to fetch, behind the ring
 
-    __device__ __forceinline__ Stream(uint32_t smem) : at(smem + threadIdx.x * 16), pitch(int(blockDim.x) * 16), stage(0) {}
-    __device__ __forceinline__ void fetch(const T *const (&rows)[TENSORS], bool some, int ahead, int cols, int t, int n)
+    // Rows `step` apart from `first` on, of `rows`.
+    __device__ __forceinline__ Stream(uint32_t smem, const T *const (&p)[TENSORS], const int64_t (&stride)[TENSORS], int64_t first,
+                                      int64_t step, int64_t rows, int cols, int t, int n)
+        : cols(cols), t(t), n(n), left(first < rows ? int((rows - first + step - 1) / step) : 0), at(smem + threadIdx.x * 16),
+          pitch(blockDim.x * 16)
+    {
+        stage = TENSORS * U * kPieces * pitch;
+        to = at, end = at + kStages * stage;
+#pragma unroll
+        for (int k = 0; k < TENSORS; ++k) {
+            next[k] = p[k] + first * stride[k] + (VEC ? 8 * t : 0);
+            advance[k] = step * stride[k];
+        }
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            fetch();
+    }
+    __device__ __forceinline__ bool has(int u) const { return 8 * (u * n + t) < cols; }
+    __device__ __forceinline__ void fetch()
     {
         if (!VEC)
             return;
-        const uint32_t to = at + uint32_t((stage + ahead) % kStages) * TENSORS * U * kPieces * pitch;
-        if (some) {
+        if (left > 0) {
+            --left;
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k)
+            for (int k = 0; k < TENSORS; ++k) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int c = column<VEC>(u, 0, t, n);
-                    if (c < cols)
+                for (int u = 0; u < U; ++u)
+                    if (has(u))
 #pragma unroll
                         for (int i = 0; i < kPieces; ++i)
                             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                             to + uint32_t((k * U + u) * kPieces + i) * pitch),
-                                         "l"(reinterpret_cast<const uint4 *>(rows[k] + c) + i)
+                                             to + ((k * U + u) * kPieces + i) * pitch),
+                                         "l"(next[k] + u * 8 * n + i * (16 / sizeof(T)))
                                          : "memory");
-                }
+                next[k] += advance[k];
+            }
+            to = to + stage == end ? end - kStages * stage : to + stage;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // The current row's units as fp32; what lies behind its end is 0.
-    __device__ __forceinline__ void take(const T *const (&rows)[TENSORS], int cols, int t, int n, float (&f)[TENSORS][U][8])
+    // The next row's units as fp32; what lies behind its end is 0.
+    __device__ __forceinline__ void take(float2 (&f)[TENSORS][U][4])
     {
         if (VEC)
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint32_t from = at + uint32_t(stage) * TENSORS * U * kPieces * pitch;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
 #pragma unroll
-        for (int k = 0; k < TENSORS; ++k)
+        for (int k = 0; k < TENSORS; ++k) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 Raw<T> raw;
-                if (VEC) {
-                    const bool in = column<VEC>(u, 0, t, n) < cols;
+                if (!VEC) {
+                    raw = load_unit<T, VEC>(next[k], cols, u, t, n);
+                } else if (has(u)) {
 #pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        uint4 &v = raw.v[i];
+                    for (int i = 0; i < kPieces; ++i)
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(from + uint32_t((k * U + u) * kPieces + i) * pitch)
+                                     : "=r"(raw.v[i].x), "=r"(raw.v[i].y), "=r"(raw.v[i].z), "=r"(raw.v[i].w)
+                                     : "r"(at + ((k * U + u) * kPieces + i) * pitch)
                                      : "memory");
-                        if (!in)
-                            v = make_uint4(0, 0, 0, 0);
-                    }
                 } else {
-                    raw = load_unit<T, VEC>(rows[k], cols, u, t, n);
+                    raw = {};
                 }
                 unpack(raw, f[k][u]);
             }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+            if (!VEC)
+                next[k] += advance[k];
+        }
+        if (VEC) {
+            at = at + stage == end ? end - kStages * stage : at + stage;
+            fetch();  // into the place that was taken from a row ago
+        }
     }
 };
 
-__device__ __forceinline__ void unpack(const Raw<bf16> &raw, float *f)
-{
-    const uint32_t w[4] = {raw.v[0].x, raw.v[0].y, raw.v[0].z, raw.v[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void unpack(const Raw<float> &raw, float *f)
-{
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        f[4 * k] = __uint_as_float(raw.v[k].x), f[4 * k + 1] = __uint_as_float(raw.v[k].y);
-        f[4 * k + 2] = __uint_as_float(raw.v[k].z), f[4 * k + 3] = __uint_as_float(raw.v[k].w);
-    }
-}
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_unit(T *p, int cols, int u, int t, int n, const float *f)
+__device__ __forceinline__ void store_unit(T *p, int cols, int u, int t, int n, const float2 *pairs)
 {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[2 * i] = pairs[i].x, f[2 * i + 1] = pairs[i].y;
     if (VEC) {
         const int c = column<VEC>(u, 0, t, n);
         if (c < cols)
@@ -185,6 +216,20 @@ __device__ __forceinline__ void store_unit(T *p, int cols, int u, int t, int n, 
     }
 }
 
+// Sums over a warp of four values at once: lanes give half of their values away for the other half of a neighbour's,
+// twice, which makes six exchanges, not five a value.  Value k ends up in lanes 8 k to 8 k + 7.
+__device__ __forceinline__ float fold4(const float (&v)[4], int lane)
+{
+    const bool upper = lane & 16, odd = lane & 8;
+    const float a = (upper ? v[2] : v[0]) + __shfl_xor_sync(kAll, upper ? v[0] : v[2], 16);
+    const float b = (upper ? v[3] : v[1]) + __shfl_xor_sync(kAll, upper ? v[1] : v[3], 16);
+    float one = (odd ? b : a) + __shfl_xor_sync(kAll, odd ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o /= 2)
+        one += __shfl_xor_sync(kAll, one, o);
+    return one;
+}
+
 // A group: `warps` warps of the block that work on one row.
 struct Group {
     int warps, index, t, n;  // its number in the block; the thread's number in it, of n
@@ -192,29 +237,44 @@ struct Group {
 
     // Sums over the group, to all of its threads.  Two buffers in turn: who writes one again has met all
     // others at the barrier that follows their reading of it.
-    template <int K>
+    template <int K>  // 1, or up to 4
     __device__ __forceinline__ void sum(float (&s)[K], int turn) const
     {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
+        const int lane = t & 31;
+        float one;
+        if (K == 1) {
+            one = s[0];
 #pragma unroll
             for (int o = 16; o > 0; o /= 2)
-                s[k] += __shfl_xor_sync(kAll, s[k], o);
-        if (warps == 1)
+                one += __shfl_xor_sync(kAll, one, o);
+        } else {
+            const float v[4] = {s[0], s[1], K > 2 ? s[2] : 0.f, K > 3 ? s[3] : 0.f};
+            one = fold4(v, lane);
+        }
+        if (warps == 1) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                s[k] = __shfl_sync(kAll, one, 8 * k);
             return;
+        }
         float *buf = shared + turn * warps * 4;
-        if (t % 32 == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                buf[t / 32 * 4 + k] = s[k];
+        if (lane % 8 == 0 && lane < 8 * K)
+            buf[t / 32 * 4 + lane / 8] = one;
         asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(n) : "memory");
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            s[k] = buf[k];
-        for (int w = 1; w < warps; ++w)
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                s[k] += buf[w * 4 + k];
+        const float4 *all = reinterpret_cast<const float4 *>(buf);
+        float2 lo = both(0.f), hi = both(0.f);
+#pragma unroll 4
+        for (int w = 0; w < warps; ++w) {
+            const float4 v = all[w];
+            lo = add2(lo, make_float2(v.x, v.y));
+            if (K > 2)
+                hi = add2(hi, make_float2(v.z, v.w));
+        }
+        s[0] = lo.x;
+        if (K > 1)
+            s[1] = lo.y;
+        if (K > 2)
+            s[2] = hi.x;
     }
 };
 
@@ -224,64 +284,74 @@ __device__ __forceinline__ Group group_of(int warps, float *shared)
     return {warps, index, int(threadIdx.x) % n, n, shared + index * warps * 8};
 }
 
+// Pair i of unit u less the mean, and 0 where it lies behind the row's end.
+template <bool VEC>
+__device__ __forceinline__ float2 centered(float2 f, float2 less, int u, int i, int cols, int t, int n)
+{
+    f = add2(f, less);
+    if (VEC)  // whole units are looked at elsewhere
+        return f;
+    return make_float2(column<VEC>(u, 2 * i, t, n) < cols ? f.x : 0.f, column<VEC>(u, 2 * i + 1, t, n) < cols ? f.y : 0.f);
+}
+
 // THREADS: of a block at most, with BLOCKS of them on an SM.
 template <typename T, bool VEC, int U, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) forward_kernel(Args<T> a, int warps)
 {
     extern __shared__ uint4 ring[];
-    __shared__ float shared[kMaxWarps * 8];
+    __shared__ alignas(16) float shared[kMaxWarps * 8];
     const Group g = group_of(warps, shared);
     const int64_t step = int64_t(gridDim.x) * (blockDim.x / g.n);
     const float inv = 1.f / float(a.cols);
-    Stream<T, VEC, U, 1> in(uint32_t(__cvta_generic_to_shared(ring)));
     int64_t row = int64_t(blockIdx.x) * (blockDim.x / g.n) + g.index;
-    auto fetch = [&](int64_t r, int ahead) {
-        const T *const rows[1] = {a.x + r * a.xs};
-        in.fetch(rows, r < a.rows, ahead, a.cols, g.t, g.n);
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-        fetch(row + i * step, i);
-    for (; row < a.rows; row += step) {
-        fetch(row + (kStages - 1) * step, kStages - 1);
-        float x[1][U][8], mean[1] = {0.f}, var[1] = {0.f};
-        const T *const rows[1] = {a.x + row * a.xs};
-        in.take(rows, a.cols, g.t, g.n, x);
+    Stream<T, VEC, U, 1> in(uint32_t(__cvta_generic_to_shared(ring)), {a.x}, {a.xs}, row, step, a.rows, a.cols, g.t, g.n);
+    T *out = a.out + row * a.outs;
+    for (; row < a.rows; row += step, out += step * a.outs) {
+        float2 x[1][U][4];
+        float mean[1], var[1];
+        in.take(x);
         auto &f = x[0];
+        float2 sum = both(0.f), less = both(0.f);
         if (a.center) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mean[0] += f[u][i];
+                for (int i = 0; i < 4; ++i)
+                    sum = add2(sum, f[u][i]);
+            mean[0] = sum.x + sum.y;
             g.sum(mean, 0);
-            mean[0] *= inv;
+            less = both(-mean[0] * inv);
+            sum = both(0.f);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            if (VEC && !in.has(u))
+                continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[u][i] -= mean[0];
-                if (column<VEC>(u, VEC ? 0 : i, g.t, g.n) < a.cols)
-                    var[0] = fmaf(f[u][i], f[u][i], var[0]);
+            for (int i = 0; i < 4; ++i) {
+                f[u][i] = centered<VEC>(f[u][i], less, u, i, a.cols, g.t, g.n);
+                sum = fma2(f[u][i], f[u][i], sum);
             }
+        }
+        var[0] = sum.x + sum.y;
         g.sum(var, 1);
-        const float r = 1.f / sqrtf(fmaf(var[0], inv, a.eps));
-        T *out = a.out + row * a.outs;
+        const float2 r = both(rsqrtf(fmaf(var[0], inv, a.eps)));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float k[8], s[8];
+            if (VEC && !in.has(u))
+                continue;
+            float2 k[4], s[4];
             if (a.w)
                 unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
             if (a.b)
                 unpack(load_unit<T, VEC>(a.b, a.cols, u, g.t, g.n), s);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[u][i] *= r;
+            for (int i = 0; i < 4; ++i) {
+                f[u][i] = mul2(f[u][i], r);
                 if (a.w)
-                    f[u][i] = a.b ? fmaf(f[u][i], k[i], s[i]) : f[u][i] * k[i];
+                    f[u][i] = a.b ? fma2(f[u][i], k[i], s[i]) : mul2(f[u][i], k[i]);
                 else if (a.b)
-                    f[u][i] += s[i];
+                    f[u][i] = add2(f[u][i], s[i]);
             }
             store_unit<T, VEC>(out, a.cols, u, g.t, g.n, f[u]);
         }
@@ -292,67 +362,66 @@ template <typename T, bool VEC, int U, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) backward_kernel(Args<T> a, int warps)
 {
     extern __shared__ uint4 ring[];
-    __shared__ float shared[kMaxWarps * 8];
+    __shared__ alignas(16) float shared[kMaxWarps * 8];
     const Group g = group_of(warps, shared);
     const int groups = blockDim.x / g.n;
     const int64_t step = int64_t(gridDim.x) * groups;
     const float inv = 1.f / float(a.cols);
-    Stream<T, VEC, U, 2> in(uint32_t(__cvta_generic_to_shared(ring)));
-    float dw[U][8] = {}, db[U][8] = {};
+    float2 dw[U][4] = {}, db[U][4] = {};
     const int64_t first = int64_t(blockIdx.x) * groups + g.index;
-    auto fetch = [&](int64_t r, int ahead) {
-        const T *const rows[2] = {a.x + r * a.xs, a.dy + r * a.dys};
-        in.fetch(rows, r < a.rows, ahead, a.cols, g.t, g.n);
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-        fetch(first + i * step, i);
-    for (int64_t row = first; row < a.rows; row += step) {
-        fetch(row + (kStages - 1) * step, kStages - 1);
-        float both[2][U][8], mean[1] = {0.f}, s[3] = {0.f, 0.f, 0.f};
-        const T *const rows[2] = {a.x + row * a.xs, a.dy + row * a.dys};
-        in.take(rows, a.cols, g.t, g.n, both);
-        auto &f = both[0], &d = both[1];
+    Stream<T, VEC, U, 2> in(uint32_t(__cvta_generic_to_shared(ring)), {a.x, a.dy}, {a.xs, a.dys}, first, step, a.rows, a.cols,
+                            g.t, g.n);
+    T *out = a.out + first * a.outs;
+    for (int64_t row = first; row < a.rows; row += step, out += step * a.outs) {
+        float2 in_row[2][U][4];
+        float mean[1], s[3];
+        in.take(in_row);
+        auto &f = in_row[0], &d = in_row[1];
+        float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f), less = both(0.f);
         if (a.center) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mean[0] += f[u][i];
+                for (int i = 0; i < 4; ++i)
+                    s0 = add2(s0, f[u][i]);
+            mean[0] = s0.x + s0.y;
             g.sum(mean, 0);
-            mean[0] *= inv;
+            less = both(-mean[0] * inv);
+            s0 = both(0.f);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float k[8];
+            if (VEC && !in.has(u))
+                continue;
+            float2 k[4];
             if (a.w)
                 unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (column<VEC>(u, VEC ? 0 : i, g.t, g.n) >= a.cols)
-                    continue;
-                f[u][i] -= mean[0];
-                const float gi = a.w ? d[u][i] * k[i] : d[u][i];
-                s[0] = fmaf(f[u][i], f[u][i], s[0]);
-                s[1] += gi;
-                s[2] = fmaf(gi, f[u][i], s[2]);
+            for (int i = 0; i < 4; ++i) {
+                f[u][i] = centered<VEC>(f[u][i], less, u, i, a.cols, g.t, g.n);
+                const float2 gi = a.w ? mul2(d[u][i], k[i]) : d[u][i];
+                s0 = fma2(f[u][i], f[u][i], s0);
+                s1 = add2(s1, gi);
+                s2 = fma2(gi, f[u][i], s2);
             }
         }
+        s[0] = s0.x + s0.y, s[1] = s1.x + s1.y, s[2] = s2.x + s2.y;
         g.sum(s, 1);
-        const float r = 1.f / sqrtf(fmaf(s[0], inv, a.eps));
-        const float along = s[2] * r * inv, level = a.center ? s[1] * inv : 0.f;
-        T *out = a.out + row * a.outs;
+        const float r = rsqrtf(fmaf(s[0], inv, a.eps));
+        const float2 rr = both(r), along = both(-(s[2] * r * inv)), level = both(a.center ? -(s[1] * inv) : 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float k[8], y[8];
+            if (VEC && !in.has(u))
+                continue;
+            float2 k[4], y[4];
             if (a.w)
                 unpack(load_unit<T, VEC>(a.w, a.cols, u, g.t, g.n), k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float n = f[u][i] * r, gi = a.w ? d[u][i] * k[i] : d[u][i];
-                y[i] = r * (fmaf(-n, along, gi) - level);
-                dw[u][i] = fmaf(d[u][i], n, dw[u][i]);
-                db[u][i] += d[u][i];
+            for (int i = 0; i < 4; ++i) {
+                const float2 n = mul2(f[u][i], rr), gi = a.w ? mul2(d[u][i], k[i]) : d[u][i];
+                y[i] = mul2(rr, add2(fma2(n, along, gi), level));
+                dw[u][i] = fma2(d[u][i], n, dw[u][i]);
+                db[u][i] = add2(db[u][i], d[u][i]);
             }
             store_unit<T, VEC>(out, a.cols, u, g.t, g.n, y);
         }
@@ -367,10 +436,188 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) backward_kernel(Args<T> a, in
             const int c = column<VEC>(u, i, g.t, g.n);
             if (c < a.cols) {
                 if (a.w)
-                    p[c] = dw[u][i];
+                    p[c] = i % 2 ? dw[u][i / 2].y : dw[u][i / 2].x;
                 if (a.b)
-                    p[a.cols + c] = db[u][i];
+                    p[a.cols + c] = i % 2 ? db[u][i / 2].y : db[u][i / 2].x;
             }
+        }
+}
+
+// ---------------------------------------------------------------- gradient of tiles of rows
+
+// Sums over a warp, to all of its lanes.
+__device__ __forceinline__ float warp_sum(float s)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        s += __shfl_xor_sync(kAll, s, o);
+    return s;
+}
+
+// `rows` rows of x and dy in shared memory at a time, the next ones on their
+// way as bulk copies.  A thread has the same V units of every row, with their
+// dw and db in registers.  It goes over the tile twice: for the sums, each warp
+// around the mean of its own part of the row, which are then joined around the
+// row's mean, and for dx.  Three meetings of the block for a tile, where a
+// group of warps has two for every row.
+template <typename T, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int rows, uint64_t wait_ns)
+{
+    namespace um = tide::umma;
+    constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes a unit
+    extern __shared__ uint4 smem[];
+    __shared__ uint64_t arrived[2];
+    __shared__ volatile int gave_up;
+    const int n = blockDim.x, t = threadIdx.x, warp = t / 32, lane = t % 32, units = a.cols / 8;
+    const int row_pieces = units * kPieces, tile_pieces = rows * 2 * row_pieces;
+    float4 *parts = reinterpret_cast<float4 *>(smem + 2 * tile_pieces), *stats = parts + rows * (n / 32);  // of every row: [warps], and joined
+    const int64_t tiles = (a.rows + rows - 1) / rows;
+    const float inv = 1.f / float(a.cols);
+    float2 dw[V][4] = {}, db[V][4] = {}, k[V][4];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (a.w && t + v * n < units)
+            unpack(load_unit<T, true>(a.w, a.cols, v, t, n), k[v]);
+    // elements that a warp has of a row: this one, and the one whose number is the lane's
+    auto count_of = [&](int w) {
+        int c = 0;
+        for (int v = 0; v < V; ++v)
+            c += max(0, min(32, units - (v * n + w * 32)));
+        return float(8 * c);
+    };
+    const float part_inv = 1.f / fmaxf(count_of(warp), 1.f), lane_count = lane < n / 32 ? count_of(lane) : 0.f;
+    if (t == 0) {
+        um::mbar_init(um::smem_addr(&arrived[0]), 1);
+        um::mbar_init(um::smem_addr(&arrived[1]), 1);
+        um::fence_barrier_init();
+        gave_up = 0;
+    }
+    __syncthreads();
+
+    auto load = [&](int64_t tile, int buf) {  // by the first warp
+        const int count = int(min(int64_t(rows), a.rows - tile * rows));
+        const uint32_t bar = um::smem_addr(&arrived[buf]), to = um::smem_addr(smem + buf * tile_pieces);
+        if (lane == 0)
+            um::mbar_expect(bar, uint32_t(count * 2 * row_pieces * 16));
+        __syncwarp();
+        for (int i = lane; i < count * 2; i += 32) {
+            const int64_t row = tile * rows + i / 2;
+            um::bulk_load(to + uint32_t(i * row_pieces) * 16, i % 2 ? a.dy + row * a.dys : a.x + row * a.xs,
+                          uint32_t(row_pieces * 16), bar);
+        }
+    };
+    auto unit = [&](const uint4 *row, int u, float2 (&f)[4]) {
+        Raw<T> raw;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            raw.v[i] = row[u * kPieces + i];
+        unpack(raw, f);
+    };
+
+    int buf = 0, phase = 0;
+    if (warp == 0 && blockIdx.x < tiles)
+        load(blockIdx.x, 0);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        __syncthreads();
+        if (warp == 0 && tile + gridDim.x < tiles)
+            load(tile + gridDim.x, buf ^ 1);
+        const int count = int(min(int64_t(rows), a.rows - tile * rows));
+        const bool here = um::mbar_wait(um::smem_addr(&arrived[buf]), phase, &gave_up, wait_ns);
+        const uint4 *base = smem + buf * tile_pieces;
+#pragma unroll 2
+        for (int r = 0; r < count; ++r) {
+            const uint4 *x = base + r * 2 * row_pieces, *dy = x + row_pieces;
+            float2 f[V][4], d[4], s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
+            float mean = 0.f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (t + v * n < units) {
+                    unit(x, t + v * n, f[v]);
+                    s0 = add2(s0, add2(add2(f[v][0], f[v][1]), add2(f[v][2], f[v][3])));
+                }
+            if (a.center) {
+                mean = warp_sum(s0.x + s0.y) * part_inv;
+            }
+            s0 = both(0.f);
+            const float2 less = both(-mean);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (t + v * n < units) {
+                    unit(dy, t + v * n, d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        f[v][e] = add2(f[v][e], less);
+                        if (a.w)
+                            d[e] = mul2(d[e], k[v][e]);
+                        s0 = fma2(f[v][e], f[v][e], s0);
+                        s1 = add2(s1, d[e]);
+                        s2 = fma2(f[v][e], d[e], s2);
+                    }
+                }
+            const float q[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, 0.f};
+            const float one = fold4(q, lane);  // value m in lanes 8 m to 8 m + 7
+            float *part = reinterpret_cast<float *>(parts + r * (n / 32) + warp);
+            if (lane % 8 == 0)
+                part[lane / 8] = lane == 24 ? mean : one;
+        }
+        __syncthreads();
+        for (int r = warp; r < count; r += n / 32) {  // a warp's part a lane, around the row's mean
+            const float4 p = lane < n / 32 ? parts[r * (n / 32) + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float mean = a.center ? warp_sum(p.w * lane_count) * inv : 0.f, off = p.w - mean;
+            const float q[4] = {fmaf(off * off, lane_count, p.x), p.y, fmaf(p.y, off, p.z), 0.f};
+            const float one = fold4(q, lane);
+            const float f = rsqrtf(fmaf(__shfl_sync(kAll, one, 0), inv, a.eps));
+            const float s1 = __shfl_sync(kAll, one, 8), s2 = __shfl_sync(kAll, one, 16);
+            if (lane == 0)  // dx = f (g - mean(g) - n mean(g n)), n = (x - mean) f
+                stats[r] = make_float4(here ? f : __int_as_float(0x7fffffff), -mean, a.center ? -s1 * inv : 0.f,
+                                       -(s2 * f * inv));
+        }
+        __syncthreads();
+        for (int r = 0; r < count; ++r) {
+            const uint4 *x = base + r * 2 * row_pieces, *dy = x + row_pieces;
+            const float4 st = stats[r];
+            const float2 f = both(st.x), less = both(st.y), level = both(st.z), along = both(st.w);
+            T *out = a.out + (tile * rows + r) * a.outs;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int u = t + v * n;
+                if (u >= units)
+                    continue;
+                float2 c[4], d[4], y[4];
+                unit(x, u, c);
+                unit(dy, u, d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 norm = mul2(add2(c[e], less), f), gi = a.w ? mul2(d[e], k[v][e]) : d[e];
+                    y[e] = mul2(f, add2(fma2(norm, along, gi), level));
+                    dw[v][e] = fma2(d[e], norm, dw[v][e]);
+                    db[v][e] = add2(db[v][e], d[e]);
+                }
+                store_unit<T, true>(out, a.cols, v, t, n, y);
+            }
+        }
+        if (buf ^= 1, buf == 0)
+            phase ^= 1;
+    }
+    if (gave_up) {  // what the wait kept from coming is NaN
+        if (t == 0)
+            g_timed_out = 1;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                dw[v][e] = db[v][e] = both(__int_as_float(0x7fffffff));
+    }
+    if (!a.partial)
+        return;
+    float *p = a.partial + int64_t(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (t + v * n < units) {
+            if (a.w)
+                store_unit<float, true>(p, a.cols, v, t, n, dw[v]);
+            if (a.b)
+                store_unit<float, true>(p + a.cols, a.cols, v, t, n, db[v]);
         }
 }
 
@@ -414,7 +661,7 @@ __global__ void __launch_bounds__(1024) wide_kernel(Args<T> a)
                 s2 = fmaf(gi, f, s2);
             }
         }
-        const float r = 1.f / sqrtf(fmaf(block_sum(s0, shared), inv, a.eps));
+        const float r = rsqrtf(fmaf(block_sum(s0, shared), inv, a.eps));
         float along = 0.f, level = 0.f;
         if (GRAD) {
             level = a.center ? block_sum(s1, shared) * inv : 0.f;
@@ -500,27 +747,55 @@ tide_status_t check_rows(const tide_norm_t *n, const void *p, int64_t stride, bo
     return TIDE_OK;
 }
 
-// How rows are shared out: units a thread, warps a row, rows a block, blocks.
+// How rows are shared out.
+enum Kind { kGroup, kTiles, kWide };
 struct Shape {
-    bool wide, vec;
-    int units, warps, groups, blocks;
+    Kind kind;
+    bool vec;
+    int warps, groups, blocks;       // kGroup: of a row; rows a block
+    int units, rows, smem;           // kTiles: units a thread, rows of a tile
+    int shares() const { return kind == kGroup ? blocks * groups : blocks; }
 };
 
-// A thread has 64 bytes of a row of one tensor, 32 of one of two.
+constexpr int kTileSmem = 224 * 1024;
+
+int64_t sms() { return std::max(tide::op_sm_count(), 1); }
+
+// Tiles of rows for the gradient of rows on 16-byte boundaries, from 1,024 columns on (32 warps' worth of units; below, a
+// group of warps is as fast), as long as the threads have
+// registers for the sums and two tiles fit into shared memory.
+bool tile_shape(const tide_norm_t *n, Shape &s)
+{
+    const int64_t bytes = 2 * n->cols * (n->dtype == TIDE_DTYPE_F32 ? 4 : 2), units = n->cols / 8;
+    const int64_t rows = std::min<int64_t>(8, (kTileSmem - 8 * 33 * 16) / 2 / bytes);
+    if (n->cols < 1024 || n->cols > 16384 || n->cols % 8 || rows < 1)
+        return false;
+    s.kind = kTiles;
+    s.units = units <= 640 ? 1 : units <= 1024 ? 2 : 4;
+    s.warps = int((units + 32 * s.units - 1) / (32 * s.units));
+    s.groups = 1;
+    s.rows = int(std::min(rows, std::max<int64_t>(1, n->rows / sms())));  // few rows: on all SMs
+    s.smem = int(2 * s.rows * bytes + s.rows * (s.warps + 1) * 16);
+    s.blocks = int(std::max<int64_t>(1, std::min((n->rows + s.rows - 1) / s.rows, sms())));
+    return s.smem <= kTileSmem;
+}
+
+// A thread has 64 bytes of a row, or 32 of one of x and dy each.
 Shape shape_of(const tide_norm_t *n, bool grad, bool vec)
 {
     Shape s = {};
     s.vec = vec;
-    s.units = (n->dtype == TIDE_DTYPE_F32 ? 2 : 4) / (grad ? 2 : 1);
-    s.warps = int((n->cols + 256 * s.units - 1) / (256 * s.units));
-    s.wide = s.warps > kMaxWarps;
-    if (s.wide)
+    if (grad && vec && tile_shape(n, s))
+        return s;
+    const int units = (n->dtype == TIDE_DTYPE_F32 ? 2 : 4) / (grad ? 2 : 1);
+    s.warps = int((n->cols + 256 * units - 1) / (256 * units));
+    s.kind = s.warps > kMaxWarps ? kWide : kGroup;
+    if (s.kind == kWide)
         s.warps = kMaxWarps;
     s.groups = std::max(1, 8 / s.warps);
     const int threads = s.warps * s.groups * 32;
     const int per_sm = threads <= 256 ? grad ? 2 : 3 : threads <= 320 ? 2 : 1;
-    s.blocks = int(std::max<int64_t>(1, std::min<int64_t>((n->rows + s.groups - 1) / s.groups,
-                                                          int64_t(std::max(tide::op_sm_count(), 1)) * per_sm)));
+    s.blocks = int(std::max<int64_t>(1, std::min((n->rows + s.groups - 1) / s.groups, sms() * per_sm)));
     return s;
 }
 
@@ -568,13 +843,27 @@ tide_status_t launch_shape(const Args<T> &a, const Shape &s, const char *what, c
     }
 }
 
+template <auto KERNEL, typename T>
+tide_status_t launch_tiles(const Args<T> &a, const Shape &s, const char *what, cudaStream_t st)
+{
+    const cudaError_t e = tide::op_allow_smem<KERNEL>(kTileSmem);
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    KERNEL<<<unsigned(s.blocks), unsigned(s.warps * 32), s.smem, st>>>(a, s.rows, tide::kWaitBudgetNs);
+    return tide::op_launched(what);
+}
+
 template <typename T, bool GRAD>
 tide_status_t launch(const Args<T> &a, const Shape &s, const char *what, cudaStream_t st)
 {
-    if (s.wide) {
+    if (s.kind == kWide) {
         wide_kernel<T, GRAD><<<unsigned(s.blocks), 1024, 0, st>>>(a);
         return tide::op_launched(what);
     }
+    if (s.kind == kTiles)
+        return s.units == 1   ? launch_tiles<tile_grad_kernel<T, 1, 640>>(a, s, what, st)
+               : s.units == 2 ? launch_tiles<tile_grad_kernel<T, 2, 512>>(a, s, what, st)
+                              : launch_tiles<tile_grad_kernel<T, 4, 512>>(a, s, what, st);
     return s.vec ? launch_shape<T, GRAD, true>(a, s, what, st) : launch_shape<T, GRAD, false>(a, s, what, st);
 }
 
@@ -587,11 +876,13 @@ tide_status_t backward(const tide_norm_t *n, const Args<T> &a, const Shape &s, v
     if (!dw && !db)
         return TIDE_OK;
     weight_grad_kernel<T><<<dim3(unsigned((n->cols + 31) / 32), 2), 1024, 0, st>>>(
-        a.partial, n->rows ? s.blocks * (s.wide ? 1 : s.groups) : 0, a.cols, static_cast<T *>(dw), static_cast<T *>(db));
+        a.partial, n->rows ? s.shares() : 0, a.cols, static_cast<T *>(dw), static_cast<T *>(db));
     return tide::op_launched("layer_norm_grad: weight");
 }
 
 }  // namespace
+
+cudaError_t tide::norm_timed_out(int *seen, cudaStream_t st) { return take_flag(g_timed_out, seen, st); }
 
 extern "C" {
 
@@ -624,8 +915,9 @@ int64_t tide_layer_norm_grad_workspace(const tide_norm_t *norm)
         return -1;
     if (!norm->weight && !norm->bias)
         return 0;
-    const Shape s = shape_of(norm, true, false);
-    return std::max<int64_t>(256, int64_t(s.blocks) * s.groups * 2 * norm->cols * 4);
+    // what rows will be on is not known here
+    const int shares = std::max(shape_of(norm, true, false).shares(), shape_of(norm, true, true).shares());
+    return std::max<int64_t>(256, int64_t(shares) * 2 * norm->cols * 4);
 }
 
 tide_status_t tide_layer_norm_grad(const tide_norm_t *norm, const void *dy, int64_t dy_stride, const void *x,

@@ -1212,15 +1212,17 @@ tide_status_t tide_ops_device_status(void *stream)
 {
     tide::record_error("");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int seen[3] = {};
-    cudaError_t e = tide::attn::take_flag(g_timed_out, &seen[0], st);
+    int seen[4] = {};
+    cudaError_t e = tide::take_flag(g_timed_out, &seen[0], st);
     if (e == cudaSuccess)
         e = tide::attn::forward_timed_out(&seen[1], st);
     if (e == cudaSuccess)
         e = tide::attn::grad_timed_out(&seen[2], st);
+    if (e == cudaSuccess)
+        e = tide::norm_timed_out(&seen[3], st);
     if (e != cudaSuccess)
         return op_fail(TIDE_ERR_CUDA, "operators' status: %s", cudaGetErrorString(e));
-    return seen[0] || seen[1] || seen[2] ? op_fail(TIDE_ERR_TIMEOUT, "a bounded device-side wait expired") : TIDE_OK;
+    return seen[0] || seen[1] || seen[2] || seen[3] ? op_fail(TIDE_ERR_TIMEOUT, "a bounded device-side wait expired") : TIDE_OK;
 }
 
 }  // extern "C"

@@ -63,6 +63,24 @@ cudaError_t op_allow_smem(int bytes)
     return e;
 }
 
+// Reads and clears a device flag (synchronises the stream).
+inline cudaError_t take_flag(const int &flag, int *seen, cudaStream_t st)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(seen, flag, sizeof *seen, 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && *seen) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(flag, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+        if (e == cudaSuccess)
+            e = cudaStreamSynchronize(st);
+    }
+    return e;
+}
+
+// Reads and clears whether a bounded wait of the layer norm's gradient ran out (layer_norm.cu).
+cudaError_t norm_timed_out(int *seen, cudaStream_t st);
+
 // Sizes are kept below 2^60 elements so that byte offsets fit 64 bits.
 constexpr int64_t kMaxExtent = int64_t(1) << 60;
 inline bool op_extent_ok(int64_t n, int64_t stride)
