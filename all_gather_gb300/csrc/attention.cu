@@ -153,24 +153,22 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     __syncthreads();
     um::fence_after();
     const uint32_t tmem = tmem_slot;  // S of both tiles, 128 columns each, then their O
-    auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait(bar, parity, &gave_up, f.wait_ns); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait_held(bar, parity, &gave_up, f.wait_ns); };
 
     if (warp >= 8) {
         um::fewer_registers<kOtherRegs>();
         if (warp == 8) {
             const bool leader = um::elected();
-            int number = blockIdx.x, slot = 0, turn = 0, stage = 0, phase = 0, taken = 0;
+            int number = blockIdx.x, slot = 0, turn = 0, stage = 0, phase = 0, taken = 0, asks = 0;
             int fills = 0, q_fills[2] = {0, 0};  // copies under way at most: the last of each place
             uint32_t q_phase[2] = {0, 0};
-            bool ok = true;
+            bool ok = true, pending = false;  // pending: an answer is under way
             while (ok) {
                 if (lane == 0) {
                     claims[taken % kClaims] = number;
                     claimed = taken + 1;
                 }
                 ++taken;
-                if (leader)
-                    um::ask_next_block(um::smem_addr(&answer), asked);
                 // which key tiles the rows see: four rows a lane
                 int head, r0;
                 place_of(f, number, head, r0);
@@ -220,8 +218,16 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                             stage = 0, phase ^= 1;
                     }
                 }
-                if (!ok || !(ok = wait(asked, (taken - 1) & 1)))
+                if (!ok)
                     break;
+                // Asked for as late as the copies ahead allow: a block that is at work on a long item must not hold
+                // the next one back from those that come free.
+                if (leader)
+                    um::ask_next_block(um::smem_addr(&answer), asked);
+                pending = true;
+                if (!(ok = wait(asked, asks & 1)))
+                    break;
+                pending = false, ++asks;
                 number = um::next_block(um::smem_addr(&answer));
                 um::fence_copies();
                 __syncwarp();
@@ -235,17 +241,19 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 }
             }
             if (!ok) {
-                // The answer that is under way, and the copies: neither may find the block gone.
+                // An answer that is under way, and the copies: neither may find the block gone.
                 auto land = [&](uint32_t bar, uint32_t parity) {
                     const uint64_t t0 = um::now_ns();
                     while (!um::mbar_try(bar, parity) && um::now_ns() - t0 < f.wait_ns) {
                     }
                 };
-                land(asked, (taken - 1) & 1);
-                const int more = um::next_block(um::smem_addr(&answer));
-                if (lane == 0 && more >= 0 && more != number) {
-                    claims[taken % kClaims] = more;
-                    claimed = taken + 1;
+                if (pending) {
+                    land(asked, asks & 1);
+                    const int more = um::next_block(um::smem_addr(&answer));
+                    if (lane == 0 && more >= 0 && more != number) {
+                        claims[taken % kClaims] = more;
+                        claimed = taken + 1;
+                    }
                 }
                 for (int i = max(0, fills - kStages); i < fills; ++i)
                     land(full + 8 * (i % kStages), (i / kStages) & 1);

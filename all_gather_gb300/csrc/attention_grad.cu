@@ -29,9 +29,12 @@ using tide::op_aligned;
 using tide::op_fail;
 namespace um = tide::umma;
 
-constexpr int kThreads = 384;  // eight warps for the elements, four that fetch, multiply, fetch lse and delta, and idle
-constexpr int kRowRegs = 224, kOtherRegs = 56;  // registers a thread, of 168 at the launch: (2 * 224 + 56) * 128 = 168 * 384
-constexpr int kClaims = 8;     // of a block's last items, kept for a wait that runs out
+constexpr int kWarps = 8;                    // for the elements: a quarter of the rows and a part of the columns each
+constexpr int kGroups = kWarps / 4, kWide = kTile / kGroups;
+constexpr int kThreads = 32 * (kWarps + 4);  // and one that fetches, one that multiplies, one for lse and delta, one idle
+constexpr int kRowRegs = 224, kOtherRegs = 56;  // registers a thread, of 168 at the launch: 256 * 224 + 128 * 56 = 384 * 168
+constexpr int kFetch = kWarps, kMultiply = kWarps + 1, kStats = kWarps + 2;
+constexpr int kClaims = 8;  // of a block's last items, kept for a wait that runs out
 
 // Set when a bounded wait runs out.
 __device__ int g_timed_out;
@@ -42,21 +45,31 @@ struct Backward {
     Heads q, k, v, dout;
     Heads out0, out1;  // keys: dv, dk; rows: -, dq
     const float *lse, *delta;
-    int items;  // tiles times heads
+    int items;        // tiles times heads, times the parts
+    int parts;        // keys: that the query heads of a key head may be shared out to, each with sums of its own
+    const int *parts_of;  // of each tile, if parts > 1
+    float *partial;   // [parts][2: dv, dk][T][Hk][D]
     uint64_t wait_ns;
     int skip_fill;  // TIDE_DEBUG_SKIP_FILL
 };
 
 struct Item {
     int number;  // -1: no more
-    Tiles tiles;  // streamed
+    Tiles tiles;   // streamed
+    int h0, h1;    // query heads
+};
+struct Place {
+    int head, t0, part, parts;  // resident head and first token; part: of parts
 };
 template <bool KEYS>
-__device__ __forceinline__ void place_of(const Backward &f, int item, int &head, int &t0)
+__device__ __forceinline__ Place place_of(const Backward &f, int item)
 {
+    const int part = KEYS ? item % f.parts : 0;
+    if (KEYS)
+        item /= f.parts;
     const int heads = KEYS ? f.pr.Hk : f.pr.Hq, tile = item / heads;  // the longest of a causal sequence first
-    head = item % heads;
-    t0 = (KEYS ? tile : f.items / heads - 1 - tile) * kTile;
+    const int at = KEYS ? tile : (f.pr.T + kTile - 1) / kTile - 1 - tile;
+    return {item % heads, at * kTile, part, KEYS && f.parts > 1 ? f.parts_of[at] : 1};
 }
 template <bool KEYS>
 __device__ __forceinline__ Span span_of(const Problem &pr, int t)
@@ -64,9 +77,45 @@ __device__ __forceinline__ Span span_of(const Problem &pr, int t)
     return KEYS ? pr.rows_of(t) : pr.keys_of(t);
 }
 
-// delta [Hq][T] = sum over d of do * o.
-__global__ void __launch_bounds__(256) delta_kernel(Problem pr, Heads dout, Heads o, float *delta)
+// How many blocks share a key tile's query heads: as many as it takes for none to have more than half of an SM's share of
+// all the steps.  By one block; sequences are looked at by a tile's ends, which decides about time only.
+__device__ void share_out(const Problem &pr, int most, int sms, int *parts_of)
 {
+    __shared__ float shared[8];
+    const int tiles = (pr.T + kTile - 1) / kTile, group = pr.Hq / pr.Hk;
+    float steps = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+        float sum = 0.f;
+        for (int i = threadIdx.x; i < tiles; i += 256) {
+            const Span a = pr.sequence(i * kTile), b = pr.sequence(min(pr.T, i * kTile + kTile) - 1);
+            const int from = pr.causal ? i * kTile : a.a < a.b ? a.a : i * kTile, to = max(a.b, b.b);
+            const float mine = float(group) * float(max(1, (to + kTile - 1) / kTile - from / kTile));
+            sum += mine;
+            if (pass)
+                parts_of[i] = max(1, min(most, int(ceilf(mine / steps))));
+        }
+        if (pass)
+            return;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            sum += __shfl_xor_sync(kAll, sum, o);
+        if (threadIdx.x % 32 == 0)
+            shared[threadIdx.x / 32] = sum;
+        __syncthreads();
+        for (int w = 0; w < 8; ++w)
+            steps += shared[w];
+        steps = fmaxf(8.f, steps * float(pr.Hk) / float(2 * sms));
+    }
+}
+
+// delta [Hq][T] = sum over d of do * o.
+__global__ void __launch_bounds__(256) delta_kernel(Problem pr, Heads dout, Heads o, float *delta, int parts, int sms,
+                                                    int *parts_of)
+{
+    if (parts > 1 && blockIdx.x == gridDim.x - 1) {
+        share_out(pr, parts, sms, parts_of);
+        return;
+    }
     const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) / 16;  // 16 lanes a row
     const int at = threadIdx.x % 16 * 8;
     const int64_t t = i / pr.Hq;
@@ -87,20 +136,33 @@ __global__ void __launch_bounds__(256) delta_kernel(Problem pr, Heads dout, Head
         delta[int64_t(h) * pr.T + t] = s;
 }
 
+// A row of an output, or of a part's sums for it.
+struct Row {
+    bf16 *out;
+    float *part;  // if not NULL
+    __device__ __forceinline__ void put(int d, const float *x) const
+    {
+        if (part)
+            tide::store8(part + d, x);
+        else
+            tide::store8(out + d, x);
+    }
+};
+
 // One output row a lane (dv, dk or dq of token t), by itself, over what it sees only; lanes with an empty span take no
-// part.  Columns [d0, d1).  Ends early where every element is NaN already.
+// part.  Query heads [h0, h1), columns [d0, d1).  Ends early where every element is NaN already.
 enum Which { kDv, kDk, kDq };
-__device__ __forceinline__ void row_alone(Which which, const Backward &f, int t, int head, Span see, int d0, int d1, bf16 *out)
+__device__ __forceinline__ void row_alone(Which which, const Backward &f, int t, int h0, int h1, Span see, int d0, int d1,
+                                          const Row &row)
 {
     const Problem &pr = f.pr;
     const Span all = warp_span(see);
     const bool mine = see.a < see.b;
     const int group = pr.Hq / pr.Hk, D = pr.D;
     const float c = pr.scale * kLog2e;
-    const int h0 = which == kDq ? head : head * group, h1 = which == kDq ? head + 1 : h0 + group;
 #pragma unroll 1
-    for (int d = d0; d < d1; d += 16) {
-        float acc[16] = {};
+    for (int d = d0; d < d1; d += 8) {
+        float acc[8] = {};
         bool more = mine;
 #pragma unroll 1
         for (int h = h0; h < h1; ++h)
@@ -112,31 +174,63 @@ __device__ __forceinline__ void row_alone(Which which, const Backward &f, int t,
                 const int64_t i = int64_t(h) * pr.T + r;
                 const float p = exp2_fast(fmaf(dot_row(f.q.row(r, h), f.k.row(key, hk), D), c, -f.lse[i] * kLog2e));
                 const float w = which == kDv ? p : p * (dot_row(f.dout.row(r, h), f.v.row(key, hk), D) - f.delta[i]);
-                const bf16 *from = which == kDv ? f.dout.row(r, h) : which == kDk ? f.q.row(r, h) : f.k.row(key, hk);
+                float x[8];
+                tide::load8((which == kDv ? f.dout.row(r, h) : which == kDk ? f.q.row(r, h) : f.k.row(key, hk)) + d, x);
                 more = false;
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    float x[8];
-                    if (d + e < d1)
-                        tide::load8(from + d + e, x);
-#pragma unroll
-                    for (int m = 0; m < 8; ++m)
-                        if (d + e < d1) {
-                            acc[e + m] = fmaf(w, x[m], acc[e + m]);
-                            more = more || !isnan(acc[e + m]);
-                        }
+                for (int m = 0; m < 8; ++m) {
+                    acc[m] = fmaf(w, x[m], acc[m]);
+                    more = more || !isnan(acc[m]);
                 }
             }
+        if (mine) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 8)
-            if (mine && d + e < d1) {
-                float x[8];
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    x[m] = which == kDv ? acc[e + m] : acc[e + m] * pr.scale;
-                tide::store8(out + d + e, x);
-            }
+            for (int m = 0; m < 8; ++m)
+                acc[m] *= which == kDv ? 1.f : pr.scale;
+            row.put(d, acc);
+        }
     }
+}
+
+struct Output {
+    Which which;
+    int d0, d1;
+    Row row;
+};
+
+__device__ __forceinline__ float2 pair(const uint32_t (&v)[kWide / 32][32], int x)
+{
+    return make_float2(__uint_as_float(v[x / 16][x % 16 * 2]), __uint_as_float(v[x / 16][x % 16 * 2 + 1]));
+}
+// Columns outside [a, b) become 0.
+__device__ __forceinline__ void clear_outside(float2 (&p)[kWide / 2], int a, int b)
+{
+#pragma unroll
+    for (int x = 0; x < kWide / 2; ++x) {
+        p[x].x = 2 * x >= a && 2 * x < b ? p[x].x : 0.f;
+        p[x].y = 2 * x + 1 >= a && 2 * x + 1 < b ? p[x].y : 0.f;
+    }
+}
+
+// A warp's columns of S or D, and their bf16 over the first half of each 32 of them.
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[kWide / 32][32])
+{
+#pragma unroll
+    for (int i = 0; i < kWide / 32; ++i)
+        um::tmem_load32(at + 32 * i, v[i]);
+    um::tmem_wait_load();
+}
+__device__ __forceinline__ void store_columns(uint32_t at, const float2 (&p)[kWide / 2])
+{
+#pragma unroll
+    for (int i = 0; i < kWide / 32; ++i) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+            w[x] = tide::pack_bf16(p[16 * i + x].x, p[16 * i + x].y);
+        um::tmem_store16(at + 32 * i, w);
+    }
+    um::tmem_wait_store();
 }
 
 // W: columns of a head in shared and tensor memory, 64 or 128.  KEYS: the resident tile is one of keys.
@@ -154,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     __shared__ alignas(16) uint4 answer;
     __shared__ alignas(16) float lse_of[2][kTile], delta_of[kTile];  // keys: of a step's rows, -lse in log2, and -delta
     __shared__ Item items[2];
-    __shared__ int claims[kClaims], claimed, done[8];  // done: items of each of the eight warps
+    __shared__ int claims[kClaims], claimed, done[kWarps];  // done: items of each of the elements' warps
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
     const uint32_t x_full = um::smem_addr(bars), x_empty = x_full + 8 * kXs, y_full = x_empty + 8 * kXs,
@@ -174,20 +268,20 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
             um::mbar_init(y_full + 8 * i, 1), um::mbar_init(y_empty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(d_full + 8 * i, 1);
-            um::mbar_init(ds_ready + 8 * i, 8);  // rows: a warp may be a step ahead of another one
+            um::mbar_init(ds_ready + 8 * i, kWarps);  // rows: a warp may be a step ahead of another one
             um::mbar_init(item_full + 8 * i, 1);
-            um::mbar_init(item_empty + 8 * i, KEYS ? 10 : 9);
+            um::mbar_init(item_empty + 8 * i, kWarps + (KEYS ? 2 : 1));
             um::mbar_init(lse_full + 8 * i, 1);
-            um::mbar_init(lse_empty + 8 * i, 8);
+            um::mbar_init(lse_empty + 8 * i, kWarps);
         }
         um::mbar_init(r_full, 1);
         um::mbar_init(r_empty, 1);
         um::mbar_init(s_full, 1);
-        um::mbar_init(p_ready, 8);
+        um::mbar_init(p_ready, kWarps);
         um::mbar_init(acc_full, 1);
-        um::mbar_init(acc_free, 8);
+        um::mbar_init(acc_free, kWarps);
         um::mbar_init(delta_full, 1);
-        um::mbar_init(delta_empty, 8);
+        um::mbar_init(delta_empty, kWarps);
         um::mbar_init(asked, 1);
         um::mbar_init(drained, 1);
         um::mbar_init(never, 1);
@@ -199,50 +293,66 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         um::prefetch_map(&f.x);
         um::prefetch_map(&f.y);
     }
-    if (threadIdx.x < 8)
+    if (threadIdx.x < kWarps)
         done[threadIdx.x] = 0;
-    if (warp == 9)
+    if (warp == kMultiply)
         um::tmem_alloc_own(um::smem_addr(&tmem_slot), 512);
     um::fence_before();
     __syncthreads();
     um::fence_after();
     const uint32_t tmem = tmem_slot;
-    auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait(bar, parity, &gave_up, f.wait_ns); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return um::mbar_wait_held(bar, parity, &gave_up, f.wait_ns); };
+    // What a warp writes of token t's results.  Keys: its share of the columns of dv or of dk; rows: of those of dq.
+    constexpr int kShare = KEYS ? kGroups / 2 : kGroups, kCols = W / kShare;
+    auto output_of = [&](const Place &at, int t, int warp) {
+        const int g = warp / 4, d0 = g % kShare * kCols, row = min(t, pr.T - 1);
+        const Which which = !KEYS ? kDq : g < kShare ? kDv : kDk;
+        float *part = nullptr;
+        if (KEYS && at.parts > 1)
+            part = f.partial + (((int64_t(at.part) * 2 + (which == kDk)) * pr.T + row) * pr.Hk + at.head) * pr.D;
+        return Output{which, d0, min(d0 + kCols, pr.D), {(which == kDv ? f.out0 : f.out1).row(row, at.head), part}};
+    };
 
-    if (warp >= 8) {
+    if (warp >= kWarps) {
         um::fewer_registers<kOtherRegs>();
-        if (warp == 8) {
+        if (warp == kFetch) {
             const bool leader = um::elected();
             int number = blockIdx.x, slot = 0, turn = 0, xi = 0, x_phase = 0, yi = 0, y_phase = 0, taken = 0;
             int x_fills = 0, y_fills = 0, r_fills = 0;  // copies under way at most: the last of each place
             bool ok = true;
+            int asks = 0;
+            bool pending = false;  // an answer is under way
             while (ok) {
-                if (lane == 0) {
-                    claims[taken % kClaims] = number;
-                    claimed = taken + 1;
-                }
-                ++taken;
-                if (leader)
-                    um::ask_next_block(um::smem_addr(&answer), asked);
-                int head, t0;
-                place_of<KEYS>(f, number, head, t0);
-                // which tiles are streamed: what the resident ones see or are seen by, four tokens a lane
-                Span see = {0x7fffffff, 0};
+                const Place at = place_of<KEYS>(f, number);
+                const bool taking = at.part < at.parts;  // there are fewer parts than there could be
+                Tiles tiles = {0, 0};
+                const int h0 = KEYS ? at.head * group + group * at.part / at.parts : at.head;
+                const int h1 = KEYS ? at.head * group + group * (at.part + 1) / at.parts : at.head + 1;
+                if (taking) {
+                    if (lane == 0) {
+                        claims[taken % kClaims] = number;
+                        claimed = taken + 1;
+                    }
+                    ++taken;
+                    // which tiles are streamed: what the resident ones see or are seen by, four tokens a lane
+                    Span see = {0x7fffffff, 0};
 #pragma unroll 1
-                for (int t = t0 + lane; t < t0 + kTile; t += 32) {
-                    const Span s = span_of<KEYS>(pr, t);
-                    if (s.a < s.b)
-                        see = {min(see.a, s.a), max(see.b, s.b)};
+                    for (int t = at.t0 + lane; t < at.t0 + kTile; t += 32) {
+                        const Span s = span_of<KEYS>(pr, t);
+                        if (s.a < s.b)
+                            see = {min(see.a, s.a), max(see.b, s.b)};
+                    }
+                    tiles = tiles_of(warp_span(see));
+                    if (!(ok = wait(item_empty + 8 * slot, turn ^ 1)))
+                        break;
+                    if (lane == 0) {
+                        items[slot] = {number, tiles, h0, h1};
+                        um::mbar_arrive(item_full + 8 * slot);
+                    }
+                    if (++slot == 2)
+                        slot = 0, turn ^= 1;
                 }
-                const Tiles tiles = tiles_of(warp_span(see));
-                if (!(ok = wait(item_empty + 8 * slot, turn ^ 1)))
-                    break;
-                if (lane == 0) {
-                    items[slot] = {number, tiles};
-                    um::mbar_arrive(item_full + 8 * slot);
-                }
-                if (++slot == 2)
-                    slot = 0, turn ^= 1;
+                const int head = at.head, t0 = at.t0;
                 if (tiles.a < tiles.b) {
                     if (!(ok = wait(r_empty, (r_fills & 1) ^ 1)))
                         break;
@@ -253,10 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     }
                     ++r_fills;
                 }
-                const int h0 = KEYS ? head * group : head / group, h1 = KEYS ? h0 + group : h0 + 1;
                 bool skip = f.skip_fill && number == 0;  // this item's first streamed tile never comes
                 for (int h = h0; ok && h < h1; ++h)
                     for (int j = tiles.a; j < tiles.b; ++j) {
+                        const int from = KEYS ? h : h / group;
                         if (!(ok = wait(x_empty + 8 * xi, x_phase ^ 1)))
                             break;
                         if (skip) {
@@ -265,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         }
                         if (leader) {
                             um::mbar_expect(x_full + 8 * xi, kTileBytes);
-                            load_tile(xs + xi * kTileBytes, &f.x, kHalves, h, j * kTile, x_full + 8 * xi);
+                            load_tile(xs + xi * kTileBytes, &f.x, kHalves, from, j * kTile, x_full + 8 * xi);
                         }
                         ++x_fills;
                         if (++xi == kXs)
@@ -274,14 +384,22 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                             break;
                         if (leader) {
                             um::mbar_expect(y_full + 8 * yi, kTileBytes);
-                            load_tile(ys + yi * kTileBytes, &f.y, kHalves, h, j * kTile, y_full + 8 * yi);
+                            load_tile(ys + yi * kTileBytes, &f.y, kHalves, from, j * kTile, y_full + 8 * yi);
                         }
                         ++y_fills;
                         if (++yi == kYs)
                             yi = 0, y_phase ^= 1;
                     }
-                if (!ok || !(ok = wait(asked, (taken - 1) & 1)))
+                if (!ok)
                     break;
+                // Asked for as late as the copies ahead allow: a block that is at work on a long item must not hold
+                // the next one back from those that come free.
+                if (leader)
+                    um::ask_next_block(um::smem_addr(&answer), asked);
+                pending = true;
+                if (!(ok = wait(asked, asks & 1)))
+                    break;
+                pending = false, ++asks;
                 number = um::next_block(um::smem_addr(&answer));
                 um::fence_copies();
                 __syncwarp();
@@ -295,17 +413,19 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 }
             }
             if (!ok) {
-                // The answer that is under way, and the copies: neither may find the block gone.
+                // An answer that is under way, and the copies: neither may find the block gone.
                 auto land = [&](uint32_t bar, uint32_t parity) {
                     const uint64_t began = um::now_ns();
                     while (!um::mbar_try(bar, parity) && um::now_ns() - began < f.wait_ns) {
                     }
                 };
-                land(asked, (taken - 1) & 1);
-                const int more = um::next_block(um::smem_addr(&answer));
-                if (lane == 0 && more >= 0 && more != number) {
-                    claims[taken % kClaims] = more;
-                    claimed = taken + 1;
+                if (pending) {
+                    land(asked, asks & 1);
+                    const int more = um::next_block(um::smem_addr(&answer));
+                    if (more >= 0 && more != number && place_of<KEYS>(f, more).part < place_of<KEYS>(f, more).parts && lane == 0) {
+                        claims[taken % kClaims] = more;
+                        claimed = taken + 1;
+                    }
                 }
                 for (int i = max(0, x_fills - kXs); i < x_fills; ++i)
                     land(x_full + 8 * (i % kXs), (i / kXs) & 1);
@@ -315,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     land(r_full, (r_fills - 1) & 1);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == kMultiply) {
             const bool leader = um::elected();
             const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
             const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
@@ -332,14 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     um::mma_commit_own(bar);
                 }
             };
-            // a sum over a streamed tile's rows, with P or dS, whose halves are 64 columns apart
+            // a sum over a streamed tile's rows, with P or dS, whose quarters are 32 columns apart
             auto sum = [&](uint32_t d, uint32_t p, uint32_t streamed, bool add, uint32_t bar) {
                 um::fence_after();
                 if (leader) {
                     const uint64_t b = um::operand_desc(streamed, true, kHalf);
 #pragma unroll
                     for (int i = 0; i < kTile / 16; ++i)
-                        um::mma_own_tmem(tmem + d, tmem + p + (i / 4) * 64 + i % 4 * 8, b + i * (2048 >> 4), idesc_acc,
+                        um::mma_own_tmem(tmem + d, tmem + p + (i / 2) * 32 + i % 2 * 8, b + i * (2048 >> 4), idesc_acc,
                                          add || i > 0);
                     um::mma_commit_own(bar);
                 }
@@ -358,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     slot = 0, turn ^= 1;
                 if (it.number < 0)
                     break;
-                const int steps = (it.tiles.b - it.tiles.a) * (KEYS ? group : 1);
+                const int steps = (it.tiles.b - it.tiles.a) * (it.h1 - it.h0);
                 if (steps == 0)
                     continue;
                 if (!(ok = wait(r_full, r_phase)))
@@ -428,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 }
             }
             __syncwarp();
-        } else if (KEYS && warp == 10) {
+        } else if (KEYS && warp == kStats) {
             int slot = 0, turn = 0, at = 0;
             uint32_t phase = 0, delta_phase = 0;
             bool ok = true;
@@ -443,9 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     slot = 0, turn ^= 1;
                 if (it.number < 0)
                     break;
-                int head, t0;
-                place_of<KEYS>(f, it.number, head, t0);
-                for (int h = head * group; ok && h < (head + 1) * group; ++h)
+                for (int h = it.h0; ok && h < it.h1; ++h)
                     for (int j = it.tiles.a; j < it.tiles.b; ++j) {
                         float l[4], d[4];
 #pragma unroll
@@ -479,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         }
     } else {
         um::more_registers<kRowRegs>();
-        const int half = warp / 4, quarter = warp % 4;
+        const int quarter = warp % 4, cols = warp / 4 * kWide;  // 32 rows, kWide columns of a step
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
         const float c = pr.scale * kLog2e;
         int slot = 0, turn = 0, at = 0;
@@ -496,33 +614,30 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 slot = 0, turn ^= 1;
             if (it.number < 0)
                 break;
-            int head, t0;
-            place_of<KEYS>(f, it.number, head, t0);
-            const int t = t0 + quarter * 32 + lane;
+            const Place place = place_of<KEYS>(f, it.number);
+            const int t = place.t0 + quarter * 32 + lane;
             const Span see = span_of<KEYS>(pr, t);
             float lse2 = 0.f, delta = 0.f;  // rows: negated
             if (!KEYS && t < pr.T) {
-                const int64_t from = int64_t(head) * pr.T + t;
+                const int64_t from = int64_t(place.head) * pr.T + t;
                 lse2 = -f.lse[from] * kLog2e;
                 delta = -f.delta[from];
             }
             __syncwarp();  // the search for the sequence took lanes apart
-            const int steps = (it.tiles.b - it.tiles.a) * (KEYS ? group : 1);
+            const int steps = (it.tiles.b - it.tiles.a) * (it.h1 - it.h0);
             int j = it.tiles.a;
             for (int n = 0; n < steps; ++n) {
-                const int first = j * kTile + half * 64;  // token of this thread's first column
+                const int first = j * kTile + cols;  // token of this thread's first column
                 if (++j == it.tiles.b)
                     j = it.tiles.a;
                 const int a = see.a - first, b = see.b - first;
-                const bool masked = __any_sync(kAll, a > 0 || b < 64);
+                const bool masked = __any_sync(kAll, a > 0 || b < kWide);
                 if (!(ok = wait(s_full, s_phase)))
                     break;
                 s_phase ^= 1;
                 um::fence_after();
-                uint32_t v[2][32];
-                um::tmem_load32(lanes + kS + half * 64, v[0]);
-                um::tmem_load32(lanes + kS + half * 64 + 32, v[1]);
-                um::tmem_wait_load();
+                uint32_t v[kWide / 32][32];
+                load_columns(lanes + kS + cols, v);
                 if (!KEYS) {  // S is not written over: free for the next one
                     um::fence_before();
                     __syncwarp();
@@ -531,31 +646,23 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 } else if (!(ok = wait(lse_full + 8 * at, lse_phase))) {
                     break;
                 }
-                float2 p[32];
+                float2 p[kWide / 2];
                 const float2 cc = make_float2(c, c);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float2 l = make_float2(lse2, lse2);
+                for (int x = 0; x < kWide / 2; x += 2) {
+                    float4 l = make_float4(lse2, lse2, lse2, lse2);
                     if (KEYS)
-                        l = *reinterpret_cast<const float2 *>(&lse_of[at][half * 64 + 2 * x]);
-                    p[x] = um::fma2(make_float2(__uint_as_float(v[x / 16][x % 16 * 2]),
-                                                __uint_as_float(v[x / 16][x % 16 * 2 + 1])), cc, l);
-                    p[x].x = exp2_fast(p[x].x), p[x].y = exp2_fast(p[x].y);
-                }
-                if (masked) {
+                        l = *reinterpret_cast<const float4 *>(&lse_of[at][cols + 2 * x]);
+                    p[x] = um::fma2(pair(v, x), cc, make_float2(l.x, l.y));
+                    p[x + 1] = um::fma2(pair(v, x + 1), cc, make_float2(l.z, l.w));
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        p[x].x = 2 * x >= a && 2 * x < b ? p[x].x : 0.f;
-                        p[x].y = 2 * x + 1 >= a && 2 * x + 1 < b ? p[x].y : 0.f;
-                    }
+                    for (int y = x; y < x + 2; ++y)
+                        p[y].x = exp2_fast(p[y].x), p[y].y = exp2_fast(p[y].y);
                 }
+                if (masked)
+                    clear_outside(p, a, b);
                 if (KEYS) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        w[x] = tide::pack_bf16(p[x].x, p[x].y);
-                    um::tmem_store32(lanes + kS + half * 64, w);
-                    um::tmem_wait_store();
+                    store_columns(lanes + kS + cols, p);
                     um::fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -573,32 +680,19 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     break;
                 d_phase ^= 1 << buf;
                 um::fence_after();
-                const uint32_t d_at = lanes + kD + buf * 128 + half * 64;
-                um::tmem_load32(d_at, v[0]);
-                um::tmem_load32(d_at + 32, v[1]);
-                um::tmem_wait_load();
-                uint32_t w[32];
+                const uint32_t d_at = lanes + kD + buf * 128 + cols;
+                load_columns(d_at, v);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float2 d = make_float2(delta, delta);
+                for (int x = 0; x < kWide / 2; x += 2) {
+                    float4 d = make_float4(delta, delta, delta, delta);
                     if (KEYS)
-                        d = *reinterpret_cast<const float2 *>(&delta_of[half * 64 + 2 * x]);
-                    d = um::add2(make_float2(__uint_as_float(v[x / 16][x % 16 * 2]),
-                                             __uint_as_float(v[x / 16][x % 16 * 2 + 1])), d);
-                    p[x] = um::mul2(p[x], d);
+                        d = *reinterpret_cast<const float4 *>(&delta_of[cols + 2 * x]);
+                    p[x] = um::mul2(p[x], um::add2(pair(v, x), make_float2(d.x, d.y)));
+                    p[x + 1] = um::mul2(p[x + 1], um::add2(pair(v, x + 1), make_float2(d.z, d.w)));
                 }
-                if (masked) {  // 0 times what is not finite
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        p[x].x = 2 * x >= a && 2 * x < b ? p[x].x : 0.f;
-                        p[x].y = 2 * x + 1 >= a && 2 * x + 1 < b ? p[x].y : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    w[x] = tide::pack_bf16(p[x].x, p[x].y);
-                um::tmem_store32(d_at, w);
-                um::tmem_wait_store();
+                if (masked)  // 0 times what is not finite
+                    clear_outside(p, a, b);
+                store_columns(d_at, p);
                 um::fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -609,26 +703,23 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
             }
             if (!ok)
                 break;
-            // Keys: the first four warps have dv, the others dk; rows: half the columns of dq each.
-            constexpr int kCols = KEYS ? W : W / 2;
-            const int d0 = KEYS ? 0 : half * kCols;
+            const Output out = output_of(place, t, warp);
             const bool some = see.a < see.b;
-            bf16 *out = (KEYS && half == 0 ? f.out0 : f.out1).row(min(t, pr.T - 1), head);
             if (steps) {
                 if (!(ok = wait(acc_full, acc_phase)))
                     break;
                 acc_phase ^= 1;
                 um::fence_after();
-                uint32_t o[kCols / 32][32];
+                uint32_t o[(kCols + 31) / 32][32];
 #pragma unroll
-                for (int i = 0; i < kCols / 32; ++i)
-                    um::tmem_load32(lanes + (KEYS && half == 0 ? kAcc0 : kAcc1) + d0 + 32 * i, o[i]);
+                for (int i = 0; i < kCols; i += 32)
+                    um::tmem_load32(lanes + (out.which == kDv ? kAcc0 : kAcc1) + out.d0 + i, o[i / 32]);
                 um::tmem_wait_load();
                 um::fence_before();
                 __syncwarp();
                 if (lane == 0)
                     um::mbar_arrive(acc_free);
-                const float by = KEYS && half == 0 ? 1.f : pr.scale;
+                const float by = out.which == kDv ? 1.f : pr.scale;
                 bool odd = false;  // not finite
 #pragma unroll
                 for (int d = 0; d < kCols; d += 8) {
@@ -639,17 +730,16 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         odd = odd || !(fabsf(x[i]) < INFINITY);
                         x[i] = some ? x[i] * by : 0.f;
                     }
-                    if (d0 + d < pr.D && t < pr.T)
-                        tide::store8(out + d0 + d, x);
+                    if (out.d0 + d < pr.D && t < pr.T)
+                        out.row.put(out.d0 + d, x);
                 }
                 odd = odd && some;
                 if (__any_sync(kAll, odd))
-                    row_alone(!KEYS ? kDq : half ? kDk : kDv, f, odd ? t : 0, head, odd ? see : Span{0, 0}, d0,
-                              min(d0 + kCols, pr.D), out);
+                    row_alone(out.which, f, odd ? t : 0, it.h0, it.h1, odd ? see : Span{0, 0}, out.d0, out.d1, out.row);
             } else if (t < pr.T) {
                 const float x[8] = {};
-                for (int d = d0; d < min(d0 + kCols, pr.D); d += 8)
-                    tide::store8(out + d, x);
+                for (int d = out.d0; d < out.d1; d += 8)
+                    out.row.put(d, x);
             }
             if (lane == 0)
                 ++done[warp];
@@ -661,21 +751,41 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     if (gave_up) {  // what was claimed and not finished is NaN
         if (threadIdx.x == 0)
             g_timed_out = 1;
-        if (warp < 8)
+        if (warp < kWarps)
             for (int i = done[warp]; i < claimed; ++i) {
-                int head, t0;
-                place_of<KEYS>(f, claims[i % kClaims], head, t0);
-                const int t = t0 + threadIdx.x % kTile, half = warp / 4;
-                if (t >= pr.T)
-                    continue;
-                bf16 *out = (KEYS && half == 0 ? f.out0 : f.out1).row(t, head);
-                const int d0 = KEYS ? 0 : half * (W / 2), d1 = KEYS ? pr.D : min(d0 + W / 2, pr.D);
-                for (int d = d0; d < d1; ++d)
-                    out[d] = __float2bfloat16_rn(__int_as_float(0x7fffffff));
+                const Place place = place_of<KEYS>(f, claims[i % kClaims]);
+                const int t = place.t0 + threadIdx.x % kTile;
+                const Output out = output_of(place, t, warp);
+                const float nan = __int_as_float(0x7fffffff), x[8] = {nan, nan, nan, nan, nan, nan, nan, nan};
+                if (t < pr.T)
+                    for (int d = out.d0; d < out.d1; d += 8)
+                        out.row.put(d, x);
             }
     }
-    if (warp == 9)
+    if (warp == kMultiply)
         um::tmem_free_own(tmem, 512);
+}
+
+// dv and dk of the tiles that were shared out: the parts' sums, in order.
+__global__ void __launch_bounds__(256) join_kernel(Problem pr, const int *parts_of, const float *partial, Heads dv, Heads dk)
+{
+    const int tile = blockIdx.x / pr.Hk, head = blockIdx.x % pr.Hk, parts = parts_of[tile], units = pr.D / 8;
+    if (parts < 2)
+        return;
+    for (int i = threadIdx.x; i < 2 * kTile * units; i += 256) {
+        const int which = i / (kTile * units), t = tile * kTile + i / units % kTile, d = i % units * 8;
+        if (t >= pr.T)
+            continue;
+        float sum[8] = {};
+        for (int p = 0; p < parts; ++p) {
+            float x[8];
+            tide::load8(partial + (((int64_t(p) * 2 + which) * pr.T + t) * pr.Hk + head) * pr.D + d, x);
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                sum[m] += x[m];
+        }
+        tide::store8((which ? dk : dv).row(t, head) + d, sum);
+    }
 }
 
 template <int W, bool KEYS>
@@ -687,6 +797,26 @@ tide_status_t launch(const Backward &f, cudaStream_t st)
         return op_fail(TIDE_ERR_CUDA, "attention_grad: %s", cudaGetErrorString(e));
     backward_kernel<W, KEYS><<<unsigned(f.items), kThreads, smem, st>>>(f);
     return tide::op_launched("attention_grad");
+}
+
+// Where a call's scratch data lies in its workspace, in bytes.
+struct Layout {
+    int parts;  // of a key tile, at most
+    int64_t parts_of = 0, partial = 0, bytes = 0;  // delta is first
+};
+Layout layout_of(const tide_attention_t *at)
+{
+    auto round_up = [](int64_t n) { return (n + 255) / 256 * 256; };
+    Layout l;
+    // Key tiles times key heads are the blocks of the first pass: where they are fewer than eight for an SM, which is
+    // too few for an even end with tiles of such different lengths, query heads that share a key head are shared out.
+    const int64_t tiles = (at->tokens + kTile - 1) / kTile, blocks = std::max<int64_t>(1, tiles * at->k_heads);
+    l.parts = int(std::min<int64_t>(at->q_heads / at->k_heads, (8 * std::max(tide::op_sm_count(), 1) + blocks - 1) / blocks));
+    l.parts_of = round_up(at->tokens * at->q_heads * 4);
+    l.partial = l.parts_of + (l.parts > 1 ? round_up(tiles * 4) : 0);
+    l.bytes = l.partial + (l.parts > 1 ? int64_t(l.parts) * 2 * at->tokens * at->k_heads * at->head_dim * 4 : 0);
+    l.bytes = std::max<int64_t>(256, l.bytes);
+    return l;
 }
 
 }  // namespace
@@ -704,9 +834,7 @@ extern "C" {
 int64_t tide_attention_grad_workspace(const tide_attention_t *at)
 {
     tide::record_error("");
-    if (check_desc(at))
-        return -1;
-    return std::max<int64_t>(256, at->tokens * at->q_heads * 4);
+    return check_desc(at) ? -1 : layout_of(at).bytes;
 }
 
 tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t *dout, const tide_heads_t *q,
@@ -729,10 +857,10 @@ tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t
         s = check_floats(at, lse, "lse");
     if (s || at->tokens == 0)
         return s;
-    const int64_t need = tide_attention_grad_workspace(at);
-    if (!workspace || workspace_bytes < need)
+    const Layout l = layout_of(at);
+    if (!workspace || workspace_bytes < l.bytes)
         return op_fail(TIDE_ERR_INVALID_ARG, "workspace of %lld bytes: need %lld", (long long)workspace_bytes,
-                       (long long)need);
+                       (long long)l.bytes);
     if (!op_aligned(workspace, 256))
         return op_fail(TIDE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
     if (!tide::encode_tiled())
@@ -758,20 +886,36 @@ tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t
         s = heads_map(&md, f.dout, p.T, p.Hq, p.D);
     if (s)
         return s;
-    delta_kernel<<<unsigned((int64_t(p.T) * p.Hq + 15) / 16), 256, 0, st>>>(p, f.dout, heads_of(at, o, p.Hq), delta);
+    int *parts_of = reinterpret_cast<int *>(static_cast<char *>(workspace) + l.parts_of);
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) + l.partial);
+    // The shared memory of the large kernels for the small ones too: an SM that changes its share waits until it is empty.
+    cudaError_t e = tide::op_prefer_smem<delta_kernel>();
+    if (e == cudaSuccess)
+        e = tide::op_prefer_smem<join_kernel>();
+    if (e != cudaSuccess)
+        return op_fail(TIDE_ERR_CUDA, "attention_grad: %s", cudaGetErrorString(e));
+    delta_kernel<<<unsigned((int64_t(p.T) * p.Hq + 15) / 16 + (l.parts > 1)), 256, 0, st>>>(
+        p, f.dout, heads_of(at, o, p.Hq), delta, l.parts, std::max(tide::op_sm_count(), 1), parts_of);
     s = tide::op_launched("attention_grad: delta");
     if (s)
         return s;
     const int tiles = (p.T + kTile - 1) / kTile;
     f.r0 = mk, f.r1 = mv, f.x = mq, f.y = md;
     f.out0 = heads_of(at, dv, p.Hk), f.out1 = heads_of(at, dk, p.Hk);
-    f.items = tiles * p.Hk;
+    f.items = tiles * p.Hk * l.parts;
+    f.parts = l.parts, f.parts_of = parts_of, f.partial = partial;
     s = p.D <= 64 ? launch<64, true>(f, st) : launch<128, true>(f, st);
     if (s)
         return s;
+    if (l.parts > 1) {
+        join_kernel<<<unsigned(tiles * p.Hk), 256, 0, st>>>(p, parts_of, partial, f.out0, f.out1);
+        s = tide::op_launched("attention_grad: join");
+        if (s)
+            return s;
+    }
     f.r0 = mq, f.r1 = md, f.x = mk, f.y = mv;
     f.out1 = heads_of(at, dq, p.Hq);
-    f.items = tiles * p.Hq;
+    f.items = tiles * p.Hq, f.parts = 1;
     return p.D <= 64 ? launch<64, false>(f, st) : launch<128, false>(f, st);
 }
 

@@ -63,6 +63,21 @@ cudaError_t op_allow_smem(int bytes)
     return e;
 }
 
+// Gives a kernel that needs little shared memory the largest share of it all the same; asked for once on each device.
+template <auto KERNEL>
+cudaError_t op_prefer_smem()
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done.load(std::memory_order_relaxed) >> dev & 1))
+        return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // Reads and clears a device flag (synchronises the stream).
 inline cudaError_t take_flag(const int &flag, int *seen, cudaStream_t st)
 {

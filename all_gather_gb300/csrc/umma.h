@@ -125,6 +125,35 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same, for waits that are on the way of every step: the hardware holds the warp back until the phase is over, or a
+// tenth of a millisecond, so that many waiting warps do not take turns at the barriers.
+__device__ __forceinline__ bool mbar_try_held(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    return ok;
+}
+__device__ __forceinline__ bool mbar_wait_held(uint32_t bar, uint32_t parity, volatile int *gave_up, uint64_t budget_ns)
+{
+    if (__all_sync(0xffffffffu, mbar_try_held(bar, parity)))
+        return true;
+    const uint64_t t0 = now_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_held(bar, parity)))
+            return true;
+        if (__any_sync(0xffffffffu, *gave_up || now_ns() - t0 > budget_ns)) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+
 // For a pair of blocks that work on one product: the bytes count at a barrier
 // of either block (an address of the cluster's shared memory).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
@@ -359,6 +388,15 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
         "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
