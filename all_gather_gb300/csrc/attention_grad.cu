@@ -104,7 +104,7 @@ __device__ void share_out(const Problem &pr, int most, int sms, int *parts_of)
         __syncthreads();
         for (int w = 0; w < 8; ++w)
             steps += shared[w];
-        steps = fmaxf(8.f, steps * float(pr.Hk) / float(2 * sms));
+        steps = fmaxf(2.f, steps * float(pr.Hk) / float(2 * sms));
     }
 }
 
@@ -808,10 +808,11 @@ Layout layout_of(const tide_attention_t *at)
 {
     auto round_up = [](int64_t n) { return (n + 255) / 256 * 256; };
     Layout l;
-    // Key tiles times key heads are the blocks of the first pass: where they are fewer than eight for an SM, which is
-    // too few for an even end with tiles of such different lengths, query heads that share a key head are shared out.
+    // Key tiles times key heads are the blocks of the first pass, and the longest of a causal sequence has 2 / tiles of
+    // their work: where they are fewer than three for an SM it would be the last one to end, and the query heads that
+    // share a key head are shared out.
     const int64_t tiles = (at->tokens + kTile - 1) / kTile, blocks = std::max<int64_t>(1, tiles * at->k_heads);
-    l.parts = int(std::min<int64_t>(at->q_heads / at->k_heads, (8 * std::max(tide::op_sm_count(), 1) + blocks - 1) / blocks));
+    l.parts = int(std::min<int64_t>(at->q_heads / at->k_heads, (3 * std::max(tide::op_sm_count(), 1) + blocks - 1) / blocks));
     l.parts_of = round_up(at->tokens * at->q_heads * 4);
     l.partial = l.parts_of + (l.parts > 1 ? round_up(tiles * 4) : 0);
     l.bytes = l.partial + (l.parts > 1 ? int64_t(l.parts) * 2 * at->tokens * at->k_heads * at->head_dim * 4 : 0);

@@ -6,10 +6,10 @@ A step is FSDP2's: the fp32 master shards are rounded to bf16 and placed as
 full parameters (all-gather), every rank runs its own tokens forward and
 backward, the ranks' bf16 gradients are folded into fp32 shards where they lie
 (reduce-scatter), and each shard is updated.  Between the two collectives run
-the operators that surround them in such a model: norm of queries and keys
-with the position rotation, SwiGLU with 8-bit checkpoints, and the vocabulary
-head with its cross entropy.  What is left (the projections, the attention
-itself, the layer norms) is plain torch.
+the operators that surround them in such a model: layer norms, norm of queries
+and keys with the position rotation, attention, SwiGLU with 8-bit checkpoints,
+and the vocabulary head with its cross entropy.  What is left, the
+projections, is plain torch.
 """
 from __future__ import annotations
 
@@ -49,20 +49,38 @@ class Block:
     def losses(self, p, tokens, targets):
         """Losses [context] of one sequence; p: the full parameters by name."""
         T, d, hq, hk = self.context, self.head_dim, self.heads, self.kv_heads
-        norm = lambda x: x * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6).to(x.dtype)  # noqa: E731
+        norm = lambda x: ad.layer_norm(x, eps=1e-6, center=False)  # noqa: E731
         x = p["embed"][tokens]
         qkv = norm(x) @ p["qkv"].t()
-        q, k, v = qkv.split([hq * d, hk * d, hk * d], 1)
-        q, k = ad.qk_norm_rope(q.view(T, hq, d), k.view(T, hk, d), self.table, self.positions, p["q_norm"],
-                               p["k_norm"])
-        k, v = (t.view(T, hk, d).repeat_interleave(hq // hk, 1) for t in (k, v))
-        score = torch.einsum("thd,shd->hts", q, k).float() * d ** -0.5
-        ahead = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
-        attn = score.masked_fill(ahead, float("-inf")).softmax(-1).to(BF16)
-        x = x + torch.einsum("hts,shd->thd", attn, v).reshape(T, hq * d) @ p["o"].t()
+        q, k, v = (t.view(T, -1, d) for t in qkv.split([hq * d, hk * d, hk * d], 1))
+        q, k = ad.qk_norm_rope(q, k, self.table, self.positions, p["q_norm"], p["k_norm"])
+        x = x + ad.attention(q, k, v).reshape(T, hq * d) @ p["o"].t()
         gate, up = (norm(x) @ p["gate_up"].t()).split(self.ffn, 1)
         x = x + ad.swiglu(gate, up) @ p["down"].t()
         return ad.linear_cross_entropy(norm(x), p["head"], targets)
+
+    def plain_losses(self, p, tokens, targets):
+        """The same in elementary operations, in the parameters' type."""
+        T, d, hq, hk = self.context, self.head_dim, self.heads, self.kv_heads
+        norm = lambda x: x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)  # noqa: E731
+        c, s = self.table.to(p["o"].dtype)[:, None].chunk(2, -1)
+
+        def turned(x):
+            a, b = x.chunk(2, -1)
+            return torch.cat((a * c - b * s, b * c + a * s), -1)
+
+        x = p["embed"][tokens]
+        qkv = norm(x) @ p["qkv"].t()
+        q, k, v = (t.view(T, -1, d) for t in qkv.split([hq * d, hk * d, hk * d], 1))
+        q, k = turned(norm(q) * p["q_norm"]), turned(norm(k) * p["k_norm"])
+        k, v = (t.repeat_interleave(hq // hk, 1) for t in (k, v))
+        score = torch.einsum("thd,shd->hts", q, k) * d ** -0.5
+        ahead = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
+        attn = score.masked_fill(ahead, float("-inf")).softmax(-1)
+        x = x + torch.einsum("hts,shd->thd", attn, v).reshape(T, hq * d) @ p["o"].t()
+        gate, up = (norm(x) @ p["gate_up"].t()).split(self.ffn, 1)
+        x = x + gate * gate.sigmoid() * up @ p["down"].t()
+        return -(norm(x) @ p["head"].t()).log_softmax(-1).gather(1, targets[:, None])[:, 0]
 
 
 def train(world=4, steps=20, lr=0.5, seed=0, model=None):
