@@ -36,7 +36,7 @@ using tide::op_aligned;
 using tide::op_fail;
 namespace um = tide::umma;
 
-constexpr int kThreads = 384;          // two groups of four warps for the rows; a warp that fetches, one that multiplies, two idle
+constexpr int kThreads = 384;          // two groups of four warps for the rows; a warp that fetches, two that multiply, one idle
 constexpr int kRowRegs = 224, kOtherRegs = 56;  // registers a thread, of 168 at the launch: (2 * 224 + 56) * 128 = 168 * 384
 constexpr int kRingBytes = 160 * 1024;
 constexpr int kClaims = 8;             // of a block's last items, kept for a wait that runs out
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     constexpr int kHalves = W / 64, kTileBytes = kHalves * kHalf, kStages = kRingBytes / kTileBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t q_at = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024, ring = q_at + 2 * kTileBytes;
-    __shared__ uint64_t bars[2 * kStages + 19];
+    __shared__ uint64_t bars[2 * kStages + 20];
     __shared__ alignas(16) uint4 answer;
     __shared__ Item items[2];
     __shared__ int claims[kClaims], claimed, done[8];  // done: items of each of the rows' warps
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages, rest = empty + 8 * kStages;
     const uint32_t q_full = rest, q_empty = rest + 16, s_full = rest + 32, p_ready = rest + 48, pv_done = rest + 64,
                    o_free = rest + 80, item_full = rest + 96, item_empty = rest + 112, asked = rest + 128,
-                   drained = rest + 136, never = rest + 144;
+                   drained = rest + 136, never = rest + 152;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Problem &pr = f.pr;
     const int group = pr.Hq / pr.Hk;
@@ -123,9 +123,10 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             um::mbar_init(full + 8 * i, 1);
-            um::mbar_init(empty + 8 * i, 1);
+            um::mbar_init(empty + 8 * i, 2);
         }
         for (int i = 0; i < 2; ++i) {
+            um::mbar_init(drained + 8 * i, 1);
             um::mbar_init(q_full + 8 * i, 1);
             um::mbar_init(q_empty + 8 * i, 1);
             um::mbar_init(s_full + 8 * i, 1);
@@ -133,10 +134,9 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             um::mbar_init(pv_done + 8 * i, 1);
             um::mbar_init(o_free + 8 * i, 4);
             um::mbar_init(item_full + 8 * i, 1);
-            um::mbar_init(item_empty + 8 * i, 9);
+            um::mbar_init(item_empty + 8 * i, 10);
         }
         um::mbar_init(asked, 1);
-        um::mbar_init(drained, 1);
         um::mbar_init(never, 1);
         um::fence_barrier_init();
         gave_up = 0, claimed = 0, answer = make_uint4(0, 0, 0, 0);
@@ -262,26 +262,24 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                         land(q_full + 8 * t, (q_fills[t] - 1) & 1);
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp < 11) {
+            // One of these for each row tile: a wait takes 250 cycles under load however long its phase has been over, and
+            // one tile's must not hold the other's products up.
+            const int t = warp - 9;
             const bool leader = um::elected();
             const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
             const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
             const uint32_t idesc_o = um::instr_desc(kTile, dn, false, true);
+            const uint32_t s_at = tmem + t * kTile, o_at = s_at + 2 * kTile;
+            const uint64_t qd = um::operand_desc(q_at + t * kTileBytes, false, 0);
             int slot = 0, turn = 0, stage = 0, phase = 0;
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+            uint32_t q_phase = 0, p_phase = 0, o_phase = 0;
             bool ok = true;
-            // S of row tile t from the key tile in a stage
-            auto scores = [&](int t, int at) {
-                um::fence_after();
-                if (leader) {
-                    const uint64_t a = um::operand_desc(q_at + t * kTileBytes, false, 0);
-                    const uint64_t b = um::operand_desc(ring + at * kTileBytes, false, 0);
-                    for (int i = 0; i < ksteps; ++i) {
-                        const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
-                        um::mma_own(tmem + t * kTile, a + off, b + off, idesc_s, i > 0);
-                    }
-                    um::mma_commit_own(s_full + 8 * t);
-                }
+            // A stage that this row tile has no use for: it has to have come all the same before its place is given back.
+            auto pass = [&](int at, uint32_t parity) {
+                ok = wait(full + 8 * at, parity);
+                if (ok && leader)
+                    um::mbar_arrive(empty + 8 * at);
             };
             while (ok) {
                 if (!(ok = wait(item_full + 8 * slot, turn)))
@@ -294,81 +292,76 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                     slot = 0, turn ^= 1;
                 if (it.number < 0)
                     break;
-                const Tiles &k0 = it.keys[0], &k1 = it.keys[1];
-                const bool both = k0.a < k0.b && k1.a < k1.b;
-                const Tiles all = both ? Tiles{min(k0.a, k1.a), max(k0.b, k1.b)} : k0.a < k0.b ? k0 : k1;
+                const Tiles &mine = it.keys[t], &other = it.keys[1 - t];
+                const bool both = mine.a < mine.b && other.a < other.b;
+                const Tiles all = both ? Tiles{min(mine.a, other.a), max(mine.b, other.b)} : mine.a < mine.b ? mine : other;
                 for (int j = all.a - 1; ok && j < all.b; ++j) {  // P v of key tile j, scores of key tile j + 1
-                    const int v_at = stage;
-                    bool v_here = j < all.a;
-                    int k_at = stage;
-                    uint32_t k_phase = phase;
-                    if (j >= all.a && ++k_at == kStages)
-                        k_at = 0, k_phase ^= 1;
-                    bool k_here = j + 1 >= all.b;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const Tiles &mine = t ? k1 : k0;
+                    if (j >= all.a) {
                         if (j >= mine.a && j < mine.b) {
-                            if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
+                            if (!(ok = wait(full + 8 * stage, phase)))
                                 break;
-                            v_here = true;
                             if (j == mine.a) {
-                                if (!(ok = wait(o_free + 8 * t, o_phase[t] ^ 1)))
+                                if (!(ok = wait(o_free + 8 * t, o_phase ^ 1)))
                                     break;
-                                o_phase[t] ^= 1;
+                                o_phase ^= 1;
                             }
-                            if (!(ok = wait(p_ready + 8 * t, p_phase[t])))
+                            if (!(ok = wait(p_ready + 8 * t, p_phase)))
                                 break;
-                            p_phase[t] ^= 1;
+                            p_phase ^= 1;
                             um::fence_after();
                             if (leader) {
-                                const uint64_t b = um::operand_desc(ring + v_at * kTileBytes, true, kHalf);
+                                const uint64_t b = um::operand_desc(ring + stage * kTileBytes, true, kHalf);
 #pragma unroll
                                 for (int i = 0; i < kTile / 16; ++i)
-                                    um::mma_own_tmem(tmem + 2 * kTile + t * kTile, tmem + t * kTile + i * 8, b + i * (2048 >> 4),
-                                                     idesc_o, j > mine.a || i > 0);
+                                    um::mma_own_tmem(o_at, s_at + i * 8, b + i * (2048 >> 4), idesc_o, j > mine.a || i > 0);
                                 um::mma_commit_own(pv_done + 8 * t);
+                                um::mma_commit_own(empty + 8 * stage);
                             }
-                        }
-                        if (j + 1 >= mine.a && j + 1 < mine.b) {
-                            if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
+                        } else {
+                            pass(stage, phase);
+                            if (!ok)
                                 break;
-                            k_here = true;
-                            if (j + 1 == mine.a) {
-                                if (!(ok = wait(q_full + 8 * t, q_phase[t])))
-                                    break;
-                                q_phase[t] ^= 1;
-                            }
-                            scores(t, k_at);
-                            if (j + 2 == mine.b && leader)
-                                um::mma_commit_own(q_empty + 8 * t);
                         }
-                    }
-                    if (!ok)
-                        break;
-                    // a tile that neither row tile needed has to have come all the same, before its place is given back
-                    if (!v_here && !(ok = wait(full + 8 * v_at, phase)))
-                        break;
-                    if (!k_here && !(ok = wait(full + 8 * k_at, k_phase)))
-                        break;
-                    if (leader) {
-                        if (j >= all.a)
-                            um::mma_commit_own(empty + 8 * v_at);
-                        if (j + 1 < all.b)
-                            um::mma_commit_own(empty + 8 * k_at);
-                    }
-                    // stages: k of all.a, then v of j and k of j + 1 in the order of their loads
-                    const int used = (j >= all.a) + (j + 1 < all.b);
-                    for (int i = 0; i < used; ++i)
                         if (++stage == kStages)
                             stage = 0, phase ^= 1;
+                    }
+                    if (j + 1 < all.b) {
+                        if (j + 1 >= mine.a && j + 1 < mine.b) {
+                            if (!(ok = wait(full + 8 * stage, phase)))
+                                break;
+                            if (j + 1 == mine.a) {
+                                if (!(ok = wait(q_full + 8 * t, q_phase)))
+                                    break;
+                                q_phase ^= 1;
+                            }
+                            um::fence_after();
+                            if (leader) {
+                                const uint64_t b = um::operand_desc(ring + stage * kTileBytes, false, 0);
+                                for (int i = 0; i < ksteps; ++i) {
+                                    const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
+                                    um::mma_own(s_at, qd + off, b + off, idesc_s, i > 0);
+                                }
+                                um::mma_commit_own(s_full + 8 * t);
+                                um::mma_commit_own(empty + 8 * stage);
+                                if (j + 2 == mine.b)
+                                    um::mma_commit_own(q_empty + 8 * t);
+                            }
+                        } else {
+                            pass(stage, phase);
+                            if (!ok)
+                                break;
+                        }
+                        // the next v is behind this k
+                        if (++stage == kStages)
+                            stage = 0, phase ^= 1;
+                    }
                 }
             }
             __syncwarp();
             if (leader) {  // nothing may be under way when the accumulators go
-                um::mma_commit_own(drained);
+                um::mma_commit_own(drained + 8 * t);
                 const uint64_t t0 = um::now_ns();
-                while (!um::mbar_try(drained, 0) && um::now_ns() - t0 < f.wait_ns) {
+                while (!um::mbar_try(drained + 8 * t, 0) && um::now_ns() - t0 < f.wait_ns) {
                 }
             }
             __syncwarp();

@@ -31,9 +31,9 @@ namespace um = tide::umma;
 
 constexpr int kWarps = 8;                    // for the elements: a quarter of the rows and a part of the columns each
 constexpr int kGroups = kWarps / 4, kWide = kTile / kGroups;
-constexpr int kThreads = 32 * (kWarps + 4);  // and one that fetches, one that multiplies, one for lse and delta, one idle
+constexpr int kThreads = 32 * (kWarps + 4);  // and one that fetches, two that multiply, one for lse and delta
 constexpr int kRowRegs = 224, kOtherRegs = 56;  // registers a thread, of 168 at the launch: 256 * 224 + 128 * 56 = 384 * 168
-constexpr int kFetch = kWarps, kMultiply = kWarps + 1, kStats = kWarps + 2;
+constexpr int kFetch = kWarps, kStats = kWarps + 1, kMultiply = kWarps + 2;  // kMultiply + 1 is the second one
 constexpr int kClaims = 8;  // of a block's last items, kept for a wait that runs out
 
 // Set when a bounded wait runs out.
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     const uint32_t resident = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
     const uint32_t xs = resident + 2 * kTileBytes, ys = xs + kXs * kTileBytes;
-    __shared__ uint64_t bars[2 * kXs + 2 * kYs + 23];
+    __shared__ uint64_t bars[2 * kXs + 2 * kYs + 24];
     __shared__ alignas(16) uint4 answer;
     __shared__ alignas(16) float lse_of[2][kTile], delta_of[kTile];  // keys: of a step's rows, -lse in log2, and -delta
     __shared__ Item items[2];
@@ -256,34 +256,34 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     const uint32_t r_full = rest, r_empty = rest + 8, s_full = rest + 16, p_ready = rest + 24, d_full = rest + 32,
                    ds_ready = rest + 48, acc_full = rest + 64, acc_free = rest + 72, item_full = rest + 80,
                    item_empty = rest + 96, lse_full = rest + 112, lse_empty = rest + 128, delta_full = rest + 144,
-                   delta_empty = rest + 152, asked = rest + 160, drained = rest + 168, never = rest + 176;
+                   delta_empty = rest + 152, asked = rest + 160, drained = rest + 168, never = rest + 184;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Problem &pr = f.pr;
     const int group = pr.Hq / pr.Hk;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kXs; ++i)
-            um::mbar_init(x_full + 8 * i, 1), um::mbar_init(x_empty + 8 * i, 1);
+            um::mbar_init(x_full + 8 * i, 1), um::mbar_init(x_empty + 8 * i, 2);
         for (int i = 0; i < kYs; ++i)
-            um::mbar_init(y_full + 8 * i, 1), um::mbar_init(y_empty + 8 * i, 1);
+            um::mbar_init(y_full + 8 * i, 1), um::mbar_init(y_empty + 8 * i, KEYS ? 2 : 1);
         for (int i = 0; i < 2; ++i) {
             um::mbar_init(d_full + 8 * i, 1);
             um::mbar_init(ds_ready + 8 * i, kWarps);  // rows: a warp may be a step ahead of another one
             um::mbar_init(item_full + 8 * i, 1);
-            um::mbar_init(item_empty + 8 * i, kWarps + (KEYS ? 2 : 1));
+            um::mbar_init(item_empty + 8 * i, kWarps + (KEYS ? 3 : 2));
+            um::mbar_init(drained + 8 * i, 1);
             um::mbar_init(lse_full + 8 * i, 1);
             um::mbar_init(lse_empty + 8 * i, kWarps);
         }
         um::mbar_init(r_full, 1);
-        um::mbar_init(r_empty, 1);
+        um::mbar_init(r_empty, 2);
         um::mbar_init(s_full, 1);
         um::mbar_init(p_ready, kWarps);
-        um::mbar_init(acc_full, 1);
+        um::mbar_init(acc_full, KEYS ? 2 : 1);
         um::mbar_init(acc_free, kWarps);
         um::mbar_init(delta_full, 1);
         um::mbar_init(delta_empty, kWarps);
         um::mbar_init(asked, 1);
-        um::mbar_init(drained, 1);
         um::mbar_init(never, 1);
         um::fence_barrier_init();
         gave_up = 0, claimed = 0, answer = make_uint4(0, 0, 0, 0);
@@ -435,13 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     land(r_full, (r_fills - 1) & 1);
             }
             __syncwarp();
-        } else if (warp == kMultiply) {
+        } else if (warp >= kMultiply) {
+            // Two warps, so that the waits of one, 250 cycles each under load, do not hold the other's products up: the
+            // first makes S and sums P Y, the second makes D and sums dS X.
+            const int which = warp - kMultiply;
             const bool leader = um::elected();
             const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
             const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
             const uint32_t idesc_acc = um::instr_desc(kTile, dn, false, true);
             // rows of a resident tile times those of a streamed one
-            auto pairs = [&](uint32_t d, uint32_t r, uint32_t streamed, uint32_t bar) {
+            auto pairs = [&](uint32_t d, uint32_t r, uint32_t streamed, uint32_t bar, uint32_t empty) {
                 um::fence_after();
                 if (leader) {
                     const uint64_t a = um::operand_desc(r, false, 0), b = um::operand_desc(streamed, false, 0);
@@ -450,10 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         um::mma_own(tmem + d, a + off, b + off, idesc_s, i > 0);
                     }
                     um::mma_commit_own(bar);
+                    um::mma_commit_own(empty);
                 }
             };
             // a sum over a streamed tile's rows, with P or dS, whose quarters are 32 columns apart
-            auto sum = [&](uint32_t d, uint32_t p, uint32_t streamed, bool add, uint32_t bar) {
+            auto sum = [&](uint32_t d, uint32_t p, uint32_t streamed, bool add, uint32_t empty) {
                 um::fence_after();
                 if (leader) {
                     const uint64_t b = um::operand_desc(streamed, true, kHalf);
@@ -461,11 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     for (int i = 0; i < kTile / 16; ++i)
                         um::mma_own_tmem(tmem + d, tmem + p + (i / 2) * 32 + i % 2 * 8, b + i * (2048 >> 4), idesc_acc,
                                          add || i > 0);
-                    um::mma_commit_own(bar);
+                    um::mma_commit_own(empty);
                 }
             };
-            int slot = 0, turn = 0, x_of_s = 0, xs_phase = 0, x_of_sum = 0, y_of_d = 0, yd_phase = 0, y_of_sum = 0;
-            uint32_t r_phase = 0, p_phase = 0, ds_phase = 0, acc_phase = 0;
+            int slot = 0, turn = 0, made = 0, made_phase = 0, summed = 0;  // ring places
+            uint32_t r_phase = 0, ready_phase = 0, acc_phase = 0;
             bool ok = true;
             while (ok) {
                 if (!(ok = wait(item_full + 8 * slot, turn)))
@@ -484,67 +488,75 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                 if (!(ok = wait(r_full, r_phase)))
                     break;
                 r_phase ^= 1;
-                auto make_s = [&] {
-                    if (!(ok = wait(x_full + 8 * x_of_s, xs_phase)))
-                        return;
-                    pairs(kS, resident, xs + x_of_s * kTileBytes, s_full);
-                    if (++x_of_s == kXs)
-                        x_of_s = 0, xs_phase ^= 1;
+                auto free_acc = [&] {  // the item before is out of the accumulators
+                    ok = wait(acc_free, acc_phase ^ 1);
+                    acc_phase ^= 1;
                 };
-                auto make_d = [&](int n) {
-                    if (!(ok = wait(y_full + 8 * y_of_d, yd_phase)))
-                        return;
-                    const int b = KEYS ? 0 : n & 1;
-                    pairs(kD + b * 128, resident + kTileBytes, ys + y_of_d * kTileBytes, d_full + 8 * b);
-                    if (!KEYS && leader)  // its only use
-                        um::mma_commit_own(y_empty + 8 * y_of_d);
-                    if (n == steps - 1 && leader)
+                auto last = [&](int n) {  // use of the resident tile
+                    if (ok && leader && n == steps - 1)
                         um::mma_commit_own(r_empty);
-                    if (++y_of_d == kYs)
-                        y_of_d = 0, yd_phase ^= 1;
                 };
-                make_s();
-                if (ok)
-                    make_d(0);
-                for (int n = 0; ok && n < steps; ++n) {
-                    if (n == 0) {
-                        if (!(ok = wait(acc_free, acc_phase ^ 1)))
+                if (which == 0) {
+                    auto make_s = [&](int n) {
+                        if (!(ok = wait(x_full + 8 * made, made_phase)))
+                            return;
+                        pairs(kS, resident, xs + made * kTileBytes, s_full, x_empty + 8 * made);
+                        last(n);
+                        if (++made == kXs)
+                            made = 0, made_phase ^= 1;
+                    };
+                    make_s(0);
+                    for (int n = 0; ok && n < steps; ++n) {
+                        if (KEYS && n == 0)
+                            free_acc();
+                        if (!ok || !(ok = wait(p_ready, ready_phase)))
                             break;
-                        acc_phase ^= 1;
+                        ready_phase ^= 1;
+                        if (KEYS) {
+                            sum(kAcc0, kS, ys + summed * kTileBytes, n > 0, y_empty + 8 * summed);
+                            if (++summed == kYs)
+                                summed = 0;
+                        }
+                        if (n + 1 < steps)
+                            make_s(n + 1);
                     }
-                    if (!(ok = wait(p_ready, p_phase)))
-                        break;
-                    p_phase ^= 1;
-                    if (KEYS) {
-                        sum(kAcc0, kS, ys + y_of_sum * kTileBytes, n > 0, y_empty + 8 * y_of_sum);
-                        if (++y_of_sum == kYs)
-                            y_of_sum = 0;
-                    }
-                    if (n + 1 < steps) {
-                        make_s();
-                        if (!KEYS && ok)
-                            make_d(n + 1);
-                        if (!ok)
+                    if (KEYS && ok && leader)
+                        um::mma_commit_own(acc_full);
+                } else {
+                    auto make_d = [&](int n) {
+                        if (!(ok = wait(y_full + 8 * made, made_phase)))
+                            return;
+                        const int b = KEYS ? 0 : n & 1;
+                        pairs(kD + b * 128, resident + kTileBytes, ys + made * kTileBytes, d_full + 8 * b, y_empty + 8 * made);
+                        last(n);
+                        if (++made == kYs)
+                            made = 0, made_phase ^= 1;
+                    };
+                    constexpr int kAhead = KEYS ? 1 : 2;  // D of so many steps fit
+                    for (int n = 0; ok && n < min(kAhead, steps); ++n)
+                        make_d(n);
+                    for (int n = 0; ok && n < steps; ++n) {
+                        if (n == 0)
+                            free_acc();
+                        const int b = KEYS ? 0 : n & 1;
+                        if (!ok || !(ok = wait(ds_ready + 8 * b, ready_phase >> b & 1)))
                             break;
+                        ready_phase ^= 1 << b;
+                        sum(kAcc1, kD + b * 128, xs + summed * kTileBytes, n > 0, x_empty + 8 * summed);
+                        if (++summed == kXs)
+                            summed = 0;
+                        if (n + kAhead < steps)
+                            make_d(n + kAhead);
                     }
-                    const int b = KEYS ? 0 : n & 1;
-                    if (!(ok = wait(ds_ready + 8 * b, ds_phase >> b & 1)))
-                        break;
-                    ds_phase ^= 1 << b;
-                    sum(kAcc1, kD + b * 128, xs + x_of_sum * kTileBytes, n > 0, x_empty + 8 * x_of_sum);
-                    if (++x_of_sum == kXs)
-                        x_of_sum = 0;
-                    if (KEYS && n + 1 < steps)
-                        make_d(n + 1);
+                    if (ok && leader)
+                        um::mma_commit_own(acc_full);
                 }
-                if (ok && leader)
-                    um::mma_commit_own(acc_full);
             }
             __syncwarp();
             if (leader) {  // nothing may be under way when the accumulators go
-                um::mma_commit_own(drained);
+                um::mma_commit_own(drained + 8 * which);
                 const uint64_t began = um::now_ns();
-                while (!um::mbar_try(drained, 0) && um::now_ns() - began < f.wait_ns) {
+                while (!um::mbar_try(drained + 8 * which, 0) && um::now_ns() - began < f.wait_ns) {
                 }
             }
             __syncwarp();
