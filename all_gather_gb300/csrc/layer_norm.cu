@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) backward_kernel(Args<T> a, in
         }
 }
 
-// ---------------------------------------------------------------- gradient of tiles of rows
+// ---------------------------------------------------------------- tiles of rows
 
 // Sums over a warp, to all of its lanes.
 __device__ __forceinline__ float warp_sum(float s)
@@ -454,36 +454,50 @@ __device__ __forceinline__ float warp_sum(float s)
     return s;
 }
 
-// `rows` rows of x and dy in shared memory at a time, the next ones on their
+// Pieces of 16 bytes that a row's copy takes at most.
+template <typename T, bool VEC>
+__host__ __device__ constexpr int pieces_of(int cols)
+{
+    return VEC ? cols / 8 * int(sizeof(T) / 2) : (cols * int(sizeof(T)) + 15) / 16 + 1;
+}
+
+// `rows` rows of x (and dy) in shared memory at a time, the next ones on their
 // way as bulk copies.  A thread has the same V units of every row, with their
-// dw and db in registers.  It goes over the tile twice: for the sums, each warp
-// around the mean of its own part of the row, which are then joined around the
-// row's mean, and for dx.  Three meetings of the block for a tile, where a
+// weight, dw and db in registers.  It goes over the tile twice: for the sums,
+// each warp around the mean of its own part of the row, which are then joined
+// around the row's mean, and for y or dx.  Three meetings of the block for a tile, where a
 // group of warps has two for every row.
-template <typename T, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int rows, uint64_t wait_ns)
+template <typename T, bool GRAD, bool VEC, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) tile_kernel(Args<T> a, int rows, uint64_t wait_ns)
 {
     namespace um = tide::umma;
     constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes a unit
+    constexpr int kTensors = GRAD ? 2 : 1;  // x, dy
+    constexpr bool kKeep = V < 4;           // weight and bias in registers; else they are read again for every row
     extern __shared__ uint4 smem[];
     __shared__ uint64_t arrived[2];
     __shared__ volatile int gave_up;
     const int n = blockDim.x, t = threadIdx.x, warp = t / 32, lane = t % 32, units = a.cols / 8;
-    const int row_pieces = units * kPieces, tile_pieces = rows * 2 * row_pieces;
+    const int row_pieces = pieces_of<T, VEC>(a.cols), tile_pieces = rows * kTensors * row_pieces;
     float4 *parts = reinterpret_cast<float4 *>(smem + 2 * tile_pieces), *stats = parts + rows * (n / 32);  // of every row: [warps], and joined
     const int64_t tiles = (a.rows + rows - 1) / rows;
     const float inv = 1.f / float(a.cols);
-    float2 dw[V][4] = {}, db[V][4] = {}, k[V][4];
+    float2 dw[V][4] = {}, db[V][4] = {}, k[V][4], bias[V][4];  // the gradient's sums; weight and bias
+    auto has = [&](int v) { return !VEC || t + v * n < units; };
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (a.w && t + v * n < units)
-            unpack(load_unit<T, true>(a.w, a.cols, v, t, n), k[v]);
+        if (kKeep && has(v)) {
+            if (a.w)
+                unpack(load_unit<T, VEC>(a.w, a.cols, v, t, n), k[v]);
+            if (!GRAD && a.b)
+                unpack(load_unit<T, VEC>(a.b, a.cols, v, t, n), bias[v]);
+        }
     // elements that a warp has of a row: this one, and the one whose number is the lane's
     auto count_of = [&](int w) {
         int c = 0;
-        for (int v = 0; v < V; ++v)
-            c += max(0, min(32, units - (v * n + w * 32)));
-        return float(8 * c);
+        for (int v = 0; v < (VEC ? V : 8 * V); ++v)
+            c += max(0, min(32, (VEC ? units : a.cols) - (v * n + w * 32)));
+        return float(VEC ? 8 * c : c);
     };
     const float part_inv = 1.f / fmaxf(count_of(warp), 1.f), lane_count = lane < n / 32 ? count_of(lane) : 0.f;
     if (t == 0) {
@@ -497,20 +511,36 @@ __global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int ro
     auto load = [&](int64_t tile, int buf) {  // by the first warp
         const int count = int(min(int64_t(rows), a.rows - tile * rows));
         const uint32_t bar = um::smem_addr(&arrived[buf]), to = um::smem_addr(smem + buf * tile_pieces);
+        // a row's aligned pieces of 16 bytes, a row a lane
+        const bool mine = lane < count * kTensors;
+        const int64_t row = tile * rows + lane / kTensors;
+        const T *from = lane % kTensors ? a.dy + row * a.dys : a.x + row * a.xs;
+        const uintptr_t first = reinterpret_cast<uintptr_t>(from) & ~uintptr_t(15);
+        const uintptr_t end = (reinterpret_cast<uintptr_t>(from + a.cols) + 15) & ~uintptr_t(15);
+        const uint32_t bytes = mine ? uint32_t(end - first) : 0, all = __reduce_add_sync(kAll, bytes);
         if (lane == 0)
-            um::mbar_expect(bar, uint32_t(count * 2 * row_pieces * 16));
+            um::mbar_expect(bar, all);
         __syncwarp();
-        for (int i = lane; i < count * 2; i += 32) {
-            const int64_t row = tile * rows + i / 2;
-            um::bulk_load(to + uint32_t(i * row_pieces) * 16, i % 2 ? a.dy + row * a.dys : a.x + row * a.xs,
-                          uint32_t(row_pieces * 16), bar);
-        }
+        if (mine)
+            um::bulk_load(to + uint32_t(lane * row_pieces) * 16, reinterpret_cast<const void *>(first), bytes, bar);
     };
-    auto unit = [&](const uint4 *row, int u, float2 (&f)[4]) {
+    // Unit v of a row at `from` in memory, from its copy.
+    auto unit = [&](const uint4 *row, const T *from, int v, float2 (&f)[4]) {
         Raw<T> raw;
+        if (VEC) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            raw.v[i] = row[u * kPieces + i];
+            for (int i = 0; i < kPieces; ++i)
+                raw.v[i] = row[(t + v * n) * kPieces + i];
+        } else {
+            const T *p = reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) + (reinterpret_cast<uintptr_t>(from) & 15));
+            T e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = column<VEC>(v, i, t, n);
+                e[i] = c < a.cols ? p[c] : T(0.f);
+            }
+            raw = *reinterpret_cast<Raw<T> *>(e);
+        }
         unpack(raw, f);
     };
 
@@ -524,15 +554,16 @@ __global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int ro
         const int count = int(min(int64_t(rows), a.rows - tile * rows));
         const bool here = um::mbar_wait(um::smem_addr(&arrived[buf]), phase, &gave_up, wait_ns);
         const uint4 *base = smem + buf * tile_pieces;
-#pragma unroll 2
+#pragma unroll(V < 4 ? 2 : 1)
         for (int r = 0; r < count; ++r) {
-            const uint4 *x = base + r * 2 * row_pieces, *dy = x + row_pieces;
+            const uint4 *x = base + r * kTensors * row_pieces, *dy = x + row_pieces;
+            const T *xf = a.x + (tile * rows + r) * a.xs, *df = GRAD ? a.dy + (tile * rows + r) * a.dys : nullptr;
             float2 f[V][4], d[4], s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
             float mean = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (t + v * n < units) {
-                    unit(x, t + v * n, f[v]);
+                if (has(v)) {
+                    unit(x, xf, v, f[v]);
                     s0 = add2(s0, add2(add2(f[v][0], f[v][1]), add2(f[v][2], f[v][3])));
                 }
             if (a.center) {
@@ -542,16 +573,22 @@ __global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int ro
             const float2 less = both(-mean);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (t + v * n < units) {
-                    unit(dy, t + v * n, d);
+                if (has(v)) {
+                    if (GRAD) {
+                        unit(dy, df, v, d);
+                        if (!kKeep && a.w)
+                            unpack(load_unit<T, VEC>(a.w, a.cols, v, t, n), k[0]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        f[v][e] = add2(f[v][e], less);
-                        if (a.w)
-                            d[e] = mul2(d[e], k[v][e]);
+                        f[v][e] = centered<VEC>(f[v][e], less, v, e, a.cols, t, n);
                         s0 = fma2(f[v][e], f[v][e], s0);
-                        s1 = add2(s1, d[e]);
-                        s2 = fma2(f[v][e], d[e], s2);
+                        if (GRAD) {
+                            if (a.w)
+                                d[e] = mul2(d[e], k[kKeep ? v : 0][e]);
+                            s1 = add2(s1, d[e]);
+                            s2 = fma2(f[v][e], d[e], s2);
+                        }
                     }
                 }
             const float q[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, 0.f};
@@ -574,26 +611,41 @@ __global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int ro
         }
         __syncthreads();
         for (int r = 0; r < count; ++r) {
-            const uint4 *x = base + r * 2 * row_pieces, *dy = x + row_pieces;
+            const uint4 *x = base + r * kTensors * row_pieces, *dy = x + row_pieces;
+            const T *xf = a.x + (tile * rows + r) * a.xs, *df = GRAD ? a.dy + (tile * rows + r) * a.dys : nullptr;
             const float4 st = stats[r];
             const float2 f = both(st.x), less = both(st.y), level = both(st.z), along = both(st.w);
             T *out = a.out + (tile * rows + r) * a.outs;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int u = t + v * n;
-                if (u >= units)
+                if (!has(v))
                     continue;
                 float2 c[4], d[4], y[4];
-                unit(x, u, c);
-                unit(dy, u, d);
+                unit(x, xf, v, c);
+                if (GRAD)
+                    unit(dy, df, v, d);
+                if (!kKeep) {
+                    if (a.w)
+                        unpack(load_unit<T, VEC>(a.w, a.cols, v, t, n), k[0]);
+                    if (!GRAD && a.b)
+                        unpack(load_unit<T, VEC>(a.b, a.cols, v, t, n), bias[0]);
+                }
+                const int kv = kKeep ? v : 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 norm = mul2(add2(c[e], less), f), gi = a.w ? mul2(d[e], k[v][e]) : d[e];
-                    y[e] = mul2(f, add2(fma2(norm, along, gi), level));
-                    dw[v][e] = fma2(d[e], norm, dw[v][e]);
-                    db[v][e] = add2(db[v][e], d[e]);
+                    const float2 norm = mul2(add2(c[e], less), f);
+                    if (GRAD) {
+                        const float2 gi = a.w ? mul2(d[e], k[kv][e]) : d[e];
+                        y[e] = mul2(f, add2(fma2(norm, along, gi), level));
+                        dw[v][e] = fma2(d[e], norm, dw[v][e]);
+                        db[v][e] = add2(db[v][e], d[e]);
+                    } else if (a.w) {
+                        y[e] = a.b ? fma2(norm, k[kv][e], bias[kv][e]) : mul2(norm, k[kv][e]);
+                    } else {
+                        y[e] = a.b ? add2(norm, bias[kv][e]) : norm;
+                    }
                 }
-                store_unit<T, true>(out, a.cols, v, t, n, y);
+                store_unit<T, VEC>(out, a.cols, v, t, n, y);
             }
         }
         if (buf ^= 1, buf == 0)
@@ -608,16 +660,16 @@ __global__ void __launch_bounds__(THREADS, 1) tile_grad_kernel(Args<T> a, int ro
             for (int e = 0; e < 4; ++e)
                 dw[v][e] = db[v][e] = both(__int_as_float(0x7fffffff));
     }
-    if (!a.partial)
+    if (!GRAD || !a.partial)
         return;
     float *p = a.partial + int64_t(blockIdx.x) * 2 * a.cols;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        if (t + v * n < units) {
+        if (has(v)) {
             if (a.w)
-                store_unit<float, true>(p, a.cols, v, t, n, dw[v]);
+                store_unit<float, VEC>(p, a.cols, v, t, n, dw[v]);
             if (a.b)
-                store_unit<float, true>(p + a.cols, a.cols, v, t, n, db[v]);
+                store_unit<float, VEC>(p + a.cols, a.cols, v, t, n, db[v]);
         }
 }
 
@@ -761,23 +813,30 @@ constexpr int kTileSmem = 224 * 1024;
 
 int64_t sms() { return std::max(tide::op_sm_count(), 1); }
 
-// Tiles of rows for the gradient of rows on 16-byte boundaries, from 1,024 columns on (32 warps' worth of units; below, a
-// group of warps is as fast), as long as the threads have
-// registers for the sums and two tiles fit into shared memory.
-bool tile_shape(const tide_norm_t *n, Shape &s)
+// Tiles of rows, from 512 columns on (four of them fit in a warp's two sweeps; below, a group of warps is
+// as fast), as long as the threads have registers for the sums and two tiles fit into shared memory.  Rows on other than
+// 16-byte boundaries are copied as the aligned pieces that hold them.  Narrow rows have several blocks an SM.
+bool tile_shape(const tide_norm_t *n, bool grad, Shape &s)
 {
-    const int64_t bytes = 2 * n->cols * (n->dtype == TIDE_DTYPE_F32 ? 4 : 2), units = n->cols / 8;
-    const int64_t rows = std::min<int64_t>(8, (kTileSmem - 8 * 33 * 16) / 2 / bytes);
-    if (n->cols < 1024 || n->cols > 16384 || n->cols % 8 || rows < 1)
+    const bool wide_type = n->dtype == TIDE_DTYPE_F32;
+    if (n->cols < 64 || n->cols > (grad && s.vec ? 16384 : 8192) || (!grad && s.vec && !wide_type))
         return false;
+    const int cols = int(n->cols), units = (cols + 7) / 8;
+    const int pieces = s.vec ? wide_type ? pieces_of<float, true>(cols) : pieces_of<bf16, true>(cols)
+                       : wide_type ? pieces_of<float, false>(cols) : pieces_of<bf16, false>(cols);
+    const int bytes = (grad ? 2 : 1) * 16 * pieces, most = grad ? 8 : 16;  // a row's copies: a lane each
     s.kind = kTiles;
     s.units = units <= 640 ? 1 : units <= 1024 ? 2 : 4;
-    s.warps = int((units + 32 * s.units - 1) / (32 * s.units));
+    s.warps = (units + 32 * s.units - 1) / (32 * s.units);
     s.groups = 1;
-    s.rows = int(std::min(rows, std::max<int64_t>(1, n->rows / sms())));  // few rows: on all SMs
-    s.smem = int(2 * s.rows * bytes + s.rows * (s.warps + 1) * 16);
-    s.blocks = int(std::max<int64_t>(1, std::min((n->rows + s.rows - 1) / s.rows, sms())));
-    return s.smem <= kTileSmem;
+    const int per_sm = std::max(1, 20 / s.warps), budget = kTileSmem / per_sm - 1024;
+    s.rows = std::min(most, (budget - most * (s.warps + 1) * 16) / 2 / bytes);
+    if (s.rows < 1)
+        return false;
+    s.rows = int(std::min<int64_t>(s.rows, std::max<int64_t>(1, n->rows / (sms() * per_sm))));  // few rows: on all SMs
+    s.smem = 2 * s.rows * bytes + s.rows * (s.warps + 1) * 16;
+    s.blocks = int(std::max<int64_t>(1, std::min((n->rows + s.rows - 1) / s.rows, sms() * per_sm)));
+    return true;
 }
 
 // A thread has 64 bytes of a row, or 32 of one of x and dy each.
@@ -785,7 +844,7 @@ Shape shape_of(const tide_norm_t *n, bool grad, bool vec)
 {
     Shape s = {};
     s.vec = vec;
-    if (grad && vec && tile_shape(n, s))
+    if (tile_shape(n, grad, s))
         return s;
     const int units = (n->dtype == TIDE_DTYPE_F32 ? 2 : 4) / (grad ? 2 : 1);
     s.warps = int((n->cols + 256 * units - 1) / (256 * units));
@@ -860,10 +919,14 @@ tide_status_t launch(const Args<T> &a, const Shape &s, const char *what, cudaStr
         wide_kernel<T, GRAD><<<unsigned(s.blocks), 1024, 0, st>>>(a);
         return tide::op_launched(what);
     }
+    if (s.kind == kTiles && s.vec)
+        return s.units == 1   ? launch_tiles<tile_kernel<T, GRAD, true, 1, 640>>(a, s, what, st)
+               : s.units == 2 ? launch_tiles<tile_kernel<T, GRAD, true, 2, 512>>(a, s, what, st)
+                              : launch_tiles<tile_kernel<T, GRAD, true, 4, 512>>(a, s, what, st);
     if (s.kind == kTiles)
-        return s.units == 1   ? launch_tiles<tile_grad_kernel<T, 1, 640>>(a, s, what, st)
-               : s.units == 2 ? launch_tiles<tile_grad_kernel<T, 2, 512>>(a, s, what, st)
-                              : launch_tiles<tile_grad_kernel<T, 4, 512>>(a, s, what, st);
+        return s.units == 1   ? launch_tiles<tile_kernel<T, GRAD, false, 1, 640>>(a, s, what, st)
+               : s.units == 2 ? launch_tiles<tile_kernel<T, GRAD, false, 2, 512>>(a, s, what, st)
+                              : launch_tiles<tile_kernel<T, GRAD, false, 4, 512>>(a, s, what, st);
     return s.vec ? launch_shape<T, GRAD, true>(a, s, what, st) : launch_shape<T, GRAD, false>(a, s, what, st);
 }
 

@@ -563,8 +563,9 @@ typedef struct {
  *   lse_r = log sum_c exp(s_rc);  o_r = sum_c exp(s_rc - lse_r) v_c.
  * q, o: device [T, Hq, D]; k, v: [T, Hk, D]; lse: device fp32 [Hq, T].  bf16
  * only; rows on 16-byte boundaries; strides of dimensions longer than 1 are
- * positive multiples of 8.  exp(s - a), a the largest score or one less than
- * 8 log2 below it, is rounded to bf16 for its product with v; sums are fp32.
+ * positive multiples of 8 (other rows are refused: TIDE_ERR_ALIGNMENT).
+ * exp(s - a), with a at most a factor 2^8 below the row's largest exp(s) so
+ * far, is rounded to bf16 for its product with v; sums are fp32.
  * A token of no sequence (before offsets[0], behind the last one, or past T)
  * sees nothing: o = 0, lse = -inf.  What a token does not see does not reach
  * its row, whether finite or not.  Offsets are not checked on the host;
@@ -623,11 +624,12 @@ TIDE_API tide_status_t tide_layer_norm_grad(const tide_norm_t *norm, const void 
 TIDE_API int64_t tide_layer_norm_grad_workspace(const tide_norm_t *norm);
 
 /*
- * Read and clear the operators' status word of the current device
+ * Read and clear the operators' status words of the current device
  * (synchronises `stream`): TIDE_ERR_TIMEOUT if a bounded device-side wait of
- * tide_ce_loss or tide_ce_grad expired there since the last such read, else
- * TIDE_OK.  What the wait kept from being computed is NaN in that call's
- * outputs.  Not to be called during a capture.
+ * tide_ce_loss, tide_ce_grad, tide_attention, tide_attention_grad or
+ * tide_layer_norm_grad expired there since the last such read, else TIDE_OK.
+ * What the wait kept from being computed is NaN in that call's outputs.  Not
+ * to be called during a capture.
  */
 TIDE_API tide_status_t tide_ops_device_status(void *stream);
 
