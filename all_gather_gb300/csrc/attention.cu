@@ -106,16 +106,17 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
     constexpr int kHalves = W / 64, kTileBytes = kHalves * kHalf, kStages = kRingBytes / kTileBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t q_at = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024, ring = q_at + 2 * kTileBytes;
-    __shared__ uint64_t bars[2 * kStages + 20];
+    __shared__ uint64_t bars[2 * kStages + 26];
     __shared__ alignas(16) uint4 answer;
     __shared__ Item items[2];
     __shared__ int claims[kClaims], claimed, done[8];  // done: items of each of the rows' warps
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int gave_up;
     const uint32_t full = um::smem_addr(bars), empty = full + 8 * kStages, rest = empty + 8 * kStages;
-    const uint32_t q_full = rest, q_empty = rest + 16, s_full = rest + 32, p_ready = rest + 48, pv_done = rest + 64,
-                   o_free = rest + 80, item_full = rest + 96, item_empty = rest + 112, asked = rest + 128,
-                   drained = rest + 136, never = rest + 152;
+    // s_full, p_ready and pv_done: of row tile t and half h of a key tile, 16 t + 8 h further on; others: 8 t
+    const uint32_t q_full = rest, q_empty = rest + 16, s_full = rest + 32, p_ready = rest + 64, pv_done = rest + 96,
+                   o_free = rest + 128, item_full = rest + 144, item_empty = rest + 160, asked = rest + 176,
+                   drained = rest + 184, never = rest + 200;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Problem &pr = f.pr;
     const int group = pr.Hq / pr.Hk;
@@ -129,9 +130,11 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             um::mbar_init(drained + 8 * i, 1);
             um::mbar_init(q_full + 8 * i, 1);
             um::mbar_init(q_empty + 8 * i, 1);
-            um::mbar_init(s_full + 8 * i, 1);
-            um::mbar_init(p_ready + 8 * i, 4);
-            um::mbar_init(pv_done + 8 * i, 1);
+            for (int h = 0; h < 2; ++h) {
+                um::mbar_init(s_full + 16 * i + 8 * h, 1);
+                um::mbar_init(p_ready + 16 * i + 8 * h, 4);
+                um::mbar_init(pv_done + 16 * i + 8 * h, 1);
+            }
             um::mbar_init(o_free + 8 * i, 4);
             um::mbar_init(item_full + 8 * i, 1);
             um::mbar_init(item_empty + 8 * i, 10);
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             // one tile's must not hold the other's products up.
             const int t = warp - 9;
             const bool leader = um::elected();
-            const uint32_t idesc_s = um::instr_desc(kTile, kTile, false, false);
+            const uint32_t idesc_s = um::instr_desc(kTile, kTile / 2, false, false);
             const int dn = (pr.D + 15) / 16 * 16, ksteps = dn / 16;
             const uint32_t idesc_o = um::instr_desc(kTile, dn, false, true);
             const uint32_t s_at = tmem + t * kTile, o_at = s_at + 2 * kTile;
@@ -280,6 +283,18 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 ok = wait(full + 8 * at, parity);
                 if (ok && leader)
                     um::mbar_arrive(empty + 8 * at);
+            };
+            // Scores of half h of the key tile in a stage, into the half of S that holds no P any more.
+            auto scores = [&](int at, int h) {
+                um::fence_after();
+                if (leader) {
+                    const uint64_t b = um::operand_desc(ring + at * kTileBytes + h * (kHalf / 2), false, 0);
+                    for (int i = 0; i < ksteps; ++i) {
+                        const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
+                        um::mma_own(s_at + h * 64, qd + off, b + off, idesc_s, i > 0);
+                    }
+                    um::mma_commit_own(s_full + 16 * t + 8 * h);
+                }
             };
             while (ok) {
                 if (!(ok = wait(item_full + 8 * slot, turn)))
@@ -296,65 +311,65 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 const bool both = mine.a < mine.b && other.a < other.b;
                 const Tiles all = both ? Tiles{min(mine.a, other.a), max(mine.b, other.b)} : mine.a < mine.b ? mine : other;
                 for (int j = all.a - 1; ok && j < all.b; ++j) {  // P v of key tile j, scores of key tile j + 1
-                    if (j >= all.a) {
-                        if (j >= mine.a && j < mine.b) {
-                            if (!(ok = wait(full + 8 * stage, phase)))
+                    const bool sums = j >= mine.a && j < mine.b, makes = j + 1 >= mine.a && j + 1 < mine.b;
+                    const int v_at = stage, v_phase = phase;
+                    if (j >= all.a && ++stage == kStages)
+                        stage = 0, phase ^= 1;
+                    const int k_at = stage, k_phase = phase;
+                    if (j + 1 < all.b && ++stage == kStages)
+                        stage = 0, phase ^= 1;
+                    if (makes) {
+                        if (!(ok = wait(full + 8 * k_at, k_phase)))
+                            break;
+                        if (j + 1 == mine.a) {
+                            if (!(ok = wait(q_full + 8 * t, q_phase)))
                                 break;
-                            if (j == mine.a) {
-                                if (!(ok = wait(o_free + 8 * t, o_phase ^ 1)))
-                                    break;
-                                o_phase ^= 1;
-                            }
-                            if (!(ok = wait(p_ready + 8 * t, p_phase)))
+                            q_phase ^= 1;
+                        }
+                    }
+                    if (sums) {
+                        if (!(ok = wait(full + 8 * v_at, v_phase)))
+                            break;
+                        if (j == mine.a) {
+                            if (!(ok = wait(o_free + 8 * t, o_phase ^ 1)))
                                 break;
-                            p_phase ^= 1;
-                            um::fence_after();
-                            if (leader) {
-                                const uint64_t b = um::operand_desc(ring + stage * kTileBytes, true, kHalf);
+                            o_phase ^= 1;
+                        }
+                    }
 #pragma unroll
-                                for (int i = 0; i < kTile / 16; ++i)
-                                    um::mma_own_tmem(o_at, s_at + i * 8, b + i * (2048 >> 4), idesc_o, j > mine.a || i > 0);
-                                um::mma_commit_own(pv_done + 8 * t);
-                                um::mma_commit_own(empty + 8 * stage);
-                            }
-                        } else {
-                            pass(stage, phase);
-                            if (!ok)
+                    for (int h = 0; h < 2; ++h) {
+                        if (sums) {
+                            if (!(ok = wait(p_ready + 16 * t + 8 * h, p_phase)))
                                 break;
-                        }
-                        if (++stage == kStages)
-                            stage = 0, phase ^= 1;
-                    }
-                    if (j + 1 < all.b) {
-                        if (j + 1 >= mine.a && j + 1 < mine.b) {
-                            if (!(ok = wait(full + 8 * stage, phase)))
-                                break;
-                            if (j + 1 == mine.a) {
-                                if (!(ok = wait(q_full + 8 * t, q_phase)))
-                                    break;
-                                q_phase ^= 1;
-                            }
                             um::fence_after();
                             if (leader) {
-                                const uint64_t b = um::operand_desc(ring + stage * kTileBytes, false, 0);
-                                for (int i = 0; i < ksteps; ++i) {
-                                    const uint32_t off = ((i % 4) * 32 + (i / 4) * kHalf) >> 4;
-                                    um::mma_own(s_at, qd + off, b + off, idesc_s, i > 0);
-                                }
-                                um::mma_commit_own(s_full + 8 * t);
-                                um::mma_commit_own(empty + 8 * stage);
-                                if (j + 2 == mine.b)
-                                    um::mma_commit_own(q_empty + 8 * t);
+                                const uint64_t b = um::operand_desc(ring + v_at * kTileBytes, true, kHalf);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    um::mma_own_tmem(o_at, s_at + h * 64 + i * 8, b + (4 * h + i) * (2048 >> 4), idesc_o,
+                                                     j > mine.a || h > 0 || i > 0);
+                                um::mma_commit_own(pv_done + 16 * t + 8 * h);
                             }
-                        } else {
-                            pass(stage, phase);
-                            if (!ok)
-                                break;
                         }
-                        // the next v is behind this k
-                        if (++stage == kStages)
-                            stage = 0, phase ^= 1;
+                        if (makes)
+                            scores(k_at, h);
                     }
+                    if (!ok)
+                        break;
+                    if (sums)
+                        p_phase ^= 1;
+                    if (leader) {
+                        if (sums)
+                            um::mma_commit_own(empty + 8 * v_at);
+                        if (makes)
+                            um::mma_commit_own(empty + 8 * k_at);
+                        if (j + 2 == mine.b)
+                            um::mma_commit_own(q_empty + 8 * t);
+                    }
+                    if (j >= all.a && !sums)
+                        pass(v_at, v_phase);
+                    if (ok && j + 1 < all.b && !makes)
+                        pass(k_at, k_phase);
                 }
             }
             __syncwarp();
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
         const uint32_t s_at = tmem + lanes + t * kTile, o_at = s_at + 2 * kTile;
         const float c = pr.scale * kLog2e;
         int slot = 0, turn = 0;
-        uint32_t s_phase = 0, pv_phase = 0;
+        uint32_t s_phase = 0;  // of the current key tile's barriers
         bool ok = true;
         for (;;) {
             if (!wait(item_full + 8 * slot, turn))
@@ -393,20 +408,21 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             const Span see = pr.keys_of(r);
             __syncwarp();  // the search for the sequence took lanes apart
             float top = -INFINITY, sum = 0.f;
-            for (int j = keys.a; j < keys.b; ++j) {
-                if (!(ok = wait(s_full + 8 * t, s_phase)))
+            for (int n = 2 * keys.a; n < 2 * keys.b; ++n) {  // halves of key tiles
+                const int h = n & 1;
+                const uint32_t half_at = s_at + h * 64;
+                if (!(ok = wait(s_full + 16 * t + 8 * h, s_phase)))
                     break;
-                s_phase ^= 1;
+                s_phase ^= h;
                 um::fence_after();
-                uint32_t v[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    um::tmem_load32(s_at + 32 * i, v[i]);
+                uint32_t v[2][32];
+                um::tmem_load32(half_at, v[0]);
+                um::tmem_load32(half_at + 32, v[1]);
                 um::tmem_wait_load();
-                const int a = see.a - j * kTile, b = see.b - j * kTile;
-                if (__any_sync(kAll, a > 0 || b < kTile)) {
+                const int a = see.a - n * 64, b = see.b - n * 64;
+                if (__any_sync(kAll, a > 0 || b < 64)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             if (32 * i + x < a || 32 * i + x >= b)
@@ -415,20 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 float m[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    m[i] = fmaxf(__uint_as_float(v[i][0]), __uint_as_float(v[i][1]));
+                    const int y = i % 2 * 16;
+                    m[i] = fmaxf(__uint_as_float(v[i / 2][y]), __uint_as_float(v[i / 2][y + 1]));
 #pragma unroll
-                    for (int x = 2; x < 32; x += 2)
-                        m[i] = um::max3(m[i], __uint_as_float(v[i][x]), __uint_as_float(v[i][x + 1]));
+                    for (int x = 2; x < 16; x += 2)
+                        m[i] = um::max3(m[i], __uint_as_float(v[i / 2][y + x]), __uint_as_float(v[i / 2][y + x + 1]));
                 }
                 const float now = um::max3(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]), top);
-                if (j == keys.a) {
+                if (n == 2 * keys.a) {
                     top = now;
                 } else if (__any_sync(kAll, (now - top) * c > kLazy || (top == -INFINITY && now > top))) {
                     // O so far goes over to the new maximum
                     const float by = now == top ? 1.f : exp2_fast((top - now) * c);
                     top = now;
                     sum *= by;
-                    if (!(ok = wait(pv_done + 8 * t, pv_phase ^ 1)))
+                    if (!(ok = wait(pv_done + 16 * t + 8 * (1 - h), s_phase ^ 1)))
                         break;
                     um::fence_after();
 #pragma unroll
@@ -446,27 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
                 const float at = isinf(top) ? 0.f : top * c;
                 const float2 cc = make_float2(c, c), aa = make_float2(-at, -at);
                 float2 part[2] = {};
+                uint32_t p[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const int i = 2 * h + x / 16, y = x % 16 * 2;
-                        float2 e = um::fma2(make_float2(__uint_as_float(v[i][y]), __uint_as_float(v[i][y + 1])), cc, aa);
-                        e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
-                        part[x % 2] = um::add2(part[x % 2], e);
-                        p[x] = tide::pack_bf16(e.x, e.y);
-                    }
-                    um::tmem_store32(s_at + 32 * h, p);
+                for (int x = 0; x < 32; ++x) {
+                    const int i = x / 16, y = x % 16 * 2;
+                    float2 e = um::fma2(make_float2(__uint_as_float(v[i][y]), __uint_as_float(v[i][y + 1])), cc, aa);
+                    e.x = exp2_fast(e.x), e.y = exp2_fast(e.y);
+                    part[x % 2] = um::add2(part[x % 2], e);
+                    p[x] = tide::pack_bf16(e.x, e.y);
                 }
+                um::tmem_store32(half_at, p);
                 um::tmem_wait_store();
                 um::fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    um::mbar_arrive(p_ready + 8 * t);
+                    um::mbar_arrive(p_ready + 16 * t + 8 * h);
                 part[0] = um::add2(part[0], part[1]);
                 sum += part[0].x + part[0].y;
-                pv_phase ^= 1;
             }
             if (!ok)
                 break;
@@ -475,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) forward_kernel(const __grid_const
             bf16 *out = f.o.row(min(r, pr.T - 1), head);
             bool odd = false;  // not finite
             if (keys.a < keys.b) {
-                if (!(ok = wait(pv_done + 8 * t, pv_phase ^ 1)))
+                if (!(ok = wait(pv_done + 16 * t + 8, s_phase ^ 1)))
                     break;
                 um::fence_after();
                 uint32_t o[W / 32][32];
