@@ -6,15 +6,26 @@
 //   g = dy w:  dx = r (g - mean(g) - n mean(g n)),  dw = sum over rows of dy n,
 //   db = sum over rows of dy  (mean(g): only with the centre)
 //
-// A group of warps has a row in registers, so x (and dy) are read once; the
-// second moment is taken around the mean that is already known, which keeps
-// its digits where the mean is large.  The gradient takes its three sums in
-// one go after the mean: sum(g n) = r sum(g (x - m)).  Statistics are computed
-// again there rather than kept: x has to be read anyway.
+// x (and dy) are read once.  Statistics are computed again in the gradient
+// rather than kept: x has to be read anyway, and sum(g n) = r sum(g (x - m)).
 //
-// A thread keeps its columns for all rows of its group, so it adds up their dw
-// and db in registers; the groups' shares go to the workspace and a second
-// kernel adds them in a fixed order.
+// Two ways of sharing rows out.  A group of warps has a row in registers, with
+// the next ones on their way (cp.async); the second moment is taken around the
+// mean that is already known, which keeps its digits where the mean is large.
+// Or a block has a tile of rows in shared memory.  bf16 rows on 16-byte
+// boundaries take the first way forward (32,768 x 4,096: 96 us, 5.6 TB/s; tiles
+// 131 us); fp32, other boundaries and the gradient the second (16,384 x 4,096
+// fp32: 110 us, groups 142; 30,000 x 2,047 bf16: 112 and 290; gradient of 32,768 x
+// 5,120 bf16: 212 us, 4.7 TB/s, groups 357).  Rows that fit neither way are read
+// again for each sum.
+//
+// A thread keeps its columns for all rows, so it adds up their dw and db in
+// registers; the blocks' shares go to the workspace and a second kernel adds
+// them in a fixed order.
+//
+// Bound by HBM and by instruction issue, half of whose slots are busy; an
+// element of the gradient takes a dozen instructions, so pairs of fp32 go through
+// one (f32x2).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -813,9 +824,10 @@ constexpr int kTileSmem = 224 * 1024;
 
 int64_t sms() { return std::max(tide::op_sm_count(), 1); }
 
-// Tiles of rows, from 512 columns on (four of them fit in a warp's two sweeps; below, a group of warps is
-// as fast), as long as the threads have registers for the sums and two tiles fit into shared memory.  Rows on other than
-// 16-byte boundaries are copied as the aligned pieces that hold them.  Narrow rows have several blocks an SM.
+// Tiles of rows: for the gradient, for fp32 and for rows on other than 16-byte boundaries, which are copied as the aligned
+// pieces that hold them; from 64 columns on, as long as the threads have registers for the sums and two tiles fit into shared
+// memory.  The gradient's limit for aligned rows is higher: 8,192 x 16,384 bf16 takes 290 us, and 550 with groups; 8,000 x
+// 16,383 takes 963, and 795 with groups.  Narrow rows have several blocks an SM.
 bool tile_shape(const tide_norm_t *n, bool grad, Shape &s)
 {
     const bool wide_type = n->dtype == TIDE_DTYPE_F32;
