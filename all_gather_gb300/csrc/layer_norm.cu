@@ -931,14 +931,16 @@ tide_status_t launch(const Args<T> &a, const Shape &s, const char *what, cudaStr
         wide_kernel<T, GRAD><<<unsigned(s.blocks), 1024, 0, st>>>(a);
         return tide::op_launched(what);
     }
-    if (s.kind == kTiles && s.vec)
-        return s.units == 1   ? launch_tiles<tile_kernel<T, GRAD, true, 1, 640>>(a, s, what, st)
-               : s.units == 2 ? launch_tiles<tile_kernel<T, GRAD, true, 2, 512>>(a, s, what, st)
-                              : launch_tiles<tile_kernel<T, GRAD, true, 4, 512>>(a, s, what, st);
-    if (s.kind == kTiles)
-        return s.units == 1   ? launch_tiles<tile_kernel<T, GRAD, false, 1, 640>>(a, s, what, st)
-               : s.units == 2 ? launch_tiles<tile_kernel<T, GRAD, false, 2, 512>>(a, s, what, st)
-                              : launch_tiles<tile_kernel<T, GRAD, false, 4, 512>>(a, s, what, st);
+    if (s.kind == kTiles && !s.vec)
+        return s.units == 1 ? launch_tiles<tile_kernel<T, GRAD, false, 1, 640>>(a, s, what, st)
+                            : launch_tiles<tile_kernel<T, GRAD, false, 2, 512>>(a, s, what, st);
+    if constexpr (GRAD || sizeof(T) == 4)
+        if (s.kind == kTiles && s.units < 4)
+            return s.units == 1 ? launch_tiles<tile_kernel<T, GRAD, true, 1, 640>>(a, s, what, st)
+                                : launch_tiles<tile_kernel<T, GRAD, true, 2, 512>>(a, s, what, st);
+    if constexpr (GRAD)
+        if (s.kind == kTiles)
+            return launch_tiles<tile_kernel<T, GRAD, true, 4, 512>>(a, s, what, st);
     return s.vec ? launch_shape<T, GRAD, true>(a, s, what, st) : launch_shape<T, GRAD, false>(a, s, what, st);
 }
 
