@@ -88,8 +88,8 @@ __device__ __forceinline__ Span span_of(const Problem &pr, int t)
     return KEYS ? pr.rows_of(t) : pr.keys_of(t);
 }
 
-// How many blocks share a key tile's query heads: as many as it takes for none to have more than half of an SM's share of
-// all the steps.  By one block; sequences are looked at by a tile's ends, which decides about time only.
+// How many blocks share a key tile's query heads: as many as it takes for none to have more than a third of an SM's share
+// of all the steps.  By one block; sequences are looked at by a tile's ends, which decides about time only.
 __device__ void share_out(const Problem &pr, int most, int sms, int *parts_of)
 {
     __shared__ float shared[8];
@@ -115,7 +115,7 @@ __device__ void share_out(const Problem &pr, int most, int sms, int *parts_of)
         __syncthreads();
         for (int w = 0; w < 8; ++w)
             steps += shared[w];
-        steps = fmaxf(2.f, steps * float(pr.Hk) / float(2 * sms));
+        steps = fmaxf(2.f, steps * float(pr.Hk) / float(3 * sms));
     }
 }
 
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     const uint32_t resident = (um::smem_addr(smem_raw) + 1023) / 1024 * 1024;
     const uint32_t xs = resident + 2 * kTileBytes, ys = xs + kXs * kTileBytes;
-    __shared__ uint64_t bars[2 * kXs + 2 * kYs + 24];
+    __shared__ uint64_t bars[2 * kXs + 2 * kYs + 21];
     __shared__ alignas(16) uint4 answer;
     __shared__ alignas(16) float lse_of[2][kTile], delta_of[kTile];  // keys: of a step's rows, -lse in log2, and -delta
     __shared__ Item items[2];
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                    y_empty = y_full + 8 * kYs, rest = y_empty + 8 * kYs;
     const uint32_t r_full = rest, r_empty = rest + 8, s_full = rest + 16, p_ready = rest + 24, d_full = rest + 32,
                    ds_ready = rest + 48, acc_full = rest + 64, acc_free = rest + 72, item_full = rest + 80,
-                   item_empty = rest + 96, lse_full = rest + 112, lse_empty = rest + 128, delta_full = rest + 144,
-                   delta_empty = rest + 152, asked = rest + 160, drained = rest + 168, never = rest + 184;
+                   item_empty = rest + 96, lse_empty = rest + 112, delta_empty = rest + 128, asked = rest + 136,
+                   drained = rest + 144, never = rest + 160;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const Problem &pr = f.pr;
     const int group = pr.Hq / pr.Hk;
@@ -278,21 +278,19 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         for (int i = 0; i < kYs; ++i)
             um::mbar_init(y_full + 8 * i, 1), um::mbar_init(y_empty + 8 * i, KEYS ? 2 : 1);
         for (int i = 0; i < 2; ++i) {
-            um::mbar_init(d_full + 8 * i, 1);
+            um::mbar_init(d_full + 8 * i, KEYS ? 2 : 1);  // D, and the delta that goes with it
             um::mbar_init(ds_ready + 8 * i, kWarps);  // rows: a warp may be a step ahead of another one
             um::mbar_init(item_full + 8 * i, 1);
             um::mbar_init(item_empty + 8 * i, kWarps + (KEYS ? 3 : 2));
             um::mbar_init(drained + 8 * i, 1);
-            um::mbar_init(lse_full + 8 * i, 1);
             um::mbar_init(lse_empty + 8 * i, kWarps);
         }
         um::mbar_init(r_full, 1);
         um::mbar_init(r_empty, 2);
-        um::mbar_init(s_full, 1);
+        um::mbar_init(s_full, KEYS ? 2 : 1);  // S, and the lse that goes with it
         um::mbar_init(p_ready, kWarps);
         um::mbar_init(acc_full, KEYS ? 2 : 1);
         um::mbar_init(acc_free, kWarps);
-        um::mbar_init(delta_full, 1);
         um::mbar_init(delta_empty, kWarps);
         um::mbar_init(asked, 1);
         um::mbar_init(never, 1);
@@ -573,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
             __syncwarp();
         } else if (KEYS && warp == kStats) {
             int slot = 0, turn = 0, at = 0;
-            uint32_t phase = 0, delta_phase = 0;
+            uint32_t phase = 0, step = 0;
             bool ok = true;
             while (ok) {
                 if (!(ok = wait(item_full + 8 * slot, turn)))
@@ -602,17 +600,20 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         for (int i = 0; i < 4; ++i)
                             lse_of[at][i * 32 + lane] = -l[i] * kLog2e;
                         __syncwarp();
-                        if (lane == 0)
-                            um::mbar_arrive(lse_full + 8 * at);
-                        if (!(ok = wait(delta_empty, delta_phase ^ 1)))
+                        // the barrier's phase before has to be over: it has two arrivals, of which this must be one
+                        if (step > 0 && !(ok = wait(s_full, step - 1 & 1)))
                             break;
-                        delta_phase ^= 1;
+                        if (lane == 0)
+                            um::mbar_arrive(s_full);
+                        if (!(ok = wait(delta_empty, step & 1 ^ 1)))  // and then D's phase before is over too
+                            break;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             delta_of[i * 32 + lane] = -d[i];
                         __syncwarp();
                         if (lane == 0)
-                            um::mbar_arrive(delta_full);
+                            um::mbar_arrive(d_full);
+                        ++step;
                         if (++at == 2)
                             at = 0, phase ^= 1;
                     }
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
         const float c = pr.scale * kLog2e;
         int slot = 0, turn = 0, at = 0;
-        uint32_t s_phase = 0, d_phase = 0, lse_phase = 0, delta_phase = 0, acc_phase = 0;
+        uint32_t s_phase = 0, d_phase = 0, acc_phase = 0;
         bool ok = true;
         for (;;) {
             if (!wait(item_full + 8 * slot, turn))
@@ -666,8 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0)
                         um::mbar_arrive(p_ready);
-                } else if (!(ok = wait(lse_full + 8 * at, lse_phase))) {
-                    break;
                 }
                 float2 p[kWide / 2];
                 const float2 cc = make_float2(c, c);
@@ -692,11 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_kernel(const __grid_cons
                         um::mbar_arrive(p_ready);
                         um::mbar_arrive(lse_empty + 8 * at);
                     }
-                    if (++at == 2)
-                        at = 0, lse_phase ^= 1;
-                    if (!(ok = wait(delta_full, delta_phase)))
-                        break;
-                    delta_phase ^= 1;
+                    at ^= 1;
                 }
                 const int buf = KEYS ? 0 : n & 1;
                 if (!(ok = wait(d_full + 8 * buf, d_phase >> buf & 1)))
@@ -795,7 +790,7 @@ __global__ void __launch_bounds__(256) join_kernel(Problem pr, const int *parts_
     const int tile = blockIdx.x / pr.Hk, head = blockIdx.x % pr.Hk, parts = parts_of[tile], units = pr.D / 8;
     if (parts < 2)
         return;
-    for (int i = threadIdx.x; i < 2 * kTile * units; i += 256) {
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < 2 * kTile * units; i += gridDim.y * 256) {
         const int which = i / (kTile * units), t = tile * kTile + i / units % kTile, d = i % units * 8;
         if (t >= pr.T)
             continue;
@@ -932,7 +927,7 @@ tide_status_t tide_attention_grad(const tide_attention_t *at, const tide_heads_t
     if (s)
         return s;
     if (l.parts > 1) {
-        join_kernel<<<unsigned(tiles * p.Hk), 256, 0, st>>>(p, parts_of, partial, f.out0, f.out1);
+        join_kernel<<<dim3(unsigned(tiles * p.Hk), 8), 256, 0, st>>>(p, parts_of, partial, f.out0, f.out1);
         s = tide::op_launched("attention_grad: join");
         if (s)
             return s;
